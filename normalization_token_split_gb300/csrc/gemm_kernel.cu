@@ -1,0 +1,705 @@
+// gemm_kernel.cu -- matrix product of E4M3 operands with one fp32 scale for
+// each block of 128 values along K, on the tcgen05 tensor cores of one GB300:
+//
+//     Y[m, n] = sum over kb of sa[m, kb] sw[n', kb]
+//                   sum over k in block kb of A[m, k] W[n, k],
+//
+// n' = n / 128 (weights in 128 x 128 blocks) or n (1 x 128 blocks).  The
+// inner sums of 128 products are left to the matrix instructions (fp32
+// accumulators in tensor memory); the scales differ from block to block, so
+// each block's sums are read back, scaled and added in fp32 registers.  One
+// rounding to the output type at the end.
+//
+// Both kernels are pipelines of specialised warps: one thread fills a ring of
+// shared-memory stages by TMA (128 bytes of K per row, 128-byte swizzle),
+// one thread issues the matrix instructions of a stage into one of several
+// tensor-memory buffers, two warps stage the scales of eight K blocks at a
+// time, and the epilogue warps drain the buffers into registers.  Every wait
+// is bounded.
+//
+//  * wide_kernel: 128 rows of A (the instruction's M) by BN rows of W, tiles
+//    walked by a persistent grid.  Each epilogue thread holds one row of A,
+//    so a K block's scale is one number per thread.
+//  * narrow_kernel, for few rows of A: 128 rows of W are the instruction's M
+//    and up to TN rows of A its N, so that the tensor cores waste nothing on
+//    absent rows and the call reads W once at HBM speed.  K is split over the
+//    CTAs of a cluster, which add their sums in rank order through
+//    distributed shared memory.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gemm_device.cuh"
+#include "nts_internal.h"
+
+namespace nts {
+
+namespace {
+
+// kStatusTimeout bits of these kernels.
+__device__ unsigned int g_gemm_status;
+
+constexpr int kChunk = 8;        // K blocks per piece of staged scales
+constexpr int kPieces = 2;       // pieces in flight
+
+struct GemmParams {
+  const float* sa;       // [M, kblocks]
+  const float* sw;       // [N / 128 or N, kblocks]
+  void* y;               // bf16 or fp32 [M, N]
+  int64_t M, N;
+  int kblocks;
+  int tiles_m, tiles_n;  // wide
+  int fp32_out;
+  int vec_out;           // rows of y start on 32-byte boundaries
+  uint64_t wait_limit_ns;
+  uint32_t missing_tx;   // test hook: bytes expected on the first stage but never sent
+};
+
+// After a wait gave up: the copies in flight land (the last S of `issued`
+// stages) and the matrix instructions in flight end, each within the limit,
+// before shared and tensor memory are given back.
+template <int S>
+__device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issued,
+                                      uint64_t limit_ns) {
+  if (threadIdx.x == 0)
+    for (int64_t j = max64(0, issued - S); j < issued; ++j)
+      (void)mbar_wait_bounded(full + 8 * (int)(j % S), (uint32_t)((j / S) & 1), limit_ns);
+  if (threadIdx.x == 32) {   // the thread that issues them
+    mma_commit(done);
+    (void)mbar_wait_bounded(done, 0, limit_ns);
+  }
+}
+
+// ---------------------------------------------------------------- wide
+
+constexpr int kWideThreads = 384;     // TMA, MMA, 2 scale warps, 8 epilogue warps
+constexpr int kGroupM = 16;           // tiles of A walked before the next tile of W
+
+template <int BN, bool ROWS>
+struct Wide {
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kBufs = 512 / BN;
+  static constexpr uint32_t kA = 128 * 128;
+  static constexpr uint32_t kStage = kA + BN * 128;
+  static constexpr int kScales = 128 + (ROWS ? BN : 4);   // floats per K block
+  static constexpr uint32_t kScaleOff = kStages * kStage;
+  static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
+  static constexpr uint32_t kBytes = kBarOff + 256;
+  static constexpr uint32_t kLaunch = kBytes + 1024;      // the base is rounded up to 1024
+};
+
+__device__ __forceinline__ void tile_at(const GemmParams& p, int64_t tile, int* tm, int* tn) {
+  const int64_t per_group = (int64_t)kGroupM * p.tiles_n;
+  const int64_t g = tile / per_group;
+  const int64_t in = tile - g * per_group;
+  const int rows = (int)min64(kGroupM, p.tiles_m - g * kGroupM);
+  *tn = (int)(in / rows);
+  *tm = (int)(g * kGroupM + (in - (int64_t)*tn * rows));
+}
+
+template <int BN, bool ROWS>
+__global__ void __launch_bounds__(kWideThreads, 1)
+wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+            const GemmParams p) {
+  using C = Wide<BN, ROWS>;
+  constexpr int S = C::kStages, NB = C::kBufs;
+  extern __shared__ unsigned char raw[];
+  const uint32_t sbase = (smem_addr(raw) + 1023u) & ~1023u;
+  unsigned char* smem = raw + (sbase - smem_addr(raw));
+  float* scales = reinterpret_cast<float*>(smem + C::kScaleOff);
+  const uint32_t bars = sbase + C::kBarOff;
+  const uint32_t full = bars, empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 8 * NB,
+                 sfull = tempty + 8 * NB, sempty = sfull + 8 * kPieces, done = sempty + 8 * kPieces,
+                 slot = done + 8;
+  volatile int* stop = reinterpret_cast<volatile int*>(smem + (slot + 4 - sbase));
+  int64_t* issued = reinterpret_cast<int64_t*>(smem + (slot + 8 - sbase));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 8);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(sfull + 8 * i, 2);
+      mbar_init(sempty + 8 * i, 8);
+    }
+    mbar_init(done, 1);
+    *stop = 0;
+    fence_mbar_init();
+    prefetch_tensor_map(&map_a);
+    prefetch_tensor_map(&map_w);
+  }
+  if (warp == 1) tmem_alloc(slot, 512);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - sbase));
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t n = 0;   // stages issued
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        int tm, tn;
+        tile_at(p, tile, &tm, &tn);
+        for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
+          const int s = (int)(n % S);
+          if (n >= S && !mbar_wait_or_stop(empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u,
+                                           p.wait_limit_ns, stop)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = sbase + s * C::kStage;
+          mbar_arrive_expect_tx(full + 8 * s, C::kStage + (n == 0 ? p.missing_tx : 0u));
+          tma_load_2d(at, &map_a, kb * 128, tm * 128, full + 8 * s);
+          tma_load_2d(at + C::kA, &map_w, kb * 128, tn * BN, full + 8 * s);
+        }
+      }
+      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+      *issued = n;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t instr = e4m3_instr(128, BN);
+      int64_t n = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
+          const int s = (int)(n % S), b = (int)(n % NB);
+          if (!mbar_wait_or_stop(full + 8 * s, (uint32_t)((n / S) & 1), p.wait_limit_ns, stop) ||
+              (n >= NB && !mbar_wait_or_stop(tempty + 8 * b, (uint32_t)((n / NB) & 1) ^ 1u,
+                                             p.wait_limit_ns, stop))) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          const uint64_t da = operand_desc(sbase + s * C::kStage);
+          const uint64_t dw = operand_desc(sbase + s * C::kStage + C::kA);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3(tmem + b * BN, da + 2 * k, dw + 2 * k, instr, k > 0);
+          mma_commit(empty + 8 * s);
+          mma_commit(tfull + 8 * b);
+        }
+      }
+      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+    }
+  } else if (warp < 4) {
+    // scale warps: lanes 8 r .. 8 r + 7 read the eight scales of a row
+    const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
+    int64_t n = 0;   // pieces staged
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      int tm, tn;
+      tile_at(p, tile, &tm, &tn);
+      bool ok = true;
+      for (int k0 = 0; k0 < p.kblocks; k0 += kChunk, ++n) {
+        const int c = (int)(n % kPieces);
+        if (n >= kPieces &&
+            !__all_sync(0xFFFFFFFFu,
+                        mbar_wait_or_stop(sempty + 8 * c, (uint32_t)((n / kPieces) & 1) ^ 1u,
+                                          p.wait_limit_ns, stop))) {
+          ok = false;
+          break;
+        }
+        float* dst = scales + (c * kChunk + kl) * C::kScales;
+        const bool in = k0 + kl < p.kblocks;
+#pragma unroll 8
+        for (int r = sub; r < 128; r += 8) {
+          const int64_t m = (int64_t)tm * 128 + r;
+          dst[r] = in && m < p.M ? __ldg(p.sa + m * p.kblocks + k0 + kl) : 0.f;
+        }
+        if (ROWS) {
+#pragma unroll 8
+          for (int r = sub; r < BN; r += 8) {
+            const int64_t w = (int64_t)tn * BN + r;
+            dst[128 + r] = in && w < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
+          }
+        } else if (sub < BN / 128) {
+          const int64_t w = (int64_t)tn * (BN / 128) + sub;
+          dst[128 + sub] = in && w * 128 < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull + 8 * c);
+      }
+      if (!ok) break;
+    }
+  } else {
+    // epilogue warps: four cover the 128 rows, two such groups the BN columns
+    constexpr int COLS = BN / 2;
+    const int group = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+    const int wblock = ROWS ? group * COLS : group * COLS / 128;
+    int64_t n = 0, piece = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      int tm, tn;
+      tile_at(p, tile, &tm, &tn);
+      float acc[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      bool ok = true;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
+        const int b = (int)(n % NB);
+        const int c = (int)(piece % kPieces);
+        if ((kb % kChunk == 0 &&
+             !__all_sync(0xFFFFFFFFu,
+                         mbar_wait_or_stop(sfull + 8 * c, (uint32_t)((piece / kPieces) & 1),
+                                           p.wait_limit_ns, stop))) ||
+            !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * b, (uint32_t)((n / NB) & 1),
+                                                       p.wait_limit_ns, stop))) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        const float* sc = scales + (c * kChunk + kb % kChunk) * C::kScales;
+        const float s = ROWS ? sc[row] : sc[row] * sc[128 + wblock];
+        const uint32_t at = tmem + b * BN + group * COLS + lanes;
+        uint32_t v[2][16];
+        tmem_load16(v[0], at);
+#pragma unroll
+        for (int j = 0; j < COLS / 16; ++j) {
+          tmem_wait16(v[j & 1]);
+          if (j + 1 < COLS / 16) tmem_load16(v[(j + 1) & 1], at + 16 * (j + 1));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float w = ROWS ? s * sc[128 + wblock + 16 * j + i] : s;
+            acc[16 * j + i] = fmaf(__uint_as_float(v[j & 1][i]), w, acc[16 * j + i]);
+          }
+        }
+        tcgen05_fence_before();
+        __syncwarp();
+        const bool last = kb % kChunk == kChunk - 1 || kb == p.kblocks - 1;
+        if (lane == 0) {
+          mbar_arrive(tempty + 8 * b);
+          if (last) mbar_arrive(sempty + 8 * c);
+        }
+        if (last) ++piece;
+      }
+      if (!ok) {
+        if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
+        break;
+      }
+      const int64_t m = (int64_t)tm * 128 + row;
+      const int64_t n0 = (int64_t)tn * BN + group * COLS;
+      if (m < p.M) {
+        if (p.fp32_out) {
+          float* y = static_cast<float*>(p.y) + m * p.N + n0;
+#pragma unroll
+          for (int j = 0; j < COLS; j += 8) {
+            if (p.vec_out && n0 + j + 8 <= p.N)
+              st_global_v8(y + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                           __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]),
+                           __float_as_uint(acc[j + 4]), __float_as_uint(acc[j + 5]),
+                           __float_as_uint(acc[j + 6]), __float_as_uint(acc[j + 7]));
+            else
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (n0 + j + i < p.N) y[j + i] = acc[j + i];
+          }
+        } else {
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + m * p.N + n0;
+#pragma unroll
+          for (int j = 0; j < COLS; j += 16) {
+            if (p.vec_out && n0 + j + 16 <= p.N)
+              st_global_v8(y + j, pack_bf16x2_rn(acc[j], acc[j + 1]),
+                           pack_bf16x2_rn(acc[j + 2], acc[j + 3]),
+                           pack_bf16x2_rn(acc[j + 4], acc[j + 5]),
+                           pack_bf16x2_rn(acc[j + 6], acc[j + 7]),
+                           pack_bf16x2_rn(acc[j + 8], acc[j + 9]),
+                           pack_bf16x2_rn(acc[j + 10], acc[j + 11]),
+                           pack_bf16x2_rn(acc[j + 12], acc[j + 13]),
+                           pack_bf16x2_rn(acc[j + 14], acc[j + 15]));
+            else
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (n0 + j + i < p.N) y[j + i] = __float2bfloat16_rn(acc[j + i]);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tcgen05_fence_before();
+  __syncthreads();
+  if (*stop) {
+    drain<S>(full, done, *issued, p.wait_limit_ns);
+    __syncthreads();
+  }
+  tcgen05_fence_after();
+  if (warp == 1) tmem_free(tmem, 512);
+}
+
+// -------------------------------------------------------------- narrow
+
+constexpr int kNarrowThreads = 256;   // TMA, MMA, 2 scale warps, 4 epilogue warps
+
+template <int TN, bool ROWS>
+struct Narrow {
+  static constexpr int kBufs = 4;
+  static constexpr uint32_t kBufCols = TN < 32 ? 32 : TN;
+  static constexpr uint32_t kCols = kBufCols * kBufs;
+  static constexpr uint32_t kW = 128 * 128;
+  static constexpr uint32_t kStage = kW + TN * 128;
+  static constexpr int kStages = 196608 / (int)kStage;    // 6 (TN = 128) to 10 (TN = 16)
+  static constexpr int kScales = TN + (ROWS ? 128 : 4);
+  static constexpr uint32_t kScaleOff = kStages * kStage;
+  static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
+  static constexpr uint32_t kBytes = kBarOff + 512;
+  static constexpr uint32_t kLaunch = kBytes + 1024;
+  static_assert(kScaleOff >= TN * 128 * 4, "the sums for the other CTAs fit the ring");
+};
+
+template <int TN, bool ROWS>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+              const GemmParams p) {
+  using C = Narrow<TN, ROWS>;
+  constexpr int S = C::kStages, NB = C::kBufs;
+  extern __shared__ unsigned char raw[];
+  const uint32_t sbase = (smem_addr(raw) + 1023u) & ~1023u;
+  unsigned char* smem = raw + (sbase - smem_addr(raw));
+  float* scales = reinterpret_cast<float*>(smem + C::kScaleOff);
+  const uint32_t bars = sbase + C::kBarOff;
+  const uint32_t full = bars, empty = full + 8 * S, tfull = empty + 8 * S, tempty = tfull + 8 * NB,
+                 sfull = tempty + 8 * NB, sempty = sfull + 8 * kPieces, done = sempty + 8 * kPieces,
+                 slot = done + 8;
+  volatile int* stop = reinterpret_cast<volatile int*>(smem + (slot + 4 - sbase));
+  int64_t* issued = reinterpret_cast<int64_t*>(smem + (slot + 8 - sbase));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // gridDim.x = tiles of W x CTAs of a cluster, gridDim.y = tiles of A
+  int split;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+  const int rank = (int)cluster_ctarank();
+  const int tn = (int)blockIdx.x / split;
+  const int tm = (int)blockIdx.y;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / split);
+  const int kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 4);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(sfull + 8 * i, 2);
+      mbar_init(sempty + 8 * i, 4);
+    }
+    mbar_init(done, 1);
+    *stop = 0;
+    fence_mbar_init();
+    prefetch_tensor_map(&map_a);
+    prefetch_tensor_map(&map_w);
+  }
+  if (warp == 1) tmem_alloc(slot, C::kCols);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - sbase));
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  float acc[TN];
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int n = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const int s = n % S;
+        if (n >= S && !mbar_wait_or_stop(empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u,
+                                         p.wait_limit_ns, stop)) {
+          ok = false;
+          break;
+        }
+        const uint32_t at = sbase + s * C::kStage;
+        mbar_arrive_expect_tx(full + 8 * s, C::kStage + (n == 0 ? p.missing_tx : 0u));
+        tma_load_2d(at, &map_w, kb * 128, tn * 128, full + 8 * s);
+        tma_load_2d(at + C::kW, &map_a, kb * 128, tm * TN, full + 8 * s);
+      }
+      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+      *issued = n;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t instr = e4m3_instr(128, TN);
+      bool ok = true;
+      int n = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const int s = n % S, b = n % NB;
+        if (!mbar_wait_or_stop(full + 8 * s, (uint32_t)((n / S) & 1), p.wait_limit_ns, stop) ||
+            (n >= NB && !mbar_wait_or_stop(tempty + 8 * b, (uint32_t)((n / NB) & 1) ^ 1u,
+                                           p.wait_limit_ns, stop))) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        const uint64_t dw = operand_desc(sbase + s * C::kStage);
+        const uint64_t da = operand_desc(sbase + s * C::kStage + C::kW);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_e4m3(tmem + b * C::kBufCols, dw + 2 * k, da + 2 * k, instr, k > 0);
+        mma_commit(empty + 8 * s);
+        mma_commit(tfull + 8 * b);
+      }
+      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+    }
+  } else if (warp < 4) {
+    const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
+    int n = 0;
+    for (int k0 = kb0; k0 < kb1; k0 += kChunk, ++n) {
+      const int c = n % kPieces;
+      if (n >= kPieces &&
+          !__all_sync(0xFFFFFFFFu,
+                      mbar_wait_or_stop(sempty + 8 * c, (uint32_t)((n / kPieces) & 1) ^ 1u,
+                                        p.wait_limit_ns, stop)))
+        break;
+      float* dst = scales + (c * kChunk + kl) * C::kScales;
+      const bool in = k0 + kl < kb1;
+#pragma unroll 8
+      for (int r = sub; r < TN; r += 8) {
+        const int64_t m = (int64_t)tm * TN + r;
+        dst[r] = in && m < p.M ? __ldg(p.sa + m * p.kblocks + k0 + kl) : 0.f;
+      }
+      if (ROWS) {
+#pragma unroll 8
+        for (int r = sub; r < 128; r += 8) {
+          const int64_t w = (int64_t)tn * 128 + r;
+          dst[TN + r] = in && w < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
+        }
+      } else if (sub == 0) {
+        dst[TN] = in ? __ldg(p.sw + (int64_t)tn * p.kblocks + k0 + kl) : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sfull + 8 * c);
+    }
+  } else {
+    const int row = (warp & 3) * 32 + lane;   // of W
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[j] = 0.f;
+    int n = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++n) {
+      const int b = n % NB, piece = n / kChunk, c = piece % kPieces;
+      if ((n % kChunk == 0 &&
+           !__all_sync(0xFFFFFFFFu,
+                       mbar_wait_or_stop(sfull + 8 * c, (uint32_t)((piece / kPieces) & 1),
+                                         p.wait_limit_ns, stop))) ||
+          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * b, (uint32_t)((n / NB) & 1),
+                                                     p.wait_limit_ns, stop))) {
+        if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
+        break;
+      }
+      tcgen05_fence_after();
+      const float* sc = scales + (c * kChunk + n % kChunk) * C::kScales;
+      const float sw = sc[TN + (ROWS ? row : 0)];
+      const uint32_t at = tmem + b * C::kBufCols + lanes;
+      uint32_t v[2][16];
+      tmem_load16(v[0], at);
+#pragma unroll
+      for (int j = 0; j < TN / 16; ++j) {
+        tmem_wait16(v[j & 1]);
+        if (j + 1 < TN / 16) tmem_load16(v[(j + 1) & 1], at + 16 * (j + 1));
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[16 * j + i] =
+              fmaf(__uint_as_float(v[j & 1][i]), sw * sc[16 * j + i], acc[16 * j + i]);
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(tempty + 8 * b);
+        if (n % kChunk == kChunk - 1) mbar_arrive(sempty + 8 * c);
+      }
+    }
+  }
+  __syncwarp();
+  tcgen05_fence_before();
+  __syncthreads();
+  if (*stop) {
+    drain<S>(full, done, *issued, p.wait_limit_ns);
+    __syncthreads();
+  }
+  tcgen05_fence_after();
+  if (warp == 1) tmem_free(tmem, C::kCols);
+
+  // The sums of this CTA's K blocks to shared memory (the ring is drained),
+  // then every CTA adds its share of the tile over the ranks, in their order.
+  float* sums = reinterpret_cast<float*>(smem);   // [TN][128]
+  if (warp >= 4) {
+    const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sums[j * 128 + row] = acc[j];
+  }
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  const int rows = (int)min64(TN, p.M - (int64_t)tm * TN);
+  for (int i = rank * kNarrowThreads + threadIdx.x; i < rows * 128; i += split * kNarrowThreads) {
+    const int64_t m = (int64_t)tm * TN + (i >> 7), nn = (int64_t)tn * 128 + (i & 127);
+    float v = 0.f;
+    for (int r = 0; r < split; ++r) v += ld_cluster_f32(map_to_rank(sbase + 4 * i, (uint32_t)r));
+    if (nn < p.N) {
+      if (p.fp32_out)
+        static_cast<float*>(p.y)[m * p.N + nn] = v;
+      else
+        static_cast<__nv_bfloat16*>(p.y)[m * p.N + nn] = __float2bfloat16_rn(v);
+    }
+  }
+  // no CTA leaves while another reads its sums
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+
+// ----------------------------------------------------------------- host
+
+using GemmKernel = void (*)(CUtensorMap, CUtensorMap, GemmParams);
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return (EncodeTiled) nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Map of an E4M3 matrix [rows, K], copied in boxes of box_rows x 128 bytes
+// with the 128-byte swizzle; rows and columns outside read as zeros.
+int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+  const EncodeTiled enc = encode_tiled();
+  if (enc == nullptr) return fail(NTS_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t step[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                         strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NTS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return NTS_OK;
+}
+
+int launch(GemmKernel kern, const GemmRequest& rq, const GemmParams& p, int box_a, int box_w,
+           dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, bool pdl) {
+  CUtensorMap map_a, map_w;
+  int rc = make_map(&map_a, rq.A, rq.M, rq.K, box_a);
+  if (rc == NTS_OK) rc = make_map(&map_w, rq.W, rq.N, rq.K, box_w);
+  if (rc == NTS_OK) rc = prepare_kernel((const void*)kern, smem);
+  if (rc != NTS_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  if (cluster > 0) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = (unsigned)cluster;
+    attr[na].val.clusterDim.y = 1;
+    attr[na++].val.clusterDim.z = 1;
+  }
+  if (pdl) attr[na++] = pdl_attribute();
+  cfg.numAttrs = na;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_w, p);
+  if (e != cudaSuccess) return fail_cuda(e, "launching the block-scaled product");
+  return NTS_OK;
+}
+
+template <int TN>
+int launch_narrow(const GemmRequest& rq, const GemmParams& p, cudaStream_t stream,
+                  const DeviceInfo& dev, const LaunchTuning& tune) {
+  const int64_t tiles_n = (p.N + 127) / 128, tiles_m = (p.M + TN - 1) / TN;
+  int split = 1;
+  while (split < 8 && 2 * split <= p.kblocks && tiles_n * tiles_m * split * 2 <= dev.sm_count)
+    split *= 2;
+  const int64_t gx = tiles_n * split;
+  if (gx > 0x7fffffffll || tiles_m > 65535)
+    return fail(NTS_ERR_UNSUPPORTED, "too many tiles in one call");
+  log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld narrow TN=%d split=%d", (long long)p.M,
+             (long long)p.N, (long long)rq.K, TN, split);
+  const dim3 grid((unsigned)gx, (unsigned)tiles_m);
+  return rq.w_rows == 1
+             ? launch(narrow_kernel<TN, true>, rq, p, TN, 128, grid, kNarrowThreads,
+                      Narrow<TN, true>::kLaunch, split, stream, tune.pdl != 0)
+             : launch(narrow_kernel<TN, false>, rq, p, TN, 128, grid, kNarrowThreads,
+                      Narrow<TN, false>::kLaunch, split, stream, tune.pdl != 0);
+}
+
+template <int BN>
+int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const DeviceInfo& dev,
+                const LaunchTuning& tune) {
+  p.tiles_m = (int)((p.M + 127) / 128);
+  p.tiles_n = (int)((p.N + BN - 1) / BN);
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((int64_t)p.tiles_m * p.tiles_n, dev.sm_count);
+  log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide BN=%d grid=%u", (long long)p.M,
+             (long long)p.N, (long long)rq.K, BN, grid);
+  return rq.w_rows == 1
+             ? launch(wide_kernel<BN, true>, rq, p, 128, BN, dim3(grid), kWideThreads,
+                      Wide<BN, true>::kLaunch, 0, stream, tune.pdl != 0)
+             : launch(wide_kernel<BN, false>, rq, p, 128, BN, dim3(grid), kWideThreads,
+                      Wide<BN, false>::kLaunch, 0, stream, tune.pdl != 0);
+}
+
+}  // namespace
+
+int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune) {
+  if (const int injected = take_injected_failure()) return injected;
+  const DeviceInfo& dev = device_info();
+  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  GemmParams p = {};
+  p.sa = rq.a_scales;
+  p.sw = rq.w_scales;
+  p.y = rq.Y;
+  p.M = rq.M;
+  p.N = rq.N;
+  p.kblocks = (int)((rq.K + 127) / 128);
+  p.fp32_out = rq.fp32_out;
+  const int64_t row_bytes = p.N * (p.fp32_out ? 4 : 2);
+  p.vec_out = row_bytes % 32 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
+  p.wait_limit_ns = tune.wait_limit_ns;
+  p.missing_tx = tune.missing_tx;
+  if (p.M <= 16) return launch_narrow<16>(rq, p, stream, dev, tune);
+  if (p.M <= 32) return launch_narrow<32>(rq, p, stream, dev, tune);
+  if (p.M <= 64) return launch_narrow<64>(rq, p, stream, dev, tune);
+  if (p.M <= 128) return launch_narrow<128>(rq, p, stream, dev, tune);
+  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 255) / 256);
+  return tiles >= dev.sm_count ? launch_wide<256>(rq, p, stream, dev, tune)
+                               : launch_wide<128>(rq, p, stream, dev, tune);
+}
+
+int read_and_clear_gemm_status(unsigned* out) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_gemm_status, sizeof(v));
+  if (e != cudaSuccess) return fail_cuda(e, "reading the product's status word");
+  if (v != 0) e = cudaMemcpyToSymbol(g_gemm_status, &zero, sizeof(zero));
+  if (e != cudaSuccess) return fail_cuda(e, "clearing the product's status word");
+  *out = v;
+  return NTS_OK;
+}
+
+}  // namespace nts
