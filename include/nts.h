@@ -1,7 +1,9 @@
 /*
  * nts.h -- C ABI of libnts, GB300 (sm_103a) kernels for per-token RMS
  * normalization: split-H layerwise QK-RMSNorm, fused RMSNorm + MX cast, and
- * MXNorm + MX cast.
+ * MXNorm + MX cast; and for the QKV projection between them: block-128 E4M3
+ * casts, the block-scaled 8-bit matrix product, and headwise QK-RMSNorm with
+ * the rotary position embedding, forward and backward.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -53,7 +55,8 @@ extern "C" {
 
 typedef enum {
     NTS_OK = 0,
-    NTS_ERR_INVALID_ARG = 1, /* null required pointer, bad size/shape/eps/N/B/fmt/p */
+    NTS_ERR_INVALID_ARG = 1, /* null required pointer, bad size/shape/eps/N/B/fmt/p; from
+                                nts_check_status: a position outside the rotation table */
     NTS_ERR_UNSUPPORTED = 2, /* valid request this build cannot run: misaligned
                                 pointer, row too wide, cluster not launchable */
     NTS_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
@@ -65,6 +68,11 @@ typedef enum {
     NTS_FMT_E2M1 = 1, /* OCP E2M1: 4 bits per element, max 6; E8M0 scales (MXFP4) */
     NTS_FMT_NVFP4 = 2 /* E2M1 elements, B = 16, one E4M3 scale per block (NVFP4) */
 } nts_elem_fmt;
+
+typedef enum {
+    NTS_OUT_BF16 = 0,
+    NTS_OUT_FP32 = 1
+} nts_out_type;
 
 /* Library version, major*10000 + minor*100 + patch. */
 NTS_API int nts_version(void);
@@ -311,9 +319,177 @@ NTS_API int nts_mxnorm_postround_cast(const void *X_dev, const float *gamma_dev,
 NTS_API int nts_mxnorm_correction(int B, int p, double *c_out);
 
 /*
+ * nts_rope_table_host -- the table of nts_qknorm_rope, on the host: row pos
+ * holds the cosines of the rot_dim/2 angles pos * base^(-2i/rot_dim), then
+ * their sines, each formed in double precision (far positions keep their
+ * angle) and rounded once to fp32.
+ *   table_host  fp32 [P, rot_dim], written.   base > 0 and finite.
+ * Errors: INVALID_ARG.
+ */
+NTS_API int nts_rope_table_host(int64_t P, int64_t rot_dim, double base, float *table_host);
+
+/*
+ * nts_qknorm_rope -- headwise QK-RMSNorm (nts_qknorm_rms_heads) of a token
+ * batch's Q and K with the rotary position embedding in the same pass, one
+ * launch.  Per head of head_dim = d values of the token at position pos:
+ *
+ *     rinv = 1 / sqrt((1/d) sum x^2 + eps)                       (fp32)
+ *     n_j  = (x_j * gamma_j) * rinv                              (fp32)
+ *     y_a  = n_a c - n_b s,   y_b = n_b c + n_a s     for every pair (a, b)
+ *            of the first rot_dim values, with c = table[pos][i] and
+ *            s = table[pos][rot_dim/2 + i], i the pair's number
+ *     y_j  = n_j                                      for j >= rot_dim
+ *
+ * and one rounding to bf16.  Pair i is (i, i + rot_dim/2), or (2i, 2i + 1)
+ * when `interleaved` is not 0.
+ *
+ *   Q_dev, K_dev    bf16, row t at t*ldq (t*ldk) elements: nheads_q (nheads_k)
+ *                   heads of head_dim values one after another.  Row strides
+ *                   let both be columns of one packed QKV buffer.
+ *   Yq_dev, Yk_dev  the same layout with strides ldyq, ldyk.  Y == X with the
+ *                   same stride (in place) is allowed; any other overlap is
+ *                   undefined.  Values between the rows are left alone.
+ *   gamma_*_dev     fp32 [head_dim].
+ *   rinv_*_dev      fp32 [T, nheads] or NULL.
+ *   positions_dev   int64 [T].  A negative position marks a padding row: its
+ *                   Q and K may hold anything, its Y is zeros and its rinv 0.
+ *                   A position >= P gives the same zeros and is reported by
+ *                   nts_check_status (INVALID_ARG).
+ *   table_dev       fp32 [P, rot_dim], P >= 1 (nts_rope_table_host).
+ *   T >= 0; head_dim a multiple of 16 up to 512; rot_dim a multiple of 16,
+ *   0 < rot_dim <= head_dim; strides multiples of 8.
+ * Errors: INVALID_ARG (null required pointer, bad sizes, eps, odd rot_dim or
+ *         one beyond head_dim, a stride below the row), UNSUPPORTED (other
+ *         head_dim or rot_dim, unaligned rows, T >= 2^31, more than 65536
+ *         heads), CUDA.
+ */
+NTS_API int nts_qknorm_rope(const void *Q_dev, int64_t ldq, const float *gamma_q_dev,
+                            void *Yq_dev, int64_t ldyq, float *rinv_q_dev, const void *K_dev,
+                            int64_t ldk, const float *gamma_k_dev, void *Yk_dev, int64_t ldyk,
+                            float *rinv_k_dev, const int64_t *positions_dev,
+                            const float *table_dev, int64_t P, int64_t T, int64_t nheads_q,
+                            int64_t nheads_k, int64_t head_dim, int64_t rot_dim,
+                            int interleaved, float eps, void *stream);
+
+/*
+ * nts_qknorm_rope_backward -- the gradient of nts_qknorm_rope.  With g the
+ * rotation of dy by the opposite angles and u_j = g_j gamma_j:
+ *
+ *     dx_j      = rinv (u_j - x_j rinv^2 (1/d) sum u x)          (bf16)
+ *     dgamma_j  = sum over tokens and heads of g_j x_j rinv      (fp32)
+ *
+ * rinv is formed again from Q and K (the forward pass's inputs).  Padding
+ * rows, and rows whose position lies outside the table, get zeros and add
+ * nothing to dgamma.  The sums have a fixed order: equal calls give equal
+ * bits.
+ *   dYq_dev, dYk_dev, dQ_dev, dK_dev  bf16, laid out as Q and K, each with its
+ *                   own row stride; dQ == dYq or dQ == Q with the same stride
+ *                   is allowed (dK likewise).
+ *   dgamma_*_dev    fp32 [head_dim], overwritten (zeros when T == 0).
+ *   workspace_dev   scratch of at least nts_qknorm_rope_backward_workspace()
+ *                   bytes, 4-byte aligned, contents arbitrary before and
+ *                   after; calls that overlap in time need one each.
+ * Other arguments, limits and errors as nts_qknorm_rope; INVALID_ARG also for
+ * a missing or short workspace.
+ */
+NTS_API int nts_qknorm_rope_backward(const void *dYq_dev, int64_t lddyq, const void *dYk_dev,
+                                     int64_t lddyk, const void *Q_dev, int64_t ldq,
+                                     const float *gamma_q_dev, const void *K_dev, int64_t ldk,
+                                     const float *gamma_k_dev, const int64_t *positions_dev,
+                                     const float *table_dev, int64_t P, void *dQ_dev,
+                                     int64_t lddq, void *dK_dev, int64_t lddk,
+                                     float *dgamma_q_dev, float *dgamma_k_dev,
+                                     void *workspace_dev, int64_t workspace_bytes, int64_t T,
+                                     int64_t nheads_q, int64_t nheads_k, int64_t head_dim,
+                                     int64_t rot_dim, int interleaved, float eps, void *stream);
+
+/* Workspace bytes of nts_qknorm_rope_backward.  Errors: INVALID_ARG. */
+NTS_API int nts_qknorm_rope_backward_workspace(int64_t head_dim, int64_t *bytes_out);
+
+/*
+ * nts_rmsnorm_blockcast -- RMSNorm fused with the cast to E4M3 codes that
+ * carry one fp32 scale per block of 128 contiguous values (the last block of
+ * a row may be shorter), the operand of nts_gemm_blockscaled:
+ *
+ *     rinv    = 1 / sqrt((1/D) sum_j x_j^2 + eps)                (fp32)
+ *     w_j     = fp32(fp32(x_j * gamma_j) * rinv), or fp32(x_j * rinv)
+ *     scale_k = fp32(max(absmax of block k, 2^-100) / 448)
+ *     code_j  = E4M3_rne_satfinite(fp32(w_j * fp32(1 / scale_k)))
+ *
+ * so code * scale stands for w.  A NaN keeps its place as the NaN code; a
+ * block that holds an infinity gets an infinite scale.
+ *   X_dev       bf16 [T, D], read.       gamma_dev   fp32 [D] or NULL.
+ *   codes_dev   uint8 [T, D], written.   scales_dev  fp32 [T, ceil(D/128)].
+ *   rinv_dev    fp32 [T] or NULL.
+ *   T >= 0; D a multiple of 16 up to 32768; eps > 0 and finite.
+ * Errors: INVALID_ARG (null X/codes/scales, T < 0, D <= 0, bad eps),
+ *         UNSUPPORTED (D % 16, D too wide, unaligned pointer), CUDA.
+ */
+NTS_API int nts_rmsnorm_blockcast(const void *X_dev, const float *gamma_dev, uint8_t *codes_dev,
+                                  float *scales_dev, float *rinv_dev, int64_t T, int64_t D,
+                                  float eps, void *stream);
+
+/*
+ * nts_blockcast -- the cast of nts_rmsnorm_blockcast without the norm
+ * (w = x), in blocks of block_rows x 128 values: 1 for activations and
+ * gradients, 128 for weights.
+ *   codes_dev   uint8 [T, D].
+ *   scales_dev  fp32 [ceil(T / block_rows), ceil(D / 128)].
+ *   D a multiple of 16; block_rows 1 or 128.
+ * Errors: as nts_rmsnorm_blockcast; INVALID_ARG also for another block_rows.
+ */
+NTS_API int nts_blockcast(const void *X_dev, uint8_t *codes_dev, float *scales_dev, int64_t T,
+                          int64_t D, int block_rows, void *stream);
+
+/*
+ * nts_blockcast_t -- the transpose of X [T, D], cast in blocks of 128 tokens
+ * of one column: the operands of a weight gradient, whose sums run over the
+ * tokens.
+ *   codes_dev   uint8 [D, Tp], Tp = T rounded up to a multiple of 16; the
+ *               codes of the Tp - T tokens beyond T are zero.
+ *   scales_dev  fp32 [D, ceil(T / 128)].
+ *   D a multiple of 16.
+ * Errors: as nts_rmsnorm_blockcast.
+ */
+NTS_API int nts_blockcast_t(const void *X_dev, uint8_t *codes_dev, float *scales_dev, int64_t T,
+                            int64_t D, void *stream);
+
+/*
+ * nts_gemm_blockscaled -- matrix product of E4M3 operands with one fp32 scale
+ * per block of 128 values along K, on the tensor cores:
+ *
+ *     Y[m][n] = sum_kb a_scales[m][kb] w_scales[n'][kb]
+ *                   sum_{k in block kb} A[m][k] W[n][k]
+ *
+ * with n' = n / 128 (w_block_rows = 128: weights in 128 x 128 blocks) or n
+ * (w_block_rows = 1).  Sums in fp32, one rounding to the output type.  For
+ * Y = X W^T take A = the cast of X and W = nts_blockcast(.., 128); the
+ * gradient of X is the same product of dY with the transposed weights (their
+ * 128 x 128 scales transposed too); the gradient of W is the product of
+ * nts_blockcast_t(dY) with nts_blockcast_t(X), w_block_rows = 1.
+ *   A_codes_dev  uint8 [M, K].   a_scales_dev  fp32 [M, ceil(K/128)].
+ *   W_codes_dev  uint8 [N, K].   w_scales_dev  fp32 [ceil(N/128) or N,
+ *                                              ceil(K/128)].
+ *   Y_dev        bf16 or fp32 [M, N] (out_type, an nts_out_type), written;
+ *                overlaps no operand.
+ *   M >= 0; N > 0; K a positive multiple of 16 (the last block may be
+ *   shorter than 128).
+ * The order of the sums depends on the shape alone: equal calls give equal
+ * bits.
+ * Errors: INVALID_ARG (null pointer, bad sizes, w_block_rows or out_type),
+ *         UNSUPPORTED (K % 16, unaligned codes or Y, sizes from 2^31 - 256),
+ *         CUDA.
+ */
+NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scales_dev,
+                                 const uint8_t *W_codes_dev, const float *w_scales_dev,
+                                 int w_block_rows, void *Y_dev, int out_type, int64_t M,
+                                 int64_t N, int64_t K, void *stream);
+
+/*
  * nts_check_status -- synchronizes `stream`, then reads and clears the
  * device status words.  Returns NTS_ERR_TIMEOUT if any kernel since the last
  * check gave up on a bounded wait (its outputs are then undefined),
+ * NTS_ERR_INVALID_ARG if a rotation call met a position outside its table,
  * NTS_ERR_CUDA if the stream reported an error, NTS_OK otherwise.
  */
 NTS_API int nts_check_status(void *stream);

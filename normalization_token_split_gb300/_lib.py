@@ -41,6 +41,17 @@ def _declare(lib):
         "nts_rmsnorm_mxcast": ([P, P, P, P, P, P, i64, i64, f32, i32, i32, P], i32),
         "nts_mxnorm_cast": ([P, P, P, P, P, P, i64, i64, f32, i32, i32, i32, P], i32),
         "nts_mxnorm_postround_cast": ([P, P, P, P, P, P, i64, i64, f32, i32, i32, i32, P], i32),
+        "nts_rope_table_host": ([i64, i64, ctypes.c_double, P], i32),
+        "nts_qknorm_rope": ([P, i64, P, P, i64, P, P, i64, P, P, i64, P, P, P, i64, i64, i64, i64,
+                             i64, i64, i32, f32, P], i32),
+        "nts_qknorm_rope_backward": ([P, i64, P, i64, P, i64, P, P, i64, P, P, P, i64, P, i64, P,
+                                      i64, P, P, P, i64, i64, i64, i64, i64, i64, i32, f32, P],
+                                     i32),
+        "nts_qknorm_rope_backward_workspace": ([i64, ctypes.POINTER(i64)], i32),
+        "nts_rmsnorm_blockcast": ([P, P, P, P, P, i64, i64, f32, P], i32),
+        "nts_blockcast": ([P, P, P, i64, i64, i32, P], i32),
+        "nts_blockcast_t": ([P, P, P, i64, i64, P], i32),
+        "nts_gemm_blockscaled": ([P, P, P, P, i32, P, i32, i64, i64, i64, P], i32),
         "nts_mxnorm_correction": ([i32, i32, ctypes.POINTER(ctypes.c_double)], i32),
         "nts_check_status": ([P], i32),
         "nts_qknorm_rms_host": ([P, P, P, P, P, P, P, i64, i64, f32, i32, P], i32),

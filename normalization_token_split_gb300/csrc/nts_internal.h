@@ -160,6 +160,60 @@ int mxnorm_cast_host_one_stream(const void* X_host, const float* gamma_dev, uint
                                 uint8_t* scales_dev, int64_t T, int64_t D, float eps, int B,
                                 int fmt, int p, void* stream);
 
+// Headwise QK-RMSNorm of Q (ten[0]) and K (ten[1]) with the rotary position
+// embedding, and its gradient (rope_kernel.cu).
+struct RopeOperand {
+  const void* x;
+  const void* dy;      // backward
+  void* out;           // y, or dx
+  const float* gamma;
+  float* rinv;         // forward, nullable
+  int64_t ldx, lddy, ldout;
+  int64_t nheads;
+};
+struct RopeRequest {
+  RopeOperand ten[2];
+  const int64_t* pos;
+  const float* table;
+  int64_t P, T, head_dim, rot_dim;
+  int interleaved;
+  float eps;
+};
+// Most CTAs (rows of partial sums in the workspace) of a gradient launch.
+constexpr int kRopePartials = 1024;
+int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
+int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k,
+                         float* workspace, cudaStream_t stream, const LaunchTuning& tune);
+
+// Casts to E4M3 codes with an fp32 scale per 128 values (blockcast_kernel.cu).
+enum CastKind { kCastNorm, kCastPlain, kCastTiles, kCastTranspose };
+struct BlockcastRequest {
+  CastKind kind;
+  const void* X;
+  const float* gamma;  // kCastNorm, nullable
+  uint8_t* codes;
+  float* scales;
+  float* rinv;         // kCastNorm, nullable
+  int64_t T, D;
+  float eps;
+};
+int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
+
+// Block-scaled product of E4M3 operands (gemm_kernel.cu).
+struct GemmRequest {
+  const void* A;
+  const float* a_scales;
+  const void* W;
+  const float* w_scales;
+  int w_rows;          // 128 or 1: rows of W per scale
+  void* Y;
+  int fp32_out;
+  int64_t M, N, K;
+};
+int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
+
+int read_and_clear_rope_status(unsigned* out);
+int read_and_clear_gemm_status(unsigned* out);
 int read_and_clear_qk_status(unsigned* out);
 int read_and_clear_mx_status(unsigned* out);
 

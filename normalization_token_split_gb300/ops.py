@@ -288,6 +288,256 @@ def mxnorm_postround_cast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
     return MxOut(codes, scales, rinv, amax)
 
 
+# ------------------------------------------ the operators around a projection
+
+BLOCK = 128    # values per scale of the block-scaled 8-bit operands
+
+
+class BlockOut(NamedTuple):
+    codes: torch.Tensor     # uint8 [T, D], or [D, Tp] transposed
+    scales: torch.Tensor    # fp32, one per block of 128 values
+    rinv: Optional[torch.Tensor]   # fp32 [T]
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _on_device(first: torch.Tensor, *others) -> None:
+    """The kernels run on the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device()
+    for t in (first, *others):
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _out(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, device=like.device, dtype=dtype)
+    _need_cuda(name, t, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _rows(name: str, t: torch.Tensor, shape=None) -> int:
+    """Row stride of a bf16 matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a matrix of shape "
+                         f"{'[T, heads * head_dim]' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim):
+    """Checks what a rotation and its gradient share; (T, nheads_q, nheads_k, P, rot_dim)."""
+    d = int(head_dim)
+    if d <= 0 or q.shape[1] % d != 0 or k.shape[1] % d != 0:
+        raise ValueError("q and k must hold whole heads of head_dim values")
+    if k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must have the same number of tokens")
+    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        _need_cuda(name, g, torch.float32)
+        if g.numel() != d:
+            raise ValueError(f"{name} must hold head_dim = {d} values, got {g.numel()}")
+    _need_cuda("positions", positions, torch.int64)
+    if positions.numel() != q.shape[0]:
+        raise ValueError("positions must hold one position per token")
+    _need_cuda("table", table, torch.float32)
+    if table.dim() != 2:
+        raise ValueError("table must be a matrix [P, rot_dim]")
+    return q.shape[0], q.shape[1] // d, k.shape[1] // d, table.shape[0], table.shape[1]
+
+
+def rope_table(P: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The rotation table of qknorm_rope: fp32 [P, rot_dim], row pos the
+    cosines of pos * base^(-2i/rot_dim), then the sines (formed on the host
+    in double precision)."""
+    t = torch.empty(int(P), int(rot_dim), dtype=torch.float32)
+    check(lib().nts_rope_table_host(int(P), int(rot_dim), float(base), _ptr(t)))
+    return t.to(device)
+
+
+def qknorm_rope(q: torch.Tensor, gamma_q: torch.Tensor, k: torch.Tensor, gamma_k: torch.Tensor,
+                positions: torch.Tensor, table: torch.Tensor, head_dim: int, eps: float = 1e-6,
+                interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
+                out_k: Optional[torch.Tensor] = None, rinv_q: Optional[torch.Tensor] = None,
+                rinv_k: Optional[torch.Tensor] = None, want_rinv: bool = False, stream=None):
+    """Headwise QK-RMSNorm of q [T, nheads_q * head_dim] and k [T, nheads_k *
+    head_dim] (bf16, rows contiguous, any row stride: columns of a packed QKV
+    buffer) with the rotary position embedding of positions (int64 [T],
+    negative: padding row, zeros out) by table (rope_table).  out_q may be q,
+    out_k may be k.  Returns (yq, yk, rinv_q or None, rinv_k or None)."""
+    ldq, ldk = _rows("q", q), _rows("k", k)
+    T, nq, nk, P, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim)
+    if out_q is None:
+        out_q = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+    if out_k is None:
+        out_k = torch.empty(k.shape, device=k.device, dtype=torch.bfloat16)
+    ldyq, ldyk = _rows("out_q", out_q, q.shape), _rows("out_k", out_k, k.shape)
+    if want_rinv or rinv_q is not None:
+        rinv_q = _out("rinv_q", rinv_q, (T, nq), torch.float32, q)
+    if want_rinv or rinv_k is not None:
+        rinv_k = _out("rinv_k", rinv_k, (T, nk), torch.float32, q)
+    _on_device(q, k, gamma_q, gamma_k, positions, table, out_q, out_k, rinv_q, rinv_k)
+    check(lib().nts_qknorm_rope(_ptr(q), ldq, _ptr(gamma_q), _ptr(out_q), ldyq, _ptr(rinv_q),
+                                _ptr(k), ldk, _ptr(gamma_k), _ptr(out_k), ldyk, _ptr(rinv_k),
+                                _ptr(positions), _ptr(table), P, T, nq, nk, int(head_dim), rot,
+                                1 if interleaved else 0, float(eps), _stream(stream)))
+    return out_q, out_k, rinv_q, rinv_k
+
+
+def qknorm_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor,
+                         gamma_q: torch.Tensor, k: torch.Tensor, gamma_k: torch.Tensor,
+                         positions: torch.Tensor, table: torch.Tensor, head_dim: int,
+                         eps: float = 1e-6, interleaved: bool = False,
+                         out_dq: Optional[torch.Tensor] = None,
+                         out_dk: Optional[torch.Tensor] = None,
+                         dgamma_q: Optional[torch.Tensor] = None,
+                         dgamma_k: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of qknorm_rope: dyq and dyk are the gradients of its outputs, q
+    and k its inputs.  out_dq and out_dk may be columns of one packed buffer.
+    Returns (dq, dk, dgamma_q, dgamma_k), the gains' gradients in fp32
+    [head_dim].  Without a workspace (uint8, rope_backward_workspace bytes)
+    one is taken from torch's allocator for the call."""
+    ldq, ldk = _rows("q", q), _rows("k", k)
+    T, nq, nk, P, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim)
+    lddyq, lddyk = _rows("dyq", dyq, q.shape), _rows("dyk", dyk, k.shape)
+    if out_dq is None:
+        out_dq = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+    if out_dk is None:
+        out_dk = torch.empty(k.shape, device=k.device, dtype=torch.bfloat16)
+    lddq, lddk = _rows("out_dq", out_dq, q.shape), _rows("out_dk", out_dk, k.shape)
+    dgamma_q = _out("dgamma_q", dgamma_q, (int(head_dim),), torch.float32, q)
+    dgamma_k = _out("dgamma_k", dgamma_k, (int(head_dim),), torch.float32, q)
+    if workspace is None:
+        workspace = torch.empty(rope_backward_workspace(head_dim), device=q.device,
+                                dtype=torch.uint8)
+        if stream is not None:
+            workspace.record_stream(stream)   # torch may hand it on only after the call has run
+    _need_cuda("workspace", workspace, torch.uint8)
+    _on_device(q, k, dyq, dyk, gamma_q, gamma_k, positions, table, out_dq, out_dk, dgamma_q,
+               dgamma_k, workspace)
+    check(lib().nts_qknorm_rope_backward(
+        _ptr(dyq), lddyq, _ptr(dyk), lddyk, _ptr(q), ldq, _ptr(gamma_q), _ptr(k), ldk,
+        _ptr(gamma_k), _ptr(positions), _ptr(table), P, _ptr(out_dq), lddq, _ptr(out_dk), lddk,
+        _ptr(dgamma_q), _ptr(dgamma_k), _ptr(workspace), workspace.numel(), T, nq, nk,
+        int(head_dim), rot, 1 if interleaved else 0, float(eps), _stream(stream)))
+    return out_dq, out_dk, dgamma_q, dgamma_k
+
+
+def rope_backward_workspace(head_dim: int) -> int:
+    """Workspace bytes of qknorm_rope_backward."""
+    n = ctypes.c_int64()
+    check(lib().nts_qknorm_rope_backward_workspace(int(head_dim), ctypes.byref(n)))
+    return n.value
+
+
+def rmsnorm_blockcast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      codes=None, scales=None, rinv=None, want_rinv: bool = False,
+                      stream=None) -> BlockOut:
+    """RMSNorm of x [T, D] (bf16) fused with the cast to E4M3 codes with an
+    fp32 scale per 128 values: BlockOut(codes [T, D], scales [T, ceil(D/128)],
+    rinv or None)."""
+    _need_cuda("x", x, torch.bfloat16)
+    T, D = x.shape
+    if gamma is not None:
+        _need_cuda("gamma", gamma, torch.float32)
+        if gamma.numel() != D:
+            raise ValueError(f"gamma must hold D = {D} values, got {gamma.numel()}")
+    codes = _out("codes", codes, (T, D), torch.uint8, x)
+    scales = _out("scales", scales, (T, _blocks(D)), torch.float32, x)
+    if want_rinv or rinv is not None:
+        rinv = _out("rinv", rinv, (T,), torch.float32, x)
+    _on_device(x, gamma, codes, scales, rinv)
+    check(lib().nts_rmsnorm_blockcast(_ptr(x), _ptr(gamma), _ptr(codes), _ptr(scales), _ptr(rinv),
+                                      T, D, float(eps), _stream(stream)))
+    return BlockOut(codes, scales, rinv)
+
+
+def blockcast(x: torch.Tensor, block_rows: int = 1, codes=None, scales=None,
+              stream=None) -> BlockOut:
+    """Cast of x [T, D] (bf16) to E4M3 codes with an fp32 scale per block of
+    block_rows x 128 values (1: activations, 128: weights):
+    BlockOut(codes [T, D], scales [ceil(T/block_rows), ceil(D/128)], None)."""
+    _need_cuda("x", x, torch.bfloat16)
+    T, D = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    codes = _out("codes", codes, (T, D), torch.uint8, x)
+    scales = _out("scales", scales, (-(-T // block_rows), _blocks(D)), torch.float32, x)
+    _on_device(x, codes, scales)
+    check(lib().nts_blockcast(_ptr(x), _ptr(codes), _ptr(scales), T, D, int(block_rows),
+                              _stream(stream)))
+    return BlockOut(codes, scales, None)
+
+
+def blockcast_t(x: torch.Tensor, codes=None, scales=None, stream=None) -> BlockOut:
+    """The transpose of x [T, D] (bf16) as E4M3 codes with an fp32 scale per
+    128 tokens of a column: BlockOut(codes [D, Tp], scales [D, ceil(T/128)],
+    None), Tp = T rounded up to a multiple of 16 (zero codes beyond T)."""
+    _need_cuda("x", x, torch.bfloat16)
+    T, D = x.shape
+    codes = _out("codes", codes, (D, -(-T // 16) * 16), torch.uint8, x)
+    scales = _out("scales", scales, (D, _blocks(T)), torch.float32, x)
+    _on_device(x, codes, scales)
+    check(lib().nts_blockcast_t(_ptr(x), _ptr(codes), _ptr(scales), T, D, _stream(stream)))
+    return BlockOut(codes, scales, None)
+
+
+def _codes(name: str, t: torch.Tensor) -> torch.Tensor:
+    if t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    _need_cuda(name, t, torch.uint8)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t
+
+
+def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
+                     w_scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """Y = A W^T of E4M3 operands (uint8 or float8_e4m3fn) with an fp32 scale
+    per 128 values along K: a_codes [M, K] with a_scales [M, ceil(K/128)],
+    w_codes [N, K] with w_scales [ceil(N/128), ceil(K/128)] (128 x 128 blocks)
+    or [N, ceil(K/128)].  Returns Y [M, N], bf16 or fp32."""
+    a_codes, w_codes = _codes("a_codes", a_codes), _codes("w_codes", w_codes)
+    M, K = a_codes.shape
+    N, Kw = w_codes.shape
+    if Kw != K:
+        raise ValueError("a_codes and w_codes must have the same K")
+    _need_cuda("a_scales", a_scales, torch.float32)
+    _need_cuda("w_scales", w_scales, torch.float32)
+    if tuple(a_scales.shape) != (M, _blocks(K)):
+        raise ValueError(f"a_scales must have shape {(M, _blocks(K))}, got {tuple(a_scales.shape)}")
+    if tuple(w_scales.shape) == (_blocks(N), _blocks(K)):
+        rows = 128
+    elif tuple(w_scales.shape) == (N, _blocks(K)):
+        rows = 1
+    else:
+        raise ValueError(f"w_scales must have shape {(_blocks(N), _blocks(K))} or "
+                         f"{(N, _blocks(K))}, got {tuple(w_scales.shape)}")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
+    out = _out("out", out, (M, N), out_dtype, a_codes)
+    _on_device(a_codes, a_scales, w_codes, w_scales, out)
+    check(lib().nts_gemm_blockscaled(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
+                                     _ptr(w_scales), rows, _ptr(out),
+                                     1 if out_dtype == torch.float32 else 0, M, N, K,
+                                     _stream(stream)))
+    return out
+
+
 def mxnorm_correction(B: int, p: int) -> float:
     c = ctypes.c_double()
     check(lib().nts_mxnorm_correction(int(B), int(p), ctypes.byref(c)))
