@@ -74,6 +74,10 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
 
 constexpr int kWideThreads = 384;     // TMA, MMA, 2 scale warps, 8 epilogue warps
 constexpr int kGroupM = 16;           // tiles of A walked before the next tile of W
+// Registers per thread at BN = 256, whose epilogue holds 128 sums and 64
+// loaded values per thread: 168 at launch, then 40 in the four other warps and
+// 232 in the epilogue's eight (128 * 40 + 256 * 232 = 384 * 168).
+constexpr int kWideRegs = 168, kWideRegsDown = 40, kWideRegsUp = 232;
 
 template <int BN, bool ROWS>
 struct Wide {
@@ -143,145 +147,154 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   allow_dependent_launch();
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      int64_t n = 0;   // stages issued
-      bool ok = true;
+  if (warp < 4) {
+    if (BN == 256) registers_down<kWideRegsDown>();
+    if (warp == 0) {
+      if (lane == 0) {
+        RingSlot<S> st;
+        int64_t n = 0;   // stages issued
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+          int tm, tn;
+          tile_at(p, tile, &tm, &tn);
+          for (int kb = 0; kb < p.kblocks; ++kb, ++n, st.advance()) {
+            if (n >= S &&
+                !mbar_wait_or_stop(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
+              ok = false;
+              break;
+            }
+            const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+            mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
+            tma_load_2d(at, &map_a, kb * 128, tm * 128, bar);
+            tma_load_2d(at + C::kA, &map_w, kb * 128, tn * BN, bar);
+          }
+        }
+        if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+        *issued = n;
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        constexpr uint32_t instr = e4m3_instr(128, BN);
+        RingSlot<S> st;
+        RingSlot<NB> tb;
+        bool ok = true, filled = false;   // filled: every buffer was used once
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+          for (int kb = 0; kb < p.kblocks; ++kb, st.advance()) {
+            if (!mbar_wait_or_stop(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
+                (filled &&
+                 !mbar_wait_or_stop(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after();
+            const uint64_t da = operand_desc(sbase + st.i * C::kStage);
+            const uint64_t dw = operand_desc(sbase + st.i * C::kStage + C::kA);
+  #pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3(tmem + tb.i * BN, da + 2 * k, dw + 2 * k, instr, k > 0);
+            mma_commit(empty + 8 * st.i);
+            mma_commit(tfull + 8 * tb.i);
+            filled |= tb.i == NB - 1;
+            tb.advance();
+          }
+        }
+        if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+      }
+    } else if (warp < 4) {
+      // scale warps: lanes 8 r .. 8 r + 7 read the eight scales of a row
+      const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
+      RingSlot<kPieces> pc;
+      bool ok = true, filled = false;
       for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
-        for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
-          const int s = (int)(n % S);
-          if (n >= S && !mbar_wait_or_stop(empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u,
-                                           p.wait_limit_ns, stop)) {
+        for (int k0 = 0; k0 < p.kblocks; k0 += kChunk) {
+          if (filled &&
+              !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sempty + 8 * pc.i, pc.parity ^ 1u,
+                                                         p.wait_limit_ns, stop))) {
             ok = false;
             break;
           }
-          const uint32_t at = sbase + s * C::kStage;
-          mbar_arrive_expect_tx(full + 8 * s, C::kStage + (n == 0 ? p.missing_tx : 0u));
-          tma_load_2d(at, &map_a, kb * 128, tm * 128, full + 8 * s);
-          tma_load_2d(at + C::kA, &map_w, kb * 128, tn * BN, full + 8 * s);
-        }
-      }
-      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
-      *issued = n;
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t instr = e4m3_instr(128, BN);
-      int64_t n = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
-          const int s = (int)(n % S), b = (int)(n % NB);
-          if (!mbar_wait_or_stop(full + 8 * s, (uint32_t)((n / S) & 1), p.wait_limit_ns, stop) ||
-              (n >= NB && !mbar_wait_or_stop(tempty + 8 * b, (uint32_t)((n / NB) & 1) ^ 1u,
-                                             p.wait_limit_ns, stop))) {
-            ok = false;
-            break;
+          float* dst = scales + (pc.i * kChunk + kl) * C::kScales;
+          const bool in = k0 + kl < p.kblocks;
+          const float* sa = p.sa + (int64_t)tm * 128 * p.kblocks + k0 + kl;
+          const int rows = (int)min64(128, p.M - (int64_t)tm * 128);
+  #pragma unroll 4
+          for (int r = sub; r < 128; r += 8)
+            dst[r] = in && r < rows ? __ldg(sa + (int64_t)r * p.kblocks) : 0.f;
+          if (ROWS) {
+            const float* sw = p.sw + (int64_t)tn * BN * p.kblocks + k0 + kl;
+            const int cols = (int)min64(BN, p.N - (int64_t)tn * BN);
+  #pragma unroll 4
+            for (int r = sub; r < BN; r += 8)
+              dst[128 + r] = in && r < cols ? __ldg(sw + (int64_t)r * p.kblocks) : 0.f;
+          } else if (sub < BN / 128) {
+            const int64_t w = (int64_t)tn * (BN / 128) + sub;
+            dst[128 + sub] = in && w * 128 < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
           }
-          tcgen05_fence_after();
-          const uint64_t da = operand_desc(sbase + s * C::kStage);
-          const uint64_t dw = operand_desc(sbase + s * C::kStage + C::kA);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3(tmem + b * BN, da + 2 * k, dw + 2 * k, instr, k > 0);
-          mma_commit(empty + 8 * s);
-          mma_commit(tfull + 8 * b);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull + 8 * pc.i);
+          filled |= pc.i == kPieces - 1;
+          pc.advance();
         }
       }
-      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
-    }
-  } else if (warp < 4) {
-    // scale warps: lanes 8 r .. 8 r + 7 read the eight scales of a row
-    const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
-    int64_t n = 0;   // pieces staged
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      int tm, tn;
-      tile_at(p, tile, &tm, &tn);
-      bool ok = true;
-      for (int k0 = 0; k0 < p.kblocks; k0 += kChunk, ++n) {
-        const int c = (int)(n % kPieces);
-        if (n >= kPieces &&
-            !__all_sync(0xFFFFFFFFu,
-                        mbar_wait_or_stop(sempty + 8 * c, (uint32_t)((n / kPieces) & 1) ^ 1u,
-                                          p.wait_limit_ns, stop))) {
-          ok = false;
-          break;
-        }
-        float* dst = scales + (c * kChunk + kl) * C::kScales;
-        const bool in = k0 + kl < p.kblocks;
-#pragma unroll 8
-        for (int r = sub; r < 128; r += 8) {
-          const int64_t m = (int64_t)tm * 128 + r;
-          dst[r] = in && m < p.M ? __ldg(p.sa + m * p.kblocks + k0 + kl) : 0.f;
-        }
-        if (ROWS) {
-#pragma unroll 8
-          for (int r = sub; r < BN; r += 8) {
-            const int64_t w = (int64_t)tn * BN + r;
-            dst[128 + r] = in && w < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
-          }
-        } else if (sub < BN / 128) {
-          const int64_t w = (int64_t)tn * (BN / 128) + sub;
-          dst[128 + sub] = in && w * 128 < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull + 8 * c);
-      }
-      if (!ok) break;
     }
   } else {
+    if (BN == 256) registers_up<kWideRegsUp>();
     // epilogue warps: four cover the 128 rows, two such groups the BN columns
-    constexpr int COLS = BN / 2;
+    constexpr int COLS = BN / 2, LD = BN == 256 ? 32 : 16;
     const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
     const int wblock = ROWS ? group * COLS : group * COLS / 128;
-    int64_t n = 0, piece = 0;
+    RingSlot<NB> tb;
+    RingSlot<kPieces> pc;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       int tm, tn;
       tile_at(p, tile, &tm, &tn);
-      float acc[COLS];
+      uint64_t acc[COLS / 2];   // pairs of columns
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
       bool ok = true;
-      for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
-        const int b = (int)(n % NB);
-        const int c = (int)(piece % kPieces);
+      for (int kb = 0; kb < p.kblocks; ++kb, tb.advance()) {
         if ((kb % kChunk == 0 &&
-             !__all_sync(0xFFFFFFFFu,
-                         mbar_wait_or_stop(sfull + 8 * c, (uint32_t)((piece / kPieces) & 1),
-                                           p.wait_limit_ns, stop))) ||
-            !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * b, (uint32_t)((n / NB) & 1),
+             !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sfull + 8 * pc.i, pc.parity,
+                                                        p.wait_limit_ns, stop))) ||
+            !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * tb.i, tb.parity,
                                                        p.wait_limit_ns, stop))) {
           ok = false;
           break;
         }
         tcgen05_fence_after();
-        const float* sc = scales + (c * kChunk + kb % kChunk) * C::kScales;
+        const uint32_t at = tmem + tb.i * BN + group * COLS + lanes;
+        uint32_t v[2][LD];
+        tmem_load(v[0], at);
+        const float* sc = scales + (pc.i * kChunk + kb % kChunk) * C::kScales;
         const float s = ROWS ? sc[row] : sc[row] * sc[128 + wblock];
-        const uint32_t at = tmem + b * BN + group * COLS + lanes;
-        uint32_t v[2][16];
-        tmem_load16(v[0], at);
+        const uint64_t ss = f2(s, s);
 #pragma unroll
-        for (int j = 0; j < COLS / 16; ++j) {
-          tmem_wait16(v[j & 1]);
-          if (j + 1 < COLS / 16) tmem_load16(v[(j + 1) & 1], at + 16 * (j + 1));
+        for (int j = 0; j < COLS / LD; ++j) {
+          tmem_wait(v[j & 1]);
+          if (j + 1 < COLS / LD) {
+            tmem_load(v[(j + 1) & 1], at + LD * (j + 1));
+          } else {   // the buffer is in registers: the next block's product may start
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty + 8 * tb.i);
+          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float w = ROWS ? s * sc[128 + wblock + 16 * j + i] : s;
-            acc[16 * j + i] = fmaf(__uint_as_float(v[j & 1][i]), w, acc[16 * j + i]);
+          for (int i = 0; i < LD / 2; ++i) {
+            uint64_t x = f2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1]));
+            if (ROWS)
+              x = f2_mul(x, *reinterpret_cast<const uint64_t*>(sc + 128 + wblock + LD * j + 2 * i));
+            acc[LD / 2 * j + i] = f2_fma(x, ss, acc[LD / 2 * j + i]);
           }
         }
-        tcgen05_fence_before();
-        __syncwarp();
-        const bool last = kb % kChunk == kChunk - 1 || kb == p.kblocks - 1;
-        if (lane == 0) {
-          mbar_arrive(tempty + 8 * b);
-          if (last) mbar_arrive(sempty + 8 * c);
+        if (kb % kChunk == kChunk - 1 || kb == p.kblocks - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty + 8 * pc.i);
+          pc.advance();
         }
-        if (last) ++piece;
       }
       if (!ok) {
         if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
@@ -290,37 +303,40 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       const int64_t m = (int64_t)tm * 128 + row;
       const int64_t n0 = (int64_t)tn * BN + group * COLS;
       if (m < p.M) {
+        const int cols = (int)min64(COLS, p.N - n0);   // may be <= 0
         if (p.fp32_out) {
           float* y = static_cast<float*>(p.y) + m * p.N + n0;
 #pragma unroll
           for (int j = 0; j < COLS; j += 8) {
-            if (p.vec_out && n0 + j + 8 <= p.N)
-              st_global_v8(y + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
-                           __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]),
-                           __float_as_uint(acc[j + 4]), __float_as_uint(acc[j + 5]),
-                           __float_as_uint(acc[j + 6]), __float_as_uint(acc[j + 7]));
+            const uint64_t* a = acc + j / 2;
+            if (p.vec_out && j + 8 <= cols)
+              st_global_v8(y + j, (uint32_t)a[0], (uint32_t)(a[0] >> 32), (uint32_t)a[1],
+                           (uint32_t)(a[1] >> 32), (uint32_t)a[2], (uint32_t)(a[2] >> 32),
+                           (uint32_t)a[3], (uint32_t)(a[3] >> 32));
             else
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (n0 + j + i < p.N) y[j + i] = acc[j + i];
+                if (j + i < cols) y[j + i] = i & 1 ? f2_hi(a[i / 2]) : f2_lo(a[i / 2]);
           }
         } else {
           __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + m * p.N + n0;
 #pragma unroll
           for (int j = 0; j < COLS; j += 16) {
-            if (p.vec_out && n0 + j + 16 <= p.N)
-              st_global_v8(y + j, pack_bf16x2_rn(acc[j], acc[j + 1]),
-                           pack_bf16x2_rn(acc[j + 2], acc[j + 3]),
-                           pack_bf16x2_rn(acc[j + 4], acc[j + 5]),
-                           pack_bf16x2_rn(acc[j + 6], acc[j + 7]),
-                           pack_bf16x2_rn(acc[j + 8], acc[j + 9]),
-                           pack_bf16x2_rn(acc[j + 10], acc[j + 11]),
-                           pack_bf16x2_rn(acc[j + 12], acc[j + 13]),
-                           pack_bf16x2_rn(acc[j + 14], acc[j + 15]));
+            const uint64_t* a = acc + j / 2;
+            if (p.vec_out && j + 16 <= cols)
+              st_global_v8(y + j, pack_bf16x2_rn(f2_lo(a[0]), f2_hi(a[0])),
+                           pack_bf16x2_rn(f2_lo(a[1]), f2_hi(a[1])),
+                           pack_bf16x2_rn(f2_lo(a[2]), f2_hi(a[2])),
+                           pack_bf16x2_rn(f2_lo(a[3]), f2_hi(a[3])),
+                           pack_bf16x2_rn(f2_lo(a[4]), f2_hi(a[4])),
+                           pack_bf16x2_rn(f2_lo(a[5]), f2_hi(a[5])),
+                           pack_bf16x2_rn(f2_lo(a[6]), f2_hi(a[6])),
+                           pack_bf16x2_rn(f2_lo(a[7]), f2_hi(a[7])));
             else
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (n0 + j + i < p.N) y[j + i] = __float2bfloat16_rn(acc[j + i]);
+                if (j + i < cols)
+                  y[j + i] = __float2bfloat16_rn(i & 1 ? f2_hi(a[i / 2]) : f2_lo(a[i / 2]));
           }
         }
       }
@@ -343,12 +359,12 @@ constexpr int kNarrowThreads = 256;   // TMA, MMA, 2 scale warps, 4 epilogue war
 
 template <int TN, bool ROWS>
 struct Narrow {
-  static constexpr int kBufs = 4;
+  static constexpr int kBufs = 4;                         // two CTAs share an SM's 512 columns
   static constexpr uint32_t kBufCols = TN < 32 ? 32 : TN;
   static constexpr uint32_t kCols = kBufCols * kBufs;
   static constexpr uint32_t kW = 128 * 128;
   static constexpr uint32_t kStage = kW + TN * 128;
-  static constexpr int kStages = 196608 / (int)kStage;    // 6 (TN = 128) to 10 (TN = 16)
+  static constexpr int kStages = 98304 / (int)kStage;     // 4 (TN = 64) or 5
   static constexpr int kScales = TN + (ROWS ? 128 : 4);
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
@@ -358,7 +374,7 @@ struct Narrow {
 };
 
 template <int TN, bool ROWS>
-__global__ void __launch_bounds__(kNarrowThreads, 1)
+__global__ void __launch_bounds__(kNarrowThreads, 2)
 narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
               const GemmParams p) {
   using C = Narrow<TN, ROWS>;
@@ -413,19 +429,18 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   float acc[TN];
   if (warp == 0) {
     if (lane == 0) {
+      RingSlot<S> st;
       bool ok = true;
       int n = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int s = n % S;
-        if (n >= S && !mbar_wait_or_stop(empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u,
-                                         p.wait_limit_ns, stop)) {
+      for (int kb = kb0; kb < kb1; ++kb, ++n, st.advance()) {
+        if (n >= S && !mbar_wait_or_stop(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
           ok = false;
           break;
         }
-        const uint32_t at = sbase + s * C::kStage;
-        mbar_arrive_expect_tx(full + 8 * s, C::kStage + (n == 0 ? p.missing_tx : 0u));
-        tma_load_2d(at, &map_w, kb * 128, tn * 128, full + 8 * s);
-        tma_load_2d(at + C::kW, &map_a, kb * 128, tm * TN, full + 8 * s);
+        const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+        mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
+        tma_load_2d(at, &map_w, kb * 128, tn * 128, bar);
+        tma_load_2d(at + C::kW, &map_a, kb * 128, tm * TN, bar);
       }
       if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
       *issued = n;
@@ -433,38 +448,36 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t instr = e4m3_instr(128, TN);
+      RingSlot<S> st;
+      RingSlot<NB> tb;
       bool ok = true;
-      int n = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int s = n % S, b = n % NB;
-        if (!mbar_wait_or_stop(full + 8 * s, (uint32_t)((n / S) & 1), p.wait_limit_ns, stop) ||
-            (n >= NB && !mbar_wait_or_stop(tempty + 8 * b, (uint32_t)((n / NB) & 1) ^ 1u,
-                                           p.wait_limit_ns, stop))) {
+      for (int n = 0; n < kb1 - kb0; ++n, st.advance(), tb.advance()) {
+        if (!mbar_wait_or_stop(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
+            (n >= NB &&
+             !mbar_wait_or_stop(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
           ok = false;
           break;
         }
         tcgen05_fence_after();
-        const uint64_t dw = operand_desc(sbase + s * C::kStage);
-        const uint64_t da = operand_desc(sbase + s * C::kStage + C::kW);
+        const uint64_t dw = operand_desc(sbase + st.i * C::kStage);
+        const uint64_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_e4m3(tmem + b * C::kBufCols, dw + 2 * k, da + 2 * k, instr, k > 0);
-        mma_commit(empty + 8 * s);
-        mma_commit(tfull + 8 * b);
+          mma_e4m3(tmem + tb.i * C::kBufCols, dw + 2 * k, da + 2 * k, instr, k > 0);
+        mma_commit(empty + 8 * st.i);
+        mma_commit(tfull + 8 * tb.i);
       }
       if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
     }
   } else if (warp < 4) {
     const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
-    int n = 0;
-    for (int k0 = kb0; k0 < kb1; k0 += kChunk, ++n) {
-      const int c = n % kPieces;
-      if (n >= kPieces &&
-          !__all_sync(0xFFFFFFFFu,
-                      mbar_wait_or_stop(sempty + 8 * c, (uint32_t)((n / kPieces) & 1) ^ 1u,
-                                        p.wait_limit_ns, stop)))
+    RingSlot<kPieces> pc;
+    for (int k0 = kb0; k0 < kb1; k0 += kChunk, pc.advance()) {
+      if (k0 - kb0 >= kPieces * kChunk &&
+          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sempty + 8 * pc.i, pc.parity ^ 1u,
+                                                     p.wait_limit_ns, stop)))
         break;
-      float* dst = scales + (c * kChunk + kl) * C::kScales;
+      float* dst = scales + (pc.i * kChunk + kl) * C::kScales;
       const bool in = k0 + kl < kb1;
 #pragma unroll 8
       for (int r = sub; r < TN; r += 8) {
@@ -481,35 +494,34 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         dst[TN] = in ? __ldg(p.sw + (int64_t)tn * p.kblocks + k0 + kl) : 0.f;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(sfull + 8 * c);
+      if (lane == 0) mbar_arrive(sfull + 8 * pc.i);
     }
   } else {
     const int row = (warp & 3) * 32 + lane;   // of W
     const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[j] = 0.f;
-    int n = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++n) {
-      const int b = n % NB, piece = n / kChunk, c = piece % kPieces;
+    RingSlot<NB> tb;
+    RingSlot<kPieces> pc;
+    for (int n = 0; n < kb1 - kb0; ++n, tb.advance()) {
       if ((n % kChunk == 0 &&
-           !__all_sync(0xFFFFFFFFu,
-                       mbar_wait_or_stop(sfull + 8 * c, (uint32_t)((piece / kPieces) & 1),
-                                         p.wait_limit_ns, stop))) ||
-          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * b, (uint32_t)((n / NB) & 1),
-                                                     p.wait_limit_ns, stop))) {
+           !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns,
+                                                      stop))) ||
+          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns,
+                                                     stop))) {
         if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
         break;
       }
       tcgen05_fence_after();
-      const float* sc = scales + (c * kChunk + n % kChunk) * C::kScales;
+      const float* sc = scales + (pc.i * kChunk + n % kChunk) * C::kScales;
       const float sw = sc[TN + (ROWS ? row : 0)];
-      const uint32_t at = tmem + b * C::kBufCols + lanes;
+      const uint32_t at = tmem + tb.i * C::kBufCols + lanes;
       uint32_t v[2][16];
-      tmem_load16(v[0], at);
+      tmem_load(v[0], at);
 #pragma unroll
       for (int j = 0; j < TN / 16; ++j) {
-        tmem_wait16(v[j & 1]);
-        if (j + 1 < TN / 16) tmem_load16(v[(j + 1) & 1], at + 16 * (j + 1));
+        tmem_wait(v[j & 1]);
+        if (j + 1 < TN / 16) tmem_load(v[(j + 1) & 1], at + 16 * (j + 1));
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           acc[16 * j + i] =
@@ -518,9 +530,10 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(tempty + 8 * b);
-        if (n % kChunk == kChunk - 1) mbar_arrive(sempty + 8 * c);
+        mbar_arrive(tempty + 8 * tb.i);
+        if (n % kChunk == kChunk - 1) mbar_arrive(sempty + 8 * pc.i);
       }
+      if (n % kChunk == kChunk - 1) pc.advance();
     }
   }
   __syncwarp();
@@ -602,12 +615,21 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int bo
 }
 
 int launch(GemmKernel kern, const GemmRequest& rq, const GemmParams& p, int box_a, int box_w,
-           dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, bool pdl) {
+           dim3 grid, int threads, int regs, size_t smem, int cluster, cudaStream_t stream,
+           bool pdl) {
   CUtensorMap map_a, map_w;
   int rc = make_map(&map_a, rq.A, rq.M, rq.K, box_a);
   if (rc == NTS_OK) rc = make_map(&map_w, rq.W, rq.N, rq.K, box_w);
   if (rc == NTS_OK) rc = prepare_kernel((const void*)kern, smem);
   if (rc != NTS_OK) return rc;
+  if (regs > 0) {   // the split of the registers presumes what the CTA is launched with
+    int have = 0;
+    rc = kernel_registers((const void*)kern, &have);
+    if (rc != NTS_OK) return rc;
+    if (have != regs)
+      return fail(NTS_ERR_UNSUPPORTED, "the product's kernel was built with %d registers, not %d",
+                  have, regs);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   int na = 0;
@@ -634,7 +656,7 @@ int launch_narrow(const GemmRequest& rq, const GemmParams& p, cudaStream_t strea
                   const DeviceInfo& dev, const LaunchTuning& tune) {
   const int64_t tiles_n = (p.N + 127) / 128, tiles_m = (p.M + TN - 1) / TN;
   int split = 1;
-  while (split < 8 && 2 * split <= p.kblocks && tiles_n * tiles_m * split * 2 <= dev.sm_count)
+  while (split < 8 && 4 * split <= p.kblocks && tiles_n * tiles_m * split <= dev.sm_count)
     split *= 2;
   const int64_t gx = tiles_n * split;
   if (gx > 0x7fffffffll || tiles_m > 65535)
@@ -643,9 +665,9 @@ int launch_narrow(const GemmRequest& rq, const GemmParams& p, cudaStream_t strea
              (long long)p.N, (long long)rq.K, TN, split);
   const dim3 grid((unsigned)gx, (unsigned)tiles_m);
   return rq.w_rows == 1
-             ? launch(narrow_kernel<TN, true>, rq, p, TN, 128, grid, kNarrowThreads,
+             ? launch(narrow_kernel<TN, true>, rq, p, TN, 128, grid, kNarrowThreads, 0,
                       Narrow<TN, true>::kLaunch, split, stream, tune.pdl != 0)
-             : launch(narrow_kernel<TN, false>, rq, p, TN, 128, grid, kNarrowThreads,
+             : launch(narrow_kernel<TN, false>, rq, p, TN, 128, grid, kNarrowThreads, 0,
                       Narrow<TN, false>::kLaunch, split, stream, tune.pdl != 0);
 }
 
@@ -656,12 +678,13 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
   p.tiles_n = (int)((p.N + BN - 1) / BN);
   const unsigned grid =
       (unsigned)std::min<int64_t>((int64_t)p.tiles_m * p.tiles_n, dev.sm_count);
+  const int regs = BN == 256 ? kWideRegs : 0;
   log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide BN=%d grid=%u", (long long)p.M,
              (long long)p.N, (long long)rq.K, BN, grid);
   return rq.w_rows == 1
-             ? launch(wide_kernel<BN, true>, rq, p, 128, BN, dim3(grid), kWideThreads,
+             ? launch(wide_kernel<BN, true>, rq, p, 128, BN, dim3(grid), kWideThreads, regs,
                       Wide<BN, true>::kLaunch, 0, stream, tune.pdl != 0)
-             : launch(wide_kernel<BN, false>, rq, p, 128, BN, dim3(grid), kWideThreads,
+             : launch(wide_kernel<BN, false>, rq, p, 128, BN, dim3(grid), kWideThreads, regs,
                       Wide<BN, false>::kLaunch, 0, stream, tune.pdl != 0);
 }
 
@@ -685,8 +708,7 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.missing_tx = tune.missing_tx;
   if (p.M <= 16) return launch_narrow<16>(rq, p, stream, dev, tune);
   if (p.M <= 32) return launch_narrow<32>(rq, p, stream, dev, tune);
-  if (p.M <= 64) return launch_narrow<64>(rq, p, stream, dev, tune);
-  if (p.M <= 128) return launch_narrow<128>(rq, p, stream, dev, tune);
+  if (p.M <= 128) return launch_narrow<64>(rq, p, stream, dev, tune);
   const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 255) / 256);
   return tiles >= dev.sm_count ? launch_wide<256>(rq, p, stream, dev, tune)
                                : launch_wide<128>(rq, p, stream, dev, tune);

@@ -148,6 +148,24 @@ int kernel_registers(const void* kernel, int* regs) {
   return NTS_OK;
 }
 
+int blocks_per_sm(const void* kernel, int threads, size_t smem, int* out) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, size_t>, int> cache;
+  const int dev = device_info().device;
+  std::lock_guard<std::mutex> lk(mu);
+  auto key = std::make_tuple(kernel, dev, threads, smem);
+  auto it = cache.find(key);
+  if (it == cache.end()) {
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e != cudaSuccess) return fail_cuda(e, "occupancy query");
+    if (n < 1) return fail(NTS_ERR_UNSUPPORTED, "the kernel does not fit on an SM");
+    it = cache.emplace(key, n).first;
+  }
+  *out = it->second;
+  return NTS_OK;
+}
+
 int max_active_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster,
                         int64_t* out) {
   static std::mutex mu;

@@ -89,6 +89,8 @@ RowShape choose_row_shape(int nvec, int force_vpt);
 int prepare_kernel(const void* kernel, size_t smem);
 // Registers per thread of a kernel (cached per device).
 int kernel_registers(const void* kernel, int* regs);
+// CTAs of this kernel that fit an SM (cached per device).
+int blocks_per_sm(const void* kernel, int threads, size_t smem, int* out);
 // Co-resident clusters of `cluster` CTAs for this launch configuration.
 int max_active_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster,
                         int64_t* out);

@@ -6,6 +6,7 @@ and the current CUDA stream through the C ABI.  Names follow the C ABI
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -303,57 +304,86 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _on_device(first: torch.Tensor, *others) -> None:
-    """The kernels run on the current device: every tensor has to live there."""
-    dev = torch.cuda.current_device()
-    for t in (first, *others):
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+# These calls serve single tokens too, where the host's share of a call is the
+# larger one, so each tensor is looked at once: type, device, layout, address.
+
+def _device(name: str, t: torch.Tensor) -> int:
+    """The current device's index; t has to live there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _out(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor) -> torch.Tensor:
+def _refuse(name: str, t: torch.Tensor, dtype, dev: int) -> None:
+    _need_cuda(name, t, dtype)
+    raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _flat(name: str, t: torch.Tensor, dtype, dev: int) -> int:
+    """Address of a contiguous tensor on the call's device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, dev)
+    return t.data_ptr()
+
+
+def _out(name: str, t: Optional[torch.Tensor], shape: tuple, dtype, dev: int) -> torch.Tensor:
     """The caller's output buffer, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, device=like.device, dtype=dtype)
-    _need_cuda(name, t, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return torch.empty(shape, device=dev, dtype=dtype)
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t
 
 
-def _rows(name: str, t: torch.Tensor, shape=None) -> int:
+def _rows(name: str, t: torch.Tensor, dev: int, shape=None) -> int:
     """Row stride of a bf16 matrix whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be a matrix of shape "
-                         f"{'[T, heads * head_dim]' if shape is None else tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(name, t, torch.bfloat16, dev)
+    if shape is None and t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix [T, heads * head_dim], got {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H = t.shape
+    row, col = t.stride()
+    if col != 1 and H > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return row if T > 1 else H
 
 
-def _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim):
-    """Checks what a rotation and its gradient share; (T, nheads_q, nheads_k, P, rot_dim)."""
-    d = int(head_dim)
-    if d <= 0 or q.shape[1] % d != 0 or k.shape[1] % d != 0:
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _raw_stream(stream, dev: int) -> int:
+        return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+else:
+    def _raw_stream(stream, dev: int) -> int:
+        return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _rope_args(q, k, gamma_q, gamma_k, positions, table, d, dev):
+    """What a rotation and its gradient share, checked: (gamma_q's, gamma_k's,
+    positions' and table's addresses, P, T, nheads_q, nheads_k, rot_dim)."""
+    T, hq = q.shape
+    Tk, hk = k.shape
+    if d <= 0 or hq % d != 0 or hk % d != 0:
         raise ValueError("q and k must hold whole heads of head_dim values")
-    if k.shape[0] != q.shape[0]:
+    if Tk != T:
         raise ValueError("q and k must have the same number of tokens")
-    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
-        _need_cuda(name, g, torch.float32)
-        if g.numel() != d:
-            raise ValueError(f"{name} must hold head_dim = {d} values, got {g.numel()}")
-    _need_cuda("positions", positions, torch.int64)
-    if positions.numel() != q.shape[0]:
-        raise ValueError("positions must hold one position per token")
-    _need_cuda("table", table, torch.float32)
     if table.dim() != 2:
         raise ValueError("table must be a matrix [P, rot_dim]")
-    return q.shape[0], q.shape[1] // d, k.shape[1] // d, table.shape[0], table.shape[1]
+    P, rot = table.shape
+    gq = _flat("gamma_q", gamma_q, torch.float32, dev)
+    gk = _flat("gamma_k", gamma_k, torch.float32, dev)
+    if gamma_q.numel() != d or gamma_k.numel() != d:
+        raise ValueError(f"gamma_q and gamma_k must hold head_dim = {d} values")
+    pos = _flat("positions", positions, torch.int64, dev)
+    if positions.numel() != T:
+        raise ValueError("positions must hold one position per token")
+    return gq, gk, pos, _flat("table", table, torch.float32, dev), P, T, hq // d, hk // d, rot
 
 
 def rope_table(P: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -375,22 +405,28 @@ def qknorm_rope(q: torch.Tensor, gamma_q: torch.Tensor, k: torch.Tensor, gamma_k
     buffer) with the rotary position embedding of positions (int64 [T],
     negative: padding row, zeros out) by table (rope_table).  out_q may be q,
     out_k may be k.  Returns (yq, yk, rinv_q or None, rinv_k or None)."""
-    ldq, ldk = _rows("q", q), _rows("k", k)
-    T, nq, nk, P, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim)
+    d = int(head_dim)
+    dev = _device("q", q)
+    ldq, ldk = _rows("q", q, dev), _rows("k", k, dev)
+    gq, gk, pos, tab, P, T, nq, nk, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, d,
+                                                     dev)
     if out_q is None:
-        out_q = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+        out_q, ldyq = torch.empty((T, nq * d), device=dev, dtype=torch.bfloat16), nq * d
+    else:
+        ldyq = _rows("out_q", out_q, dev, q.shape)
     if out_k is None:
-        out_k = torch.empty(k.shape, device=k.device, dtype=torch.bfloat16)
-    ldyq, ldyk = _rows("out_q", out_q, q.shape), _rows("out_k", out_k, k.shape)
+        out_k, ldyk = torch.empty((T, nk * d), device=dev, dtype=torch.bfloat16), nk * d
+    else:
+        ldyk = _rows("out_k", out_k, dev, k.shape)
     if want_rinv or rinv_q is not None:
-        rinv_q = _out("rinv_q", rinv_q, (T, nq), torch.float32, q)
+        rinv_q = _out("rinv_q", rinv_q, (T, nq), torch.float32, dev)
     if want_rinv or rinv_k is not None:
-        rinv_k = _out("rinv_k", rinv_k, (T, nk), torch.float32, q)
-    _on_device(q, k, gamma_q, gamma_k, positions, table, out_q, out_k, rinv_q, rinv_k)
-    check(lib().nts_qknorm_rope(_ptr(q), ldq, _ptr(gamma_q), _ptr(out_q), ldyq, _ptr(rinv_q),
-                                _ptr(k), ldk, _ptr(gamma_k), _ptr(out_k), ldyk, _ptr(rinv_k),
-                                _ptr(positions), _ptr(table), P, T, nq, nk, int(head_dim), rot,
-                                1 if interleaved else 0, float(eps), _stream(stream)))
+        rinv_k = _out("rinv_k", rinv_k, (T, nk), torch.float32, dev)
+    check(lib().nts_qknorm_rope(
+        q.data_ptr(), ldq, gq, out_q.data_ptr(), ldyq,
+        None if rinv_q is None else rinv_q.data_ptr(), k.data_ptr(), ldk, gk, out_k.data_ptr(),
+        ldyk, None if rinv_k is None else rinv_k.data_ptr(), pos, tab, P, T, nq, nk, d, rot,
+        1 if interleaved else 0, eps, _raw_stream(stream, dev)))
     return out_q, out_k, rinv_q, rinv_k
 
 
@@ -408,32 +444,36 @@ def qknorm_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor,
     Returns (dq, dk, dgamma_q, dgamma_k), the gains' gradients in fp32
     [head_dim].  Without a workspace (uint8, rope_backward_workspace bytes)
     one is taken from torch's allocator for the call."""
-    ldq, ldk = _rows("q", q), _rows("k", k)
-    T, nq, nk, P, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, head_dim)
-    lddyq, lddyk = _rows("dyq", dyq, q.shape), _rows("dyk", dyk, k.shape)
+    d = int(head_dim)
+    dev = _device("q", q)
+    ldq, ldk = _rows("q", q, dev), _rows("k", k, dev)
+    gq, gk, pos, tab, P, T, nq, nk, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, d,
+                                                     dev)
+    lddyq, lddyk = _rows("dyq", dyq, dev, q.shape), _rows("dyk", dyk, dev, k.shape)
     if out_dq is None:
-        out_dq = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+        out_dq, lddq = torch.empty((T, nq * d), device=dev, dtype=torch.bfloat16), nq * d
+    else:
+        lddq = _rows("out_dq", out_dq, dev, q.shape)
     if out_dk is None:
-        out_dk = torch.empty(k.shape, device=k.device, dtype=torch.bfloat16)
-    lddq, lddk = _rows("out_dq", out_dq, q.shape), _rows("out_dk", out_dk, k.shape)
-    dgamma_q = _out("dgamma_q", dgamma_q, (int(head_dim),), torch.float32, q)
-    dgamma_k = _out("dgamma_k", dgamma_k, (int(head_dim),), torch.float32, q)
+        out_dk, lddk = torch.empty((T, nk * d), device=dev, dtype=torch.bfloat16), nk * d
+    else:
+        lddk = _rows("out_dk", out_dk, dev, k.shape)
+    dgamma_q = _out("dgamma_q", dgamma_q, (d,), torch.float32, dev)
+    dgamma_k = _out("dgamma_k", dgamma_k, (d,), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(rope_backward_workspace(head_dim), device=q.device,
-                                dtype=torch.uint8)
+        workspace = torch.empty(rope_backward_workspace(d), device=dev, dtype=torch.uint8)
         if stream is not None:
             workspace.record_stream(stream)   # torch may hand it on only after the call has run
-    _need_cuda("workspace", workspace, torch.uint8)
-    _on_device(q, k, dyq, dyk, gamma_q, gamma_k, positions, table, out_dq, out_dk, dgamma_q,
-               dgamma_k, workspace)
+    ws = _flat("workspace", workspace, torch.uint8, dev)
     check(lib().nts_qknorm_rope_backward(
-        _ptr(dyq), lddyq, _ptr(dyk), lddyk, _ptr(q), ldq, _ptr(gamma_q), _ptr(k), ldk,
-        _ptr(gamma_k), _ptr(positions), _ptr(table), P, _ptr(out_dq), lddq, _ptr(out_dk), lddk,
-        _ptr(dgamma_q), _ptr(dgamma_k), _ptr(workspace), workspace.numel(), T, nq, nk,
-        int(head_dim), rot, 1 if interleaved else 0, float(eps), _stream(stream)))
+        dyq.data_ptr(), lddyq, dyk.data_ptr(), lddyk, q.data_ptr(), ldq, gq, k.data_ptr(), ldk, gk,
+        pos, tab, P, out_dq.data_ptr(), lddq, out_dk.data_ptr(), lddk, dgamma_q.data_ptr(),
+        dgamma_k.data_ptr(), ws, workspace.numel(), T, nq, nk, d, rot, 1 if interleaved else 0, eps,
+        _raw_stream(stream, dev)))
     return out_dq, out_dk, dgamma_q, dgamma_k
 
 
+@functools.lru_cache(maxsize=None)
 def rope_backward_workspace(head_dim: int) -> int:
     """Workspace bytes of qknorm_rope_backward."""
     n = ctypes.c_int64()
@@ -447,19 +487,21 @@ def rmsnorm_blockcast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps
     """RMSNorm of x [T, D] (bf16) fused with the cast to E4M3 codes with an
     fp32 scale per 128 values: BlockOut(codes [T, D], scales [T, ceil(D/128)],
     rinv or None)."""
-    _need_cuda("x", x, torch.bfloat16)
+    dev = _device("x", x)
+    px = _flat("x", x, torch.bfloat16, dev)
     T, D = x.shape
+    pg = None
     if gamma is not None:
-        _need_cuda("gamma", gamma, torch.float32)
+        pg = _flat("gamma", gamma, torch.float32, dev)
         if gamma.numel() != D:
             raise ValueError(f"gamma must hold D = {D} values, got {gamma.numel()}")
-    codes = _out("codes", codes, (T, D), torch.uint8, x)
-    scales = _out("scales", scales, (T, _blocks(D)), torch.float32, x)
+    codes = _out("codes", codes, (T, D), torch.uint8, dev)
+    scales = _out("scales", scales, (T, _blocks(D)), torch.float32, dev)
     if want_rinv or rinv is not None:
-        rinv = _out("rinv", rinv, (T,), torch.float32, x)
-    _on_device(x, gamma, codes, scales, rinv)
-    check(lib().nts_rmsnorm_blockcast(_ptr(x), _ptr(gamma), _ptr(codes), _ptr(scales), _ptr(rinv),
-                                      T, D, float(eps), _stream(stream)))
+        rinv = _out("rinv", rinv, (T,), torch.float32, dev)
+    check(lib().nts_rmsnorm_blockcast(px, pg, codes.data_ptr(), scales.data_ptr(),
+                                      None if rinv is None else rinv.data_ptr(), T, D, eps,
+                                      _raw_stream(stream, dev)))
     return BlockOut(codes, scales, rinv)
 
 
@@ -468,15 +510,15 @@ def blockcast(x: torch.Tensor, block_rows: int = 1, codes=None, scales=None,
     """Cast of x [T, D] (bf16) to E4M3 codes with an fp32 scale per block of
     block_rows x 128 values (1: activations, 128: weights):
     BlockOut(codes [T, D], scales [ceil(T/block_rows), ceil(D/128)], None)."""
-    _need_cuda("x", x, torch.bfloat16)
+    dev = _device("x", x)
+    px = _flat("x", x, torch.bfloat16, dev)
     T, D = x.shape
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
-    codes = _out("codes", codes, (T, D), torch.uint8, x)
-    scales = _out("scales", scales, (-(-T // block_rows), _blocks(D)), torch.float32, x)
-    _on_device(x, codes, scales)
-    check(lib().nts_blockcast(_ptr(x), _ptr(codes), _ptr(scales), T, D, int(block_rows),
-                              _stream(stream)))
+    codes = _out("codes", codes, (T, D), torch.uint8, dev)
+    scales = _out("scales", scales, (-(-T // block_rows), _blocks(D)), torch.float32, dev)
+    check(lib().nts_blockcast(px, codes.data_ptr(), scales.data_ptr(), T, D, block_rows,
+                              _raw_stream(stream, dev)))
     return BlockOut(codes, scales, None)
 
 
@@ -484,22 +526,21 @@ def blockcast_t(x: torch.Tensor, codes=None, scales=None, stream=None) -> BlockO
     """The transpose of x [T, D] (bf16) as E4M3 codes with an fp32 scale per
     128 tokens of a column: BlockOut(codes [D, Tp], scales [D, ceil(T/128)],
     None), Tp = T rounded up to a multiple of 16 (zero codes beyond T)."""
-    _need_cuda("x", x, torch.bfloat16)
+    dev = _device("x", x)
+    px = _flat("x", x, torch.bfloat16, dev)
     T, D = x.shape
-    codes = _out("codes", codes, (D, -(-T // 16) * 16), torch.uint8, x)
-    scales = _out("scales", scales, (D, _blocks(T)), torch.float32, x)
-    _on_device(x, codes, scales)
-    check(lib().nts_blockcast_t(_ptr(x), _ptr(codes), _ptr(scales), T, D, _stream(stream)))
+    codes = _out("codes", codes, (D, -(-T // 16) * 16), torch.uint8, dev)
+    scales = _out("scales", scales, (D, _blocks(T)), torch.float32, dev)
+    check(lib().nts_blockcast_t(px, codes.data_ptr(), scales.data_ptr(), T, D,
+                                _raw_stream(stream, dev)))
     return BlockOut(codes, scales, None)
 
 
-def _codes(name: str, t: torch.Tensor) -> torch.Tensor:
-    if t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    _need_cuda(name, t, torch.uint8)
+def _codes(name: str, t: torch.Tensor, dev: int) -> int:
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    return t
+    return _flat(name, t, torch.float8_e4m3fn if t.dtype is torch.float8_e4m3fn else torch.uint8,
+                 dev)
 
 
 def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
@@ -509,32 +550,32 @@ def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: tor
     per 128 values along K: a_codes [M, K] with a_scales [M, ceil(K/128)],
     w_codes [N, K] with w_scales [ceil(N/128), ceil(K/128)] (128 x 128 blocks)
     or [N, ceil(K/128)].  Returns Y [M, N], bf16 or fp32."""
-    a_codes, w_codes = _codes("a_codes", a_codes), _codes("w_codes", w_codes)
+    dev = _device("a_codes", a_codes)
+    pa, pw = _codes("a_codes", a_codes, dev), _codes("w_codes", w_codes, dev)
     M, K = a_codes.shape
     N, Kw = w_codes.shape
     if Kw != K:
         raise ValueError("a_codes and w_codes must have the same K")
-    _need_cuda("a_scales", a_scales, torch.float32)
-    _need_cuda("w_scales", w_scales, torch.float32)
-    if tuple(a_scales.shape) != (M, _blocks(K)):
-        raise ValueError(f"a_scales must have shape {(M, _blocks(K))}, got {tuple(a_scales.shape)}")
-    if tuple(w_scales.shape) == (_blocks(N), _blocks(K)):
+    psa = _flat("a_scales", a_scales, torch.float32, dev)
+    psw = _flat("w_scales", w_scales, torch.float32, dev)
+    kb = _blocks(K)
+    if a_scales.shape != (M, kb):
+        raise ValueError(f"a_scales must have shape {(M, kb)}, got {tuple(a_scales.shape)}")
+    if w_scales.shape == (_blocks(N), kb):
         rows = 128
-    elif tuple(w_scales.shape) == (N, _blocks(K)):
+    elif w_scales.shape == (N, kb):
         rows = 1
     else:
-        raise ValueError(f"w_scales must have shape {(_blocks(N), _blocks(K))} or "
-                         f"{(N, _blocks(K))}, got {tuple(w_scales.shape)}")
+        raise ValueError(f"w_scales must have shape {(_blocks(N), kb)} or {(N, kb)}, "
+                         f"got {tuple(w_scales.shape)}")
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
-    out = _out("out", out, (M, N), out_dtype, a_codes)
-    _on_device(a_codes, a_scales, w_codes, w_scales, out)
-    check(lib().nts_gemm_blockscaled(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
-                                     _ptr(w_scales), rows, _ptr(out),
-                                     1 if out_dtype == torch.float32 else 0, M, N, K,
-                                     _stream(stream)))
+    out = _out("out", out, (M, N), out_dtype, dev)
+    check(lib().nts_gemm_blockscaled(pa, psa, pw, psw, rows, out.data_ptr(),
+                                     1 if out_dtype is torch.float32 else 0, M, N, K,
+                                     _raw_stream(stream, dev)))
     return out
 
 
