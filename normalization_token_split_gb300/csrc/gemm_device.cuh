@@ -9,23 +9,37 @@
 
 namespace nts {
 
-// Wait for a phase of `bar`; false once `limit_ns` passed here or another
-// role of the CTA set *stop (then set here too).  The clock is read only once
-// many tries have failed: a read takes longer than most waits.
-__device__ __forceinline__ bool mbar_wait_or_stop(uint32_t bar, uint32_t parity,
-                                                  uint64_t limit_ns, volatile int* stop) {
-  for (int i = 0; i < 256; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*stop) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      *stop = 1;
-      return false;
+// A warp's wait for a phase of `bar`, all lanes together: false once
+// `limit_ns` passed here or another role of the CTA set *stop (then set here
+// too).  Every branch is taken on a vote, so the compiler knows that the warp
+// stays together and keeps addresses and descriptors in uniform registers, and
+// the clock is read only once many tries have failed: a read takes longer than
+// most waits.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile int* stop) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  uint64_t t0 = 0;
+  for (unsigned i = 1;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if (i % 64 == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      const bool late = t - t0 > limit_ns;
+      if (late) *stop = 1;
+      if (__any_sync(0xFFFFFFFFu, late || *stop)) return false;
     }
   }
+}
+
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // A place in a ring of N barriers: the slot and the parity of its phase.
@@ -165,6 +179,19 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+
+// One fp32 value from global into shared memory without waiting for it (zero
+// when !in; nothing is read then).
+__device__ __forceinline__ void copy_async_f32(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {

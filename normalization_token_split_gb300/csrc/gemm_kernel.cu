@@ -64,7 +64,7 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
   if (threadIdx.x == 0)
     for (int64_t j = max64(0, issued - S); j < issued; ++j)
       (void)mbar_wait_bounded(full + 8 * (int)(j % S), (uint32_t)((j / S) & 1), limit_ns);
-  if (threadIdx.x == 32) {   // the thread that issues them
+  if (threadIdx.x >> 5 == 1 && elect_one()) {   // the thread that issues them
     mma_commit(done);
     (void)mbar_wait_bounded(done, 0, limit_ns);
   }
@@ -129,7 +129,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       mbar_init(tempty + 8 * i, 8);
     }
     for (int i = 0; i < kPieces; ++i) {
-      mbar_init(sfull + 8 * i, 2);
+      mbar_init(sfull + 8 * i, 64);
       mbar_init(sempty + 8 * i, 8);
     }
     mbar_init(done, 1);
@@ -150,58 +150,60 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   if (warp < 4) {
     if (BN == 256) registers_down<kWideRegsDown>();
     if (warp == 0) {
-      if (lane == 0) {
-        RingSlot<S> st;
-        int64_t n = 0;   // stages issued
-        bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-          int tm, tn;
-          tile_at(p, tile, &tm, &tn);
-          for (int kb = 0; kb < p.kblocks; ++kb, ++n, st.advance()) {
-            if (n >= S &&
-                !mbar_wait_or_stop(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
-              ok = false;
-              break;
-            }
-            const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+      RingSlot<S> st;
+      int64_t n = 0;   // stages issued
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        int tm, tn;
+        tile_at(p, tile, &tm, &tn);
+        for (int kb = 0; kb < p.kblocks; ++kb, ++n, st.advance()) {
+          if (n >= S && !warp_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+          if (elect_one()) {
             mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
             tma_load_2d(at, &map_a, kb * 128, tm * 128, bar);
             tma_load_2d(at + C::kA, &map_w, kb * 128, tn * BN, bar);
           }
+          __syncwarp();
         }
+      }
+      if (lane == 0) {
         if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
         *issued = n;
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        constexpr uint32_t instr = e4m3_instr(128, BN);
-        RingSlot<S> st;
-        RingSlot<NB> tb;
-        bool ok = true, filled = false;   // filled: every buffer was used once
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-          for (int kb = 0; kb < p.kblocks; ++kb, st.advance()) {
-            if (!mbar_wait_or_stop(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
-                (filled &&
-                 !mbar_wait_or_stop(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
-              ok = false;
-              break;
-            }
-            tcgen05_fence_after();
+      constexpr uint32_t instr = e4m3_instr(128, BN);
+      RingSlot<S> st;
+      RingSlot<NB> tb;
+      bool ok = true, filled = false;   // filled: every buffer was used once
+      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int kb = 0; kb < p.kblocks; ++kb, st.advance()) {
+          if (!warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
+              (filled && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          if (elect_one()) {
             const uint64_t da = operand_desc(sbase + st.i * C::kStage);
             const uint64_t dw = operand_desc(sbase + st.i * C::kStage + C::kA);
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_e4m3(tmem + tb.i * BN, da + 2 * k, dw + 2 * k, instr, k > 0);
             mma_commit(empty + 8 * st.i);
             mma_commit(tfull + 8 * tb.i);
-            filled |= tb.i == NB - 1;
-            tb.advance();
           }
+          __syncwarp();
+          filled |= tb.i == NB - 1;
+          tb.advance();
         }
-        if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
       }
+      if (!ok && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
     } else if (warp < 4) {
-      // scale warps: lanes 8 r .. 8 r + 7 read the eight scales of a row
+      // scale warps: lanes 8 r .. 8 r + 7 copy the eight scales of a row
       const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
       RingSlot<kPieces> pc;
       bool ok = true, filled = false;
@@ -210,30 +212,28 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         tile_at(p, tile, &tm, &tn);
         for (int k0 = 0; k0 < p.kblocks; k0 += kChunk) {
           if (filled &&
-              !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sempty + 8 * pc.i, pc.parity ^ 1u,
-                                                         p.wait_limit_ns, stop))) {
+              !warp_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop)) {
             ok = false;
             break;
           }
-          float* dst = scales + (pc.i * kChunk + kl) * C::kScales;
+          const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
           const bool in = k0 + kl < p.kblocks;
-          const float* sa = p.sa + (int64_t)tm * 128 * p.kblocks + k0 + kl;
           const int rows = (int)min64(128, p.M - (int64_t)tm * 128);
-  #pragma unroll 4
-          for (int r = sub; r < 128; r += 8)
-            dst[r] = in && r < rows ? __ldg(sa + (int64_t)r * p.kblocks) : 0.f;
-          if (ROWS) {
-            const float* sw = p.sw + (int64_t)tn * BN * p.kblocks + k0 + kl;
-            const int cols = (int)min64(BN, p.N - (int64_t)tn * BN);
-  #pragma unroll 4
-            for (int r = sub; r < BN; r += 8)
-              dst[128 + r] = in && r < cols ? __ldg(sw + (int64_t)r * p.kblocks) : 0.f;
-          } else if (sub < BN / 128) {
-            const int64_t w = (int64_t)tn * (BN / 128) + sub;
-            dst[128 + sub] = in && w * 128 < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
+          const float* sa = p.sa + (int64_t)tm * 128 * p.kblocks + k0 + kl;
+#pragma unroll 4
+          for (int r = sub; r < 128; r += 8) {
+            const bool here = in && r < rows;
+            copy_async_f32(dst + 4 * r, here ? sa + (int64_t)r * p.kblocks : p.sa, here);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sfull + 8 * pc.i);
+          const int64_t w0 = ROWS ? (int64_t)tn * BN : (int64_t)tn * (BN / 128);
+          const int cols = (int)min64(ROWS ? BN : BN / 128, (ROWS ? p.N : (p.N + 127) / 128) - w0);
+          const float* sw = p.sw + w0 * p.kblocks + k0 + kl;
+#pragma unroll 4
+          for (int r = sub; r < (ROWS ? BN : BN / 128); r += 8) {
+            const bool here = in && r < cols;
+            copy_async_f32(dst + 4 * (128 + r), here ? sw + (int64_t)r * p.kblocks : p.sw, here);
+          }
+          copy_async_arrive(sfull + 8 * pc.i);
           filled |= pc.i == kPieces - 1;
           pc.advance();
         }
@@ -258,10 +258,8 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       bool ok = true;
       for (int kb = 0; kb < p.kblocks; ++kb, tb.advance()) {
         if ((kb % kChunk == 0 &&
-             !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sfull + 8 * pc.i, pc.parity,
-                                                        p.wait_limit_ns, stop))) ||
-            !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * tb.i, tb.parity,
-                                                       p.wait_limit_ns, stop))) {
+             !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) ||
+            !warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) {
           ok = false;
           break;
         }
@@ -284,7 +282,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           }
 #pragma unroll
           for (int i = 0; i < LD / 2; ++i) {
-            uint64_t x = f2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1]));
+            uint64_t x = (uint64_t)v[j & 1][2 * i + 1] << 32 | v[j & 1][2 * i];
             if (ROWS)
               x = f2_mul(x, *reinterpret_cast<const uint64_t*>(sc + 128 + wblock + LD * j + 2 * i));
             acc[LD / 2 * j + i] = f2_fma(x, ss, acc[LD / 2 * j + i]);
@@ -409,7 +407,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       mbar_init(tempty + 8 * i, 4);
     }
     for (int i = 0; i < kPieces; ++i) {
-      mbar_init(sfull + 8 * i, 2);
+      mbar_init(sfull + 8 * i, 64);
       mbar_init(sempty + 8 * i, 4);
     }
     mbar_init(done, 1);
@@ -428,37 +426,39 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
 
   float acc[TN];
   if (warp == 0) {
-    if (lane == 0) {
-      RingSlot<S> st;
-      bool ok = true;
-      int n = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++n, st.advance()) {
-        if (n >= S && !mbar_wait_or_stop(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
-          ok = false;
-          break;
-        }
-        const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+    RingSlot<S> st;
+    bool ok = true;
+    int n = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++n, st.advance()) {
+      if (n >= S && !warp_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
+        ok = false;
+        break;
+      }
+      const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+      if (elect_one()) {
         mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
         tma_load_2d(at, &map_w, kb * 128, tn * 128, bar);
         tma_load_2d(at + C::kW, &map_a, kb * 128, tm * TN, bar);
       }
+      __syncwarp();
+    }
+    if (lane == 0) {
       if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
       *issued = n;
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t instr = e4m3_instr(128, TN);
-      RingSlot<S> st;
-      RingSlot<NB> tb;
-      bool ok = true;
-      for (int n = 0; n < kb1 - kb0; ++n, st.advance(), tb.advance()) {
-        if (!mbar_wait_or_stop(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
-            (n >= NB &&
-             !mbar_wait_or_stop(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
-          ok = false;
-          break;
-        }
-        tcgen05_fence_after();
+    constexpr uint32_t instr = e4m3_instr(128, TN);
+    RingSlot<S> st;
+    RingSlot<NB> tb;
+    bool ok = true;
+    for (int n = 0; n < kb1 - kb0; ++n, st.advance(), tb.advance()) {
+      if (!warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
+          (n >= NB && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
+        ok = false;
+        break;
+      }
+      tcgen05_fence_after();
+      if (elect_one()) {
         const uint64_t dw = operand_desc(sbase + st.i * C::kStage);
         const uint64_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
 #pragma unroll
@@ -467,34 +467,31 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         mma_commit(empty + 8 * st.i);
         mma_commit(tfull + 8 * tb.i);
       }
-      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
+      __syncwarp();
     }
+    if (!ok && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
   } else if (warp < 4) {
     const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
     RingSlot<kPieces> pc;
     for (int k0 = kb0; k0 < kb1; k0 += kChunk, pc.advance()) {
       if (k0 - kb0 >= kPieces * kChunk &&
-          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sempty + 8 * pc.i, pc.parity ^ 1u,
-                                                     p.wait_limit_ns, stop)))
+          !warp_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop))
         break;
-      float* dst = scales + (pc.i * kChunk + kl) * C::kScales;
+      const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
       const bool in = k0 + kl < kb1;
-#pragma unroll 8
+#pragma unroll 4
       for (int r = sub; r < TN; r += 8) {
         const int64_t m = (int64_t)tm * TN + r;
-        dst[r] = in && m < p.M ? __ldg(p.sa + m * p.kblocks + k0 + kl) : 0.f;
+        const bool here = in && m < p.M;
+        copy_async_f32(dst + 4 * r, here ? p.sa + m * p.kblocks + k0 + kl : p.sa, here);
       }
-      if (ROWS) {
-#pragma unroll 8
-        for (int r = sub; r < 128; r += 8) {
-          const int64_t w = (int64_t)tn * 128 + r;
-          dst[TN + r] = in && w < p.N ? __ldg(p.sw + w * p.kblocks + k0 + kl) : 0.f;
-        }
-      } else if (sub == 0) {
-        dst[TN] = in ? __ldg(p.sw + (int64_t)tn * p.kblocks + k0 + kl) : 0.f;
+#pragma unroll 4
+      for (int r = sub; r < (ROWS ? 128 : 1); r += 8) {
+        const int64_t w = ROWS ? (int64_t)tn * 128 + r : tn;
+        const bool here = in && (!ROWS || w < p.N);
+        copy_async_f32(dst + 4 * (TN + r), here ? p.sw + w * p.kblocks + k0 + kl : p.sw, here);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sfull + 8 * pc.i);
+      copy_async_arrive(sfull + 8 * pc.i);
     }
   } else {
     const int row = (warp & 3) * 32 + lane;   // of W
@@ -505,10 +502,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     RingSlot<kPieces> pc;
     for (int n = 0; n < kb1 - kb0; ++n, tb.advance()) {
       if ((n % kChunk == 0 &&
-           !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns,
-                                                      stop))) ||
-          !__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns,
-                                                     stop))) {
+           !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) ||
+          !warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) {
         if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
         break;
       }

@@ -491,13 +491,15 @@ __device__ __forceinline__ RopeRing rope_ring(const RopeParams& p, unsigned char
   return r;
 }
 
-// Waits for stage s; a warp gives up together.
+// Waits for stage s: lane 0 tries for the warp.
 __device__ __forceinline__ bool ring_wait(const RopeParams& p, const RopeRing& r, int s,
                                           uint32_t parity) {
-  const bool ok =
-      __all_sync(0xFFFFFFFFu, mbar_wait_bounded(r.bars + 8 * s, parity, p.wait_limit_ns));
-  if (!ok && (threadIdx.x & 31) == 0) atomicOr(&g_rope_status, kStatusTimeout);
-  return ok;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) {
+    ok = mbar_wait_bounded(r.bars + 8 * s, parity, p.wait_limit_ns);
+    if (!ok) atomicOr(&g_rope_status, kStatusTimeout);
+  }
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
 // After an expired wait at stage s: the copies in flight (every stage) land, bounded.
