@@ -57,15 +57,23 @@ struct GemmParams {
 
 // After a wait gave up: the copies in flight land (the last S of `issued`
 // stages) and the matrix instructions in flight end, each within the limit,
-// before shared and tensor memory are given back.
-template <int S>
+// before shared and tensor memory are given back.  The second CTA of a pair
+// has its copies counted on the first one's barriers; it gives them a
+// millisecond, a thousand times what a copy takes.
+template <int S, bool PAIR>
 __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issued,
                                       uint64_t limit_ns) {
-  if (threadIdx.x == 0)
-    for (int64_t j = max64(0, issued - S); j < issued; ++j)
-      (void)mbar_wait_bounded(full + 8 * (int)(j % S), (uint32_t)((j / S) & 1), limit_ns);
-  if (threadIdx.x >> 5 == 1 && elect_one()) {   // the thread that issues them
-    mma_commit(done);
+  const bool first = !PAIR || cluster_ctarank() == 0;
+  if (threadIdx.x == 0) {
+    if (first)
+      for (int64_t j = max64(0, issued - S); j < issued; ++j)
+        (void)mbar_wait_bounded(full + 8 * (int)(j % S), (uint32_t)((j / S) & 1), limit_ns);
+    else
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
+      }
+  }
+  if (first && threadIdx.x >> 5 == 1 && elect_one()) {   // the thread that issues them
+    mma_commit<PAIR>(done);
     (void)mbar_wait_bounded(done, 0, limit_ns);
   }
 }
@@ -75,16 +83,18 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
 constexpr int kWideThreads = 384;     // TMA, MMA, 2 scale warps, 8 epilogue warps
 constexpr int kGroupM = 16;           // tiles of A walked before the next tile of W
 // Registers per thread at BN = 256, whose epilogue holds 128 sums and 64
-// loaded values per thread: 168 at launch, then 40 in the four other warps and
-// 232 in the epilogue's eight (128 * 40 + 256 * 232 = 384 * 168).
-constexpr int kWideRegs = 168, kWideRegsDown = 40, kWideRegsUp = 232;
+// loaded values per thread: 168 at launch, then 56 in the four other warps and
+// 224 in the epilogue's eight (128 * 56 + 256 * 224 = 384 * 168).
+constexpr int kWideRegs = 168, kWideRegsDown = 56, kWideRegsUp = 224;
 
 template <int BN, bool ROWS>
 struct Wide {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr bool kPair = BN == 256;
+  static constexpr int kTileM = kPair ? 256 : 128;        // rows of A per tile
+  static constexpr int kStages = 6;
   static constexpr int kBufs = 512 / BN;
-  static constexpr uint32_t kA = 128 * 128;
-  static constexpr uint32_t kStage = kA + BN * 128;
+  static constexpr uint32_t kA = 128 * 128;               // of this CTA
+  static constexpr uint32_t kStage = kA + 128 * 128;      // W: 128 rows per CTA either way
   static constexpr int kScales = 128 + (ROWS ? BN : 4);   // floats per K block
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
@@ -107,6 +117,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const GemmParams p) {
   using C = Wide<BN, ROWS>;
   constexpr int S = C::kStages, NB = C::kBufs;
+  constexpr bool PAIR = C::kPair;
   extern __shared__ unsigned char raw[];
   const uint32_t sbase = (smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* smem = raw + (sbase - smem_addr(raw));
@@ -126,7 +137,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, 8);
+      mbar_init(tempty + 8 * i, PAIR ? 16 : 8);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(sfull + 8 * i, 64);
@@ -138,14 +149,21 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     prefetch_tensor_map(&map_a);
     prefetch_tensor_map(&map_w);
   }
-  if (warp == 1) tmem_alloc(slot, 512);
+  if (warp == 1) tmem_alloc<PAIR>(slot, 512);
   tcgen05_fence_before();
   __syncthreads();
+  if (PAIR) {   // the other CTA's barriers are there before anything signals them
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - sbase));
   grid_dependency_wait();
   allow_dependent_launch();
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const int64_t first = PAIR ? cluster_id_x() : blockIdx.x;
+  const int64_t step = PAIR ? num_clusters_x() : gridDim.x;
 
   if (warp < 4) {
     if (BN == 256) registers_down<kWideRegsDown>();
@@ -153,7 +171,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       RingSlot<S> st;
       int64_t n = 0;   // stages issued
       bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int64_t tile = first; tile < tiles && ok; tile += step) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
         for (int kb = 0; kb < p.kblocks; ++kb, ++n, st.advance()) {
@@ -162,10 +180,13 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             break;
           }
           const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+          // a pair's copies all count on the first CTA's barrier
+          const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
           if (elect_one()) {
-            mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
-            tma_load_2d(at, &map_a, kb * 128, tm * 128, bar);
-            tma_load_2d(at + C::kA, &map_w, kb * 128, tn * BN, bar);
+            if (rank == 0)
+              mbar_arrive_expect_tx(bar, C::kStage * (PAIR ? 2 : 1) + (n == 0 ? p.missing_tx : 0u));
+            tma_load_2d<PAIR>(at, &map_a, kb * 128, tm * C::kTileM + rank * 128, counts);
+            tma_load_2d<PAIR>(at + C::kA, &map_w, kb * 128, tn * BN + rank * 128, counts);
           }
           __syncwarp();
         }
@@ -174,27 +195,28 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
         *issued = n;
       }
-    } else if (warp == 1) {
-      constexpr uint32_t instr = e4m3_instr(128, BN);
+    } else if (warp == 1 && rank == 0) {
+      constexpr uint32_t instr = e4m3_instr(C::kTileM, BN);
       RingSlot<S> st;
       RingSlot<NB> tb;
       bool ok = true, filled = false;   // filled: every buffer was used once
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int64_t tile = first; tile < tiles && ok; tile += step) {
         for (int kb = 0; kb < p.kblocks; ++kb, st.advance()) {
-          if (!warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
-              (filled && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
+          // addresses first: behind the waits only the matrix instructions are left
+          const uint64_t da = operand_desc(sbase + st.i * C::kStage);
+          const uint64_t dw = operand_desc(sbase + st.i * C::kStage + C::kA);
+          const uint32_t d = tmem + tb.i * BN;
+          const uint32_t release = empty + 8 * st.i, ready = tfull + 8 * tb.i;
+          if ((filled && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop)) ||
+              !warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop)) {
             ok = false;
             break;
           }
           tcgen05_fence_after();
           if (elect_one()) {
-            const uint64_t da = operand_desc(sbase + st.i * C::kStage);
-            const uint64_t dw = operand_desc(sbase + st.i * C::kStage + C::kA);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3(tmem + tb.i * BN, da + 2 * k, dw + 2 * k, instr, k > 0);
-            mma_commit(empty + 8 * st.i);
-            mma_commit(tfull + 8 * tb.i);
+            mma_block<PAIR>(d, da, dw, instr);
+            mma_commit<PAIR>(release);
+            mma_commit<PAIR>(ready);
           }
           __syncwarp();
           filled |= tb.i == NB - 1;
@@ -202,12 +224,12 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
       }
       if (!ok && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
-    } else if (warp < 4) {
+    } else if (warp > 1) {
       // scale warps: lanes 8 r .. 8 r + 7 copy the eight scales of a row
       const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
       RingSlot<kPieces> pc;
       bool ok = true, filled = false;
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int64_t tile = first; tile < tiles && ok; tile += step) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
         for (int k0 = 0; k0 < p.kblocks; k0 += kChunk) {
@@ -218,8 +240,9 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           }
           const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
           const bool in = k0 + kl < p.kblocks;
-          const int rows = (int)min64(128, p.M - (int64_t)tm * 128);
-          const float* sa = p.sa + (int64_t)tm * 128 * p.kblocks + k0 + kl;
+          const int64_t m0 = (int64_t)tm * C::kTileM + rank * 128;
+          const int rows = (int)min64(128, p.M - m0);   // may be <= 0
+          const float* sa = p.sa + m0 * p.kblocks + k0 + kl;
 #pragma unroll 4
           for (int r = sub; r < 128; r += 8) {
             const bool here = in && r < rows;
@@ -247,48 +270,67 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
     const int wblock = ROWS ? group * COLS : group * COLS / 128;
+    constexpr int STEPS = COLS / LD;   // even: a block's first load goes where it began
     RingSlot<NB> tb;
     RingSlot<kPieces> pc;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    uint32_t v[2][LD];
+    // the block in buffer tb is there: its first columns are on their way
+    auto begin = [&] {
+      if (!warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) return false;
+      tcgen05_fence_after();
+      tmem_load(v[0], tmem + tb.i * BN + group * COLS + lanes);
+      return true;
+    };
+    for (int64_t tile = first; tile < tiles; tile += step) {
       int tm, tn;
       tile_at(p, tile, &tm, &tn);
       uint64_t acc[COLS / 2];   // pairs of columns
 #pragma unroll
       for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
-      bool ok = true;
-      for (int kb = 0; kb < p.kblocks; ++kb, tb.advance()) {
-        if ((kb % kChunk == 0 &&
-             !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) ||
-            !warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) {
+      bool ok = begin();
+      for (int kb = 0; kb < p.kblocks && ok; ++kb) {
+        const int in_piece = kb & (kChunk - 1);
+        if (in_piece == 0 &&
+            !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) {
           ok = false;
           break;
         }
-        tcgen05_fence_after();
-        const uint32_t at = tmem + tb.i * BN + group * COLS + lanes;
-        uint32_t v[2][LD];
-        tmem_load(v[0], at);
-        const float* sc = scales + (pc.i * kChunk + kb % kChunk) * C::kScales;
+        const float* sc = scales + (pc.i * kChunk + in_piece) * C::kScales;
         const float s = ROWS ? sc[row] : sc[row] * sc[128 + wblock];
         const uint64_t ss = f2(s, s);
+        const uint32_t at = tmem + tb.i * BN + group * COLS + lanes;
 #pragma unroll
-        for (int j = 0; j < COLS / LD; ++j) {
+        for (int j = 0; j < STEPS; ++j) {
           tmem_wait(v[j & 1]);
-          if (j + 1 < COLS / LD) {
+          if (j + 1 < STEPS) {
             tmem_load(v[(j + 1) & 1], at + LD * (j + 1));
-          } else {   // the buffer is in registers: the next block's product may start
+          } else {   // all in registers: the buffer is free, the next block begins
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + 8 * tb.i);
+            if (lane == 0) {
+              if (PAIR)
+                mbar_arrive_cluster(map_to_rank(tempty + 8 * tb.i, 0));
+              else
+                mbar_arrive(tempty + 8 * tb.i);
+            }
+            tb.advance();
+            if (kb + 1 < p.kblocks) ok = begin();
           }
 #pragma unroll
-          for (int i = 0; i < LD / 2; ++i) {
-            uint64_t x = (uint64_t)v[j & 1][2 * i + 1] << 32 | v[j & 1][2 * i];
-            if (ROWS)
-              x = f2_mul(x, *reinterpret_cast<const uint64_t*>(sc + 128 + wblock + LD * j + 2 * i));
-            acc[LD / 2 * j + i] = f2_fma(x, ss, acc[LD / 2 * j + i]);
+          for (int i = 0; i < LD / 2; i += 2) {
+            uint64_t x0 = (uint64_t)v[j & 1][2 * i + 1] << 32 | v[j & 1][2 * i];
+            uint64_t x1 = (uint64_t)v[j & 1][2 * i + 3] << 32 | v[j & 1][2 * i + 2];
+            if (ROWS) {
+              const ulonglong2 w =
+                  *reinterpret_cast<const ulonglong2*>(sc + 128 + wblock + LD * j + 2 * i);
+              x0 = f2_mul(x0, w.x);
+              x1 = f2_mul(x1, w.y);
+            }
+            acc[LD / 2 * j + i] = f2_fma(x0, ss, acc[LD / 2 * j + i]);
+            acc[LD / 2 * j + i + 1] = f2_fma(x1, ss, acc[LD / 2 * j + i + 1]);
           }
         }
-        if (kb % kChunk == kChunk - 1 || kb == p.kblocks - 1) {
+        if (in_piece == kChunk - 1 || kb == p.kblocks - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(sempty + 8 * pc.i);
           pc.advance();
@@ -298,7 +340,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
         break;
       }
-      const int64_t m = (int64_t)tm * 128 + row;
+      const int64_t m = (int64_t)tm * C::kTileM + rank * 128 + row;
       const int64_t n0 = (int64_t)tn * BN + group * COLS;
       if (m < p.M) {
         const int cols = (int)min64(COLS, p.N - n0);   // may be <= 0
@@ -344,11 +386,15 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   tcgen05_fence_before();
   __syncthreads();
   if (*stop) {
-    drain<S>(full, done, *issued, p.wait_limit_ns);
+    drain<S, PAIR>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
   }
+  if (PAIR) {   // no CTA leaves while the other's instructions use its memory
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
   tcgen05_fence_after();
-  if (warp == 1) tmem_free(tmem, 512);
+  if (warp == 1) tmem_free<PAIR>(tmem, 512);
 }
 
 // -------------------------------------------------------------- narrow
@@ -416,7 +462,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     prefetch_tensor_map(&map_a);
     prefetch_tensor_map(&map_w);
   }
-  if (warp == 1) tmem_alloc(slot, C::kCols);
+  if (warp == 1) tmem_alloc<false>(slot, C::kCols);
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
@@ -437,8 +483,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
       if (elect_one()) {
         mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
-        tma_load_2d(at, &map_w, kb * 128, tn * 128, bar);
-        tma_load_2d(at + C::kW, &map_a, kb * 128, tm * TN, bar);
+        tma_load_2d<false>(at, &map_w, kb * 128, tn * 128, bar);
+        tma_load_2d<false>(at + C::kW, &map_a, kb * 128, tm * TN, bar);
       }
       __syncwarp();
     }
@@ -452,20 +498,20 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     RingSlot<NB> tb;
     bool ok = true;
     for (int n = 0; n < kb1 - kb0; ++n, st.advance(), tb.advance()) {
-      if (!warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop) ||
-          (n >= NB && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop))) {
+      const uint64_t dw = operand_desc(sbase + st.i * C::kStage);
+      const uint64_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
+      const uint32_t d = tmem + tb.i * C::kBufCols;
+      const uint32_t release = empty + 8 * st.i, ready = tfull + 8 * tb.i;
+      if ((n >= NB && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop)) ||
+          !warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop)) {
         ok = false;
         break;
       }
       tcgen05_fence_after();
       if (elect_one()) {
-        const uint64_t dw = operand_desc(sbase + st.i * C::kStage);
-        const uint64_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_e4m3(tmem + tb.i * C::kBufCols, dw + 2 * k, da + 2 * k, instr, k > 0);
-        mma_commit(empty + 8 * st.i);
-        mma_commit(tfull + 8 * tb.i);
+        mma_block<false>(d, dw, da, instr);
+        mma_commit<false>(release);
+        mma_commit<false>(ready);
       }
       __syncwarp();
     }
@@ -535,11 +581,11 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   tcgen05_fence_before();
   __syncthreads();
   if (*stop) {
-    drain<S>(full, done, *issued, p.wait_limit_ns);
+    drain<S, false>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
   }
   tcgen05_fence_after();
-  if (warp == 1) tmem_free(tmem, C::kCols);
+  if (warp == 1) tmem_free<false>(tmem, C::kCols);
 
   // The sums of this CTA's K blocks to shared memory (the ring is drained),
   // then every CTA adds its share of the tile over the ranks, in their order.
@@ -609,6 +655,15 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int bo
   return NTS_OK;
 }
 
+cudaLaunchAttribute cluster_attribute(int cluster) {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)cluster;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
 int launch(GemmKernel kern, const GemmRequest& rq, const GemmParams& p, int box_a, int box_w,
            dim3 grid, int threads, int regs, size_t smem, int cluster, cudaStream_t stream,
            bool pdl) {
@@ -633,12 +688,7 @@ int launch(GemmKernel kern, const GemmRequest& rq, const GemmParams& p, int box_
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  if (cluster > 0) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = (unsigned)cluster;
-    attr[na].val.clusterDim.y = 1;
-    attr[na++].val.clusterDim.z = 1;
-  }
+  attr[na++] = cluster_attribute(cluster);
   if (pdl) attr[na++] = pdl_attribute();
   cfg.numAttrs = na;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_w, p);
@@ -666,21 +716,32 @@ int launch_narrow(const GemmRequest& rq, const GemmParams& p, cudaStream_t strea
                       Narrow<TN, false>::kLaunch, split, stream, tune.pdl != 0);
 }
 
-template <int BN>
+template <int BN, bool ROWS>
 int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const DeviceInfo& dev,
                 const LaunchTuning& tune) {
-  p.tiles_m = (int)((p.M + 127) / 128);
+  using C = Wide<BN, ROWS>;
+  p.tiles_m = (int)((p.M + C::kTileM - 1) / C::kTileM);
   p.tiles_n = (int)((p.N + BN - 1) / BN);
-  const unsigned grid =
-      (unsigned)std::min<int64_t>((int64_t)p.tiles_m * p.tiles_n, dev.sm_count);
-  const int regs = BN == 256 ? kWideRegs : 0;
-  log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide BN=%d grid=%u", (long long)p.M,
-             (long long)p.N, (long long)rq.K, BN, grid);
-  return rq.w_rows == 1
-             ? launch(wide_kernel<BN, true>, rq, p, 128, BN, dim3(grid), kWideThreads, regs,
-                      Wide<BN, true>::kLaunch, 0, stream, tune.pdl != 0)
-             : launch(wide_kernel<BN, false>, rq, p, 128, BN, dim3(grid), kWideThreads, regs,
-                      Wide<BN, false>::kLaunch, 0, stream, tune.pdl != 0);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const int cluster = C::kPair ? 2 : 1;
+  int64_t most = dev.sm_count;
+  if (C::kPair) {
+    int rc = prepare_kernel((const void*)wide_kernel<BN, ROWS>, C::kLaunch);
+    if (rc != NTS_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = cluster_attribute(cluster);
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = C::kLaunch;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    rc = max_active_clusters((const void*)wide_kernel<BN, ROWS>, cfg, cluster, &most);
+    if (rc != NTS_OK) return rc;
+  }
+  const unsigned grid = (unsigned)(std::min(tiles, most) * cluster);
+  log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide %dx%d grid=%u", (long long)p.M,
+             (long long)p.N, (long long)rq.K, C::kTileM, BN, grid);
+  return launch(wide_kernel<BN, ROWS>, rq, p, 128, 128, dim3(grid), kWideThreads,
+                C::kPair ? kWideRegs : 0, C::kLaunch, cluster, stream, tune.pdl != 0);
 }
 
 }  // namespace
@@ -704,9 +765,12 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   if (p.M <= 16) return launch_narrow<16>(rq, p, stream, dev, tune);
   if (p.M <= 32) return launch_narrow<32>(rq, p, stream, dev, tune);
   if (p.M <= 128) return launch_narrow<64>(rq, p, stream, dev, tune);
-  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 255) / 256);
-  return tiles >= dev.sm_count ? launch_wide<256>(rq, p, stream, dev, tune)
-                               : launch_wide<128>(rq, p, stream, dev, tune);
+  const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  if (2 * pairs >= dev.sm_count)
+    return rq.w_rows == 1 ? launch_wide<256, true>(rq, p, stream, dev, tune)
+                          : launch_wide<256, false>(rq, p, stream, dev, tune);
+  return rq.w_rows == 1 ? launch_wide<128, true>(rq, p, stream, dev, tune)
+                        : launch_wide<128, false>(rq, p, stream, dev, tune);
 }
 
 int read_and_clear_gemm_status(unsigned* out) {
