@@ -9,26 +9,84 @@
 
 namespace nts {
 
-// A warp's wait for a phase of `bar`, all lanes together: false once
-// `limit_ns` passed here or another role of the CTA set *stop (then set here
-// too).  Every branch is taken on a vote, so the compiler knows that the warp
-// stays together and keeps addresses and descriptors in uniform registers, and
-// the clock is read only once many tries have failed: a read takes longer than
-// most waits.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                          volatile int* stop) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  uint64_t t0 = 0;
-  for (unsigned i = 1;; ++i) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    if (i % 64 == 0) {
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      const bool late = t - t0 > limit_ns;
-      if (late) *stop = 1;
-      if (__any_sync(0xFFFFFFFFu, late || *stop)) return false;
-    }
-  }
+// Whether a phase of `bar` is complete, without waiting.  While the matrix
+// instructions and the copies keep shared memory busy, an answer takes ~170
+// cycles (24 on an idle SM): asked for early, it is there when it is needed.
+__device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+// A bounded wait for a phase of `bar`, at once over when `done` (an earlier
+// answer of bar_test) is set.  It costs a satisfied wait two branches and no
+// vote: a role's loop passes several for every K block, and at ~25 cycles a
+// branch they decide how fast it turns.  A wait that expires (limit_ns, or
+// another role of the CTA set *stop) sets *stop and `late`; once `late` is set
+// the waits that follow return at once, so a role may look at it only now and
+// then, as long as what it does meanwhile stays inside its own memory.  The
+// clock is read only after many tries: a read takes longer than most waits.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                         uint32_t stop, uint32_t& late, uint32_t done = 0) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred p, q;\n\t"
+      ".reg .u64 t0, t;\n\t"
+      ".reg .u32 n;\n\t"
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q bra DONE;\n\t"
+      "mov.u32 n, 0;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 64;\n\t"
+      "@q bra TRY;\n\t"
+      "mov.u64 t0, %%globaltimer;\n"
+      "SLOW:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 n, [%4];\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra LATE;\n\t"
+      "mov.u64 t, %%globaltimer;\n\t"
+      "sub.u64 t, t, t0;\n\t"
+      "setp.le.u64 q, t, %3;\n\t"
+      "@q bra SLOW;\n"
+      "LATE:\n\t"
+      "mov.u32 %0, 1;\n\t"
+      "st.volatile.shared.u32 [%4], 1;\n"
+      "DONE:\n\t"
+      "}"
+      : "+r"(late)
+      : "r"(bar), "r"(parity), "l"(limit_ns), "r"(stop), "r"(done | late)
+      : "memory");
+}
+
+// Arrive on `bar` from the lanes with on != 0, without a branch.  CLUSTER: a
+// barrier of a CTA of this cluster (an address of map_to_rank), without a
+// cluster-wide release: what it orders are tensor-memory loads that their own
+// wait has completed, and a release at cluster scope took ~1300 cycles.
+template <bool CLUSTER>
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
+  if (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)on)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)on)
+        : "memory");
 }
 
 // One lane of a converged warp, always the same one.
@@ -125,10 +183,11 @@ __device__ __forceinline__ void tcgen05_fence_after() {
 
 // Descriptor of a shared-memory operand tile: rows of 128 bytes along K,
 // 128-byte swizzle, groups of eight rows 1024 bytes apart; the tile starts on
-// a 1024-byte boundary and a step of 32 values along K adds 32 bytes.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// a 1024-byte boundary and a step of 32 values along K adds 32 bytes.  The
+// upper word is the same for every tile; this is the lower one.
+constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand_desc(uint32_t addr) {
+  return (addr & 0x3FFFFu) >> 4 | 1u << 16;
 }
 
 // Instruction descriptor for E4M3 x E4M3 -> fp32, both operands along K,
@@ -137,34 +196,53 @@ __host__ __device__ constexpr uint32_t e4m3_instr(int m, int n) {
   return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
-// D = A B^T (+ D when acc): 32 values along K; one thread.  PAIR: the two
+// D = A B^T over one K block (128 values, four steps of which the first
+// overwrites D); one thread; a and b are operand_desc words.  PAIR: the two
 // CTAs' halves of A's rows (each CTA's shared memory) times both halves of B's
-// rows (one in each CTA); each CTA's tensor memory takes its rows of D.
+// rows (one in each CTA); each CTA's tensor memory takes its rows of D.  One
+// asm block, so that no step's descriptors stay in registers.
 template <bool PAIR>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
-                                         bool acc) {
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, uint32_t instr) {
   if (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.u32 p, %4, %4;\n\t"
+        "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "setp.eq.u32 p, %4, %4;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "r"(kDescHigh)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.u32 p, %4, %4;\n\t"
+        "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "setp.eq.u32 p, %4, %4;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
+        "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "r"(kDescHigh)
         : "memory");
-}
-
-// The product of one K block (128 values): four steps, the first of which
-// overwrites D.
-template <bool PAIR>
-__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t instr) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) mma_e4m3<PAIR>(d, a + 2 * k, b + 2 * k, instr, k > 0);
 }
 
 // Arrive on `bar` (PAIR: on that barrier in both CTAs) once every matrix
@@ -181,12 +259,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
-}
-
-// Arrive on a barrier of a CTA of this cluster (an address of map_to_rank).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
 }
 
 // 16 or 32 columns of this warp's 32 lanes of tensor memory: one lane per thread.

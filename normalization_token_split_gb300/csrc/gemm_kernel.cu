@@ -80,21 +80,31 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
 
 // ---------------------------------------------------------------- wide
 
-constexpr int kWideThreads = 384;     // TMA, MMA, 2 scale warps, 8 epilogue warps
-constexpr int kGroupM = 16;           // tiles of A walked before the next tile of W
-// Registers per thread at BN = 256, whose epilogue holds 128 sums and 64
-// loaded values per thread: 168 at launch, then 56 in the four other warps and
-// 224 in the epilogue's eight (128 * 56 + 256 * 224 = 384 * 168).
-constexpr int kWideRegs = 168, kWideRegsDown = 56, kWideRegsUp = 224;
+constexpr int kGroupM = 16;   // tiles of A walked before the next tile of W
 
+// BN = 256: a pair of CTAs works on 256 rows of A by 256 rows of W.  Each CTA
+// holds its 128 rows of A and half of W's rows, so an SM stores and reads 32 KB
+// per K block for 512 cycles of matrix instructions.  BN = 128: one CTA, 128
+// rows of A, for products with too few tiles for the pairs.
+//
+// Eight epilogue warps: four (one per 32 rows) for each half of the columns,
+// 32 columns at a time, the next 32 on their way while these are scaled and
+// added -- across K blocks too.  At BN = 256 a thread holds 128 sums and 64
+// loaded values, more than 384 threads have registers for: 168 at launch, then
+// 72 in the four other warps and 216 in the epilogue's eight (128 * 72 + 256 *
+// 216 = 384 * 168).
 template <int BN, bool ROWS>
 struct Wide {
   static constexpr bool kPair = BN == 256;
   static constexpr int kTileM = kPair ? 256 : 128;        // rows of A per tile
-  static constexpr int kStages = 6;
-  static constexpr int kBufs = 512 / BN;
-  static constexpr uint32_t kA = 128 * 128;               // of this CTA
-  static constexpr uint32_t kStage = kA + 128 * 128;      // W: 128 rows per CTA either way
+  static constexpr int kRowsW = kPair ? BN / 2 : BN;      // rows of W per CTA
+  static constexpr int kCols = BN / 2;                    // columns per epilogue warp
+  static constexpr int kThreads = 384;                    // TMA, MMA, 2 scale warps; epilogue
+  static constexpr int kRegs = kPair ? 168 : 0, kRegsDown = 72, kRegsUp = 216;
+  static constexpr uint32_t kA = 128 * 128;
+  static constexpr uint32_t kStage = kA + kRowsW * 128;
+  static constexpr int kStages = 196608 / (int)kStage;    // 6
+  static constexpr int kBufs = kPair ? 2 : 3;             // at most 512 columns; divides kStages
   static constexpr int kScales = 128 + (ROWS ? BN : 4);   // floats per K block
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
@@ -112,7 +122,7 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int64_t tile, int* 
 }
 
 template <int BN, bool ROWS>
-__global__ void __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(Wide<BN, ROWS>::kThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
             const GemmParams p) {
   using C = Wide<BN, ROWS>;
@@ -145,6 +155,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     mbar_init(done, 1);
     *stop = 0;
+    *issued = 0;
     fence_mbar_init();
     prefetch_tensor_map(&map_a);
     prefetch_tensor_map(&map_w);
@@ -164,219 +175,222 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int rank = PAIR ? (int)cluster_ctarank() : 0;
   const int64_t first = PAIR ? cluster_id_x() : blockIdx.x;
   const int64_t step = PAIR ? num_clusters_x() : gridDim.x;
+  const uint32_t stop_at = slot + 4;
+  uint32_t late = 0;
 
   if (warp < 4) {
-    if (BN == 256) registers_down<kWideRegsDown>();
+    if (PAIR) registers_down<C::kRegsDown>();
+    const bool leader = elect_one();
     if (warp == 0) {
       RingSlot<S> st;
       int64_t n = 0;   // stages issued
-      bool ok = true;
-      for (int64_t tile = first; tile < tiles && ok; tile += step) {
+      for (int64_t tile = first; tile < tiles && !late; tile += step) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
-        for (int kb = 0; kb < p.kblocks; ++kb, ++n, st.advance()) {
-          if (n >= S && !warp_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
-            ok = false;
-            break;
+        const int ya = tm * C::kTileM + rank * 128, yw = tn * BN + rank * C::kRowsW;
+        for (int k0 = 0; k0 < p.kblocks && !late; k0 += kChunk) {
+          const int k1 = min(k0 + kChunk, p.kblocks);
+          for (int kb = k0; kb < k1; ++kb, st.advance()) {
+            const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
+            // a pair's copies all count on the first CTA's barrier
+            const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
+            bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
+            if (leader) {
+              if (rank == 0)
+                mbar_arrive_expect_tx(
+                    bar, C::kStage * (PAIR ? 2 : 1) +
+                             (tile == first && kb == 0 ? p.missing_tx : 0u));
+              tma_load_2d<PAIR>(at, &map_a, kb * 128, ya, counts);
+              tma_load_2d<PAIR>(at + C::kA, &map_w, kb * 128, yw, counts);
+            }
+            __syncwarp();
           }
-          const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
-          // a pair's copies all count on the first CTA's barrier
-          const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
-          if (elect_one()) {
-            if (rank == 0)
-              mbar_arrive_expect_tx(bar, C::kStage * (PAIR ? 2 : 1) + (n == 0 ? p.missing_tx : 0u));
-            tma_load_2d<PAIR>(at, &map_a, kb * 128, tm * C::kTileM + rank * 128, counts);
-            tma_load_2d<PAIR>(at + C::kA, &map_w, kb * 128, tn * BN + rank * 128, counts);
-          }
-          __syncwarp();
+          n += k1 - k0;
         }
       }
-      if (lane == 0) {
-        if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
-        *issued = n;
-      }
+      if (lane == 0) *issued = n;
     } else if (warp == 1 && rank == 0) {
+      // One K block after the other, whatever tile it belongs to: every block
+      // begins its sums anew.  S blocks a turn, so that slots, buffers and
+      // descriptors are constants.
       constexpr uint32_t instr = e4m3_instr(C::kTileM, BN);
-      RingSlot<S> st;
-      RingSlot<NB> tb;
-      bool ok = true, filled = false;   // filled: every buffer was used once
-      for (int64_t tile = first; tile < tiles && ok; tile += step) {
-        for (int kb = 0; kb < p.kblocks; ++kb, st.advance()) {
-          // addresses first: behind the waits only the matrix instructions are left
-          const uint64_t da = operand_desc(sbase + st.i * C::kStage);
-          const uint64_t dw = operand_desc(sbase + st.i * C::kStage + C::kA);
-          const uint32_t d = tmem + tb.i * BN;
-          const uint32_t release = empty + 8 * st.i, ready = tfull + 8 * tb.i;
-          if ((filled && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop)) ||
-              !warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop)) {
-            ok = false;
-            break;
-          }
+      static_assert(S % NB == 0, "a turn goes round both rings");
+      constexpr uint32_t flips = S / NB % 2;   // whether a turn flips the buffers' parity
+      const uint32_t da = operand_desc(sbase), dw = operand_desc(sbase + C::kA);
+      const int64_t blocks = first < tiles ? ((tiles - first + step - 1) / step) * p.kblocks : 0;
+      uint32_t parity = 0, stored = 0, drained = 1;   // answers on the block to come
+      for (int64_t n = 0; n < blocks && !late; n += S, parity ^= 1u) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          if (n + i >= blocks) break;
+          bar_wait(tempty + 8 * (i % NB), (parity & flips) ^ (i / NB & 1) ^ 1u, p.wait_limit_ns,
+                   stop_at, late, drained);
+          bar_wait(full + 8 * i, parity, p.wait_limit_ns, stop_at, late, stored);
+          constexpr int kLast = S - 1;
+          const int j = i == kLast ? 0 : i + 1;
+          const uint32_t turn = i == kLast ? parity ^ 1u : parity;
+          stored = bar_test(full + 8 * j, turn);
+          drained = bar_test(tempty + 8 * (j % NB), (turn & flips) ^ (j / NB & 1) ^ 1u);
           tcgen05_fence_after();
-          if (elect_one()) {
-            mma_block<PAIR>(d, da, dw, instr);
-            mma_commit<PAIR>(release);
-            mma_commit<PAIR>(ready);
+          if (leader) {
+            constexpr uint32_t kNext = C::kStage >> 4;
+            mma_block<PAIR>(tmem + i % NB * BN, da + i * kNext, dw + i * kNext, instr);
+            mma_commit<PAIR>(tfull + 8 * (i % NB));
+            mma_commit<PAIR>(empty + 8 * i);
           }
           __syncwarp();
-          filled |= tb.i == NB - 1;
-          tb.advance();
         }
       }
-      if (!ok && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
     } else if (warp > 1) {
-      // scale warps: lanes 8 r .. 8 r + 7 copy the eight scales of a row
+      // scale warps: lanes 8 r .. 8 r + 7 copy the eight scales of a row; of W
+      // without ROWS, the eight of each 128-row block
       const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
       RingSlot<kPieces> pc;
-      bool ok = true, filled = false;
-      for (int64_t tile = first; tile < tiles && ok; tile += step) {
+      for (int64_t tile = first; tile < tiles && !late; tile += step) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
-        for (int k0 = 0; k0 < p.kblocks; k0 += kChunk) {
-          if (filled &&
-              !warp_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop)) {
-            ok = false;
-            break;
-          }
+        const int64_t m0 = (int64_t)tm * C::kTileM + rank * 128, n0 = (int64_t)tn * BN;
+        for (int k0 = 0; k0 < p.kblocks && !late; k0 += kChunk) {
+          bar_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop_at, late);
           const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
           const bool in = k0 + kl < p.kblocks;
-          const int64_t m0 = (int64_t)tm * C::kTileM + rank * 128;
-          const int rows = (int)min64(128, p.M - m0);   // may be <= 0
-          const float* sa = p.sa + m0 * p.kblocks + k0 + kl;
 #pragma unroll 4
           for (int r = sub; r < 128; r += 8) {
-            const bool here = in && r < rows;
-            copy_async_f32(dst + 4 * r, here ? sa + (int64_t)r * p.kblocks : p.sa, here);
+            const bool here = in && m0 + r < p.M;
+            copy_async_f32(dst + 4 * r, here ? p.sa + (m0 + r) * p.kblocks + k0 + kl : p.sa, here);
           }
-          const int64_t w0 = ROWS ? (int64_t)tn * BN : (int64_t)tn * (BN / 128);
-          const int cols = (int)min64(ROWS ? BN : BN / 128, (ROWS ? p.N : (p.N + 127) / 128) - w0);
-          const float* sw = p.sw + w0 * p.kblocks + k0 + kl;
 #pragma unroll 4
           for (int r = sub; r < (ROWS ? BN : BN / 128); r += 8) {
-            const bool here = in && r < cols;
-            copy_async_f32(dst + 4 * (128 + r), here ? sw + (int64_t)r * p.kblocks : p.sw, here);
+            const int64_t n = n0 + (ROWS ? r : 128 * r);
+            const bool here = in && n < p.N;
+            const int64_t w = ROWS ? n : n / 128;
+            copy_async_f32(dst + 4 * (128 + r), here ? p.sw + w * p.kblocks + k0 + kl : p.sw, here);
           }
           copy_async_arrive(sfull + 8 * pc.i);
-          filled |= pc.i == kPieces - 1;
           pc.advance();
         }
       }
     }
   } else {
-    if (BN == 256) registers_up<kWideRegsUp>();
-    // epilogue warps: four cover the 128 rows, two such groups the BN columns
-    constexpr int COLS = BN / 2, LD = BN == 256 ? 32 : 16;
+    if (PAIR) registers_up<C::kRegsUp>();
+    constexpr int COLS = C::kCols, STEPS = COLS / 32;   // even: a block's first load goes to v[0]
     const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-    const int wblock = ROWS ? group * COLS : group * COLS / 128;
-    constexpr int STEPS = COLS / LD;   // even: a block's first load goes where it began
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32u << 16) + COLS * group;
+    const int wblock = ROWS ? COLS * group : COLS * group / 128;
+    const uint32_t drained = PAIR ? map_to_rank(tempty, 0) : tempty;
     RingSlot<NB> tb;
     RingSlot<kPieces> pc;
-    uint32_t v[2][LD];
+    uint32_t v[2][32];
     // the block in buffer tb is there: its first columns are on their way
-    auto begin = [&] {
-      if (!warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) return false;
+    const float* sc = nullptr;
+    auto begin = [&](uint32_t ready) {
+      bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late, ready);
+      __syncwarp();
       tcgen05_fence_after();
-      tmem_load(v[0], tmem + tb.i * BN + group * COLS + lanes);
-      return true;
+      tmem_load(v[0], mine + tb.i * BN);
     };
-    for (int64_t tile = first; tile < tiles; tile += step) {
+    for (int64_t tile = first; tile < tiles && !late; tile += step) {
       int tm, tn;
       tile_at(p, tile, &tm, &tn);
-      uint64_t acc[COLS / 2];   // pairs of columns
+      float acc[COLS];
 #pragma unroll
-      for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
-      bool ok = begin();
-      for (int kb = 0; kb < p.kblocks && ok; ++kb) {
-        const int in_piece = kb & (kChunk - 1);
-        if (in_piece == 0 &&
-            !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) {
-          ok = false;
-          break;
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      // a block's scales are asked for a block ahead: shared memory is busy
+      auto scale = [&] { return ROWS ? sc[row] : sc[row] * sc[128 + wblock]; };
+      bar_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop_at, late);
+      __syncwarp();
+      sc = scales + pc.i * kChunk * C::kScales;
+      float next = scale();
+      begin(0);
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        const float s = next;
+        const float* scw = sc + 128 + wblock;
+        const bool more = kb + 1 < p.kblocks, turn = (kb & (kChunk - 1)) == kChunk - 1;
+        const int piece = pc.i;
+        sc += C::kScales;
+        if (turn || !more) {
+          pc.advance();
+          if (more) {
+            bar_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop_at, late);
+            __syncwarp();
+            sc = scales + pc.i * kChunk * C::kScales;
+          }
         }
-        const float* sc = scales + (pc.i * kChunk + in_piece) * C::kScales;
-        const float s = ROWS ? sc[row] : sc[row] * sc[128 + wblock];
-        const uint64_t ss = f2(s, s);
-        const uint32_t at = tmem + tb.i * BN + group * COLS + lanes;
+        if (more) next = scale();
+        const uint32_t at = mine + tb.i * BN;
+        uint32_t ready = 0;
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {
           tmem_wait(v[j & 1]);
           if (j + 1 < STEPS) {
-            tmem_load(v[(j + 1) & 1], at + LD * (j + 1));
+            tmem_load(v[(j + 1) & 1], at + 32 * (j + 1));
+            if (j + 2 == STEPS) {
+              RingSlot<NB> nx = tb;
+              nx.advance();
+              ready = bar_test(tfull + 8 * nx.i, nx.parity);
+            }
           } else {   // all in registers: the buffer is free, the next block begins
             tcgen05_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (PAIR)
-                mbar_arrive_cluster(map_to_rank(tempty + 8 * tb.i, 0));
-              else
-                mbar_arrive(tempty + 8 * tb.i);
-            }
+            arrive_if<PAIR>(drained + 8 * tb.i, lane == 0);
             tb.advance();
-            if (kb + 1 < p.kblocks) ok = begin();
+            if (more) begin(ready);
           }
+          // one fma per value: in pairs (f32x2) the loaded registers are no operands
+          // without two moves for each pair, 121 instructions for 64 values
 #pragma unroll
-          for (int i = 0; i < LD / 2; i += 2) {
-            uint64_t x0 = (uint64_t)v[j & 1][2 * i + 1] << 32 | v[j & 1][2 * i];
-            uint64_t x1 = (uint64_t)v[j & 1][2 * i + 3] << 32 | v[j & 1][2 * i + 2];
+          for (int i = 0; i < 32; i += 4) {
+            float4 w = make_float4(s, s, s, s);
             if (ROWS) {
-              const ulonglong2 w =
-                  *reinterpret_cast<const ulonglong2*>(sc + 128 + wblock + LD * j + 2 * i);
-              x0 = f2_mul(x0, w.x);
-              x1 = f2_mul(x1, w.y);
+              w = *reinterpret_cast<const float4*>(scw + 32 * j + i);
+              w.x *= s, w.y *= s, w.z *= s, w.w *= s;
             }
-            acc[LD / 2 * j + i] = f2_fma(x0, ss, acc[LD / 2 * j + i]);
-            acc[LD / 2 * j + i + 1] = f2_fma(x1, ss, acc[LD / 2 * j + i + 1]);
+            const uint32_t* x = &v[j & 1][i];
+            float* a = acc + 32 * j + i;
+            a[0] = fmaf(__uint_as_float(x[0]), w.x, a[0]);
+            a[1] = fmaf(__uint_as_float(x[1]), w.y, a[1]);
+            a[2] = fmaf(__uint_as_float(x[2]), w.z, a[2]);
+            a[3] = fmaf(__uint_as_float(x[3]), w.w, a[3]);
           }
         }
-        if (in_piece == kChunk - 1 || kb == p.kblocks - 1) {
+        if (turn || !more) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(sempty + 8 * pc.i);
-          pc.advance();
+          arrive_if<false>(sempty + 8 * piece, lane == 0);
         }
       }
-      if (!ok) {
-        if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
-        break;
-      }
+      if (late) break;
       const int64_t m = (int64_t)tm * C::kTileM + rank * 128 + row;
-      const int64_t n0 = (int64_t)tn * BN + group * COLS;
+      const int64_t n0 = (int64_t)tn * BN + COLS * group;
+      const int cols = (int)min64(COLS, p.N - n0);   // may be <= 0
       if (m < p.M) {
-        const int cols = (int)min64(COLS, p.N - n0);   // may be <= 0
         if (p.fp32_out) {
           float* y = static_cast<float*>(p.y) + m * p.N + n0;
 #pragma unroll
           for (int j = 0; j < COLS; j += 8) {
-            const uint64_t* a = acc + j / 2;
+            const float* a = acc + j;
             if (p.vec_out && j + 8 <= cols)
-              st_global_v8(y + j, (uint32_t)a[0], (uint32_t)(a[0] >> 32), (uint32_t)a[1],
-                           (uint32_t)(a[1] >> 32), (uint32_t)a[2], (uint32_t)(a[2] >> 32),
-                           (uint32_t)a[3], (uint32_t)(a[3] >> 32));
+              st_global_v8(y + j, __float_as_uint(a[0]), __float_as_uint(a[1]),
+                           __float_as_uint(a[2]), __float_as_uint(a[3]), __float_as_uint(a[4]),
+                           __float_as_uint(a[5]), __float_as_uint(a[6]), __float_as_uint(a[7]));
             else
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (j + i < cols) y[j + i] = i & 1 ? f2_hi(a[i / 2]) : f2_lo(a[i / 2]);
+                if (j + i < cols) y[j + i] = a[i];
           }
         } else {
           __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + m * p.N + n0;
 #pragma unroll
           for (int j = 0; j < COLS; j += 16) {
-            const uint64_t* a = acc + j / 2;
+            const float* a = acc + j;
             if (p.vec_out && j + 16 <= cols)
-              st_global_v8(y + j, pack_bf16x2_rn(f2_lo(a[0]), f2_hi(a[0])),
-                           pack_bf16x2_rn(f2_lo(a[1]), f2_hi(a[1])),
-                           pack_bf16x2_rn(f2_lo(a[2]), f2_hi(a[2])),
-                           pack_bf16x2_rn(f2_lo(a[3]), f2_hi(a[3])),
-                           pack_bf16x2_rn(f2_lo(a[4]), f2_hi(a[4])),
-                           pack_bf16x2_rn(f2_lo(a[5]), f2_hi(a[5])),
-                           pack_bf16x2_rn(f2_lo(a[6]), f2_hi(a[6])),
-                           pack_bf16x2_rn(f2_lo(a[7]), f2_hi(a[7])));
+              st_global_v8(y + j, pack_bf16x2_rn(a[0], a[1]), pack_bf16x2_rn(a[2], a[3]),
+                           pack_bf16x2_rn(a[4], a[5]), pack_bf16x2_rn(a[6], a[7]),
+                           pack_bf16x2_rn(a[8], a[9]), pack_bf16x2_rn(a[10], a[11]),
+                           pack_bf16x2_rn(a[12], a[13]), pack_bf16x2_rn(a[14], a[15]));
             else
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (j + i < cols)
-                  y[j + i] = __float2bfloat16_rn(i & 1 ? f2_hi(a[i / 2]) : f2_lo(a[i / 2]));
+                if (j + i < cols) y[j + i] = __float2bfloat16_rn(a[i]);
           }
         }
       }
@@ -385,6 +399,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
+  if (late && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
   if (*stop) {
     drain<S, PAIR>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
@@ -458,6 +473,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     }
     mbar_init(done, 1);
     *stop = 0;
+    *issued = 0;
     fence_mbar_init();
     prefetch_tensor_map(&map_a);
     prefetch_tensor_map(&map_w);
@@ -470,59 +486,47 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   grid_dependency_wait();
   allow_dependent_launch();
 
+  const uint32_t stop_at = slot + 4;
+  uint32_t late = 0;
+  const bool leader = elect_one();
   float acc[TN];
   if (warp == 0) {
     RingSlot<S> st;
-    bool ok = true;
-    int n = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++n, st.advance()) {
-      if (n >= S && !warp_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop)) {
-        ok = false;
-        break;
-      }
+    for (int kb = kb0; kb < kb1 && !late; ++kb, st.advance()) {
       const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar, C::kStage + (n == 0 ? p.missing_tx : 0u));
+      bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
+      if (leader) {
+        mbar_arrive_expect_tx(bar, C::kStage + (kb == kb0 ? p.missing_tx : 0u));
         tma_load_2d<false>(at, &map_w, kb * 128, tn * 128, bar);
         tma_load_2d<false>(at + C::kW, &map_a, kb * 128, tm * TN, bar);
+        *issued = kb + 1 - kb0;
       }
       __syncwarp();
-    }
-    if (lane == 0) {
-      if (!ok) atomicOr(&g_gemm_status, kStatusTimeout);
-      *issued = n;
     }
   } else if (warp == 1) {
     constexpr uint32_t instr = e4m3_instr(128, TN);
     RingSlot<S> st;
     RingSlot<NB> tb;
-    bool ok = true;
-    for (int n = 0; n < kb1 - kb0; ++n, st.advance(), tb.advance()) {
-      const uint64_t dw = operand_desc(sbase + st.i * C::kStage);
-      const uint64_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
+    for (int kb = kb0; kb < kb1 && !late; ++kb, st.advance(), tb.advance()) {
+      const uint32_t dw = operand_desc(sbase + st.i * C::kStage);
+      const uint32_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
       const uint32_t d = tmem + tb.i * C::kBufCols;
       const uint32_t release = empty + 8 * st.i, ready = tfull + 8 * tb.i;
-      if ((n >= NB && !warp_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop)) ||
-          !warp_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop)) {
-        ok = false;
-        break;
-      }
+      bar_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop_at, late);
+      bar_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop_at, late);
       tcgen05_fence_after();
-      if (elect_one()) {
+      if (leader) {
         mma_block<false>(d, dw, da, instr);
-        mma_commit<false>(release);
         mma_commit<false>(ready);
+        mma_commit<false>(release);
       }
       __syncwarp();
     }
-    if (!ok && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
   } else if (warp < 4) {
     const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
     RingSlot<kPieces> pc;
-    for (int k0 = kb0; k0 < kb1; k0 += kChunk, pc.advance()) {
-      if (k0 - kb0 >= kPieces * kChunk &&
-          !warp_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop))
-        break;
+    for (int k0 = kb0; k0 < kb1 && !late; k0 += kChunk, pc.advance()) {
+      bar_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
       const bool in = k0 + kl < kb1;
 #pragma unroll 4
@@ -546,15 +550,15 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     for (int j = 0; j < TN; ++j) acc[j] = 0.f;
     RingSlot<NB> tb;
     RingSlot<kPieces> pc;
-    for (int n = 0; n < kb1 - kb0; ++n, tb.advance()) {
-      if ((n % kChunk == 0 &&
-           !warp_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop)) ||
-          !warp_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop)) {
-        if (lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
-        break;
+    const float* sc = nullptr;
+    for (int n = 0; n < kb1 - kb0 && !late; ++n, tb.advance(), sc += C::kScales) {
+      if (n % kChunk == 0) {
+        bar_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop_at, late);
+        sc = scales + pc.i * kChunk * C::kScales;
       }
+      bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late);
+      __syncwarp();
       tcgen05_fence_after();
-      const float* sc = scales + (pc.i * kChunk + n % kChunk) * C::kScales;
       const float sw = sc[TN + (ROWS ? row : 0)];
       const uint32_t at = tmem + tb.i * C::kBufCols + lanes;
       uint32_t v[2][16];
@@ -570,16 +574,17 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       }
       tcgen05_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(tempty + 8 * tb.i);
-        if (n % kChunk == kChunk - 1) mbar_arrive(sempty + 8 * pc.i);
+      arrive_if<false>(tempty + 8 * tb.i, lane == 0);
+      if (n % kChunk == kChunk - 1) {
+        arrive_if<false>(sempty + 8 * pc.i, lane == 0);
+        pc.advance();
       }
-      if (n % kChunk == kChunk - 1) pc.advance();
     }
   }
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
+  if (late && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
   if (*stop) {
     drain<S, false>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
@@ -730,7 +735,7 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
     if (rc != NTS_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = cluster_attribute(cluster);
-    cfg.blockDim = dim3(kWideThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kLaunch;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -740,8 +745,8 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
   const unsigned grid = (unsigned)(std::min(tiles, most) * cluster);
   log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide %dx%d grid=%u", (long long)p.M,
              (long long)p.N, (long long)rq.K, C::kTileM, BN, grid);
-  return launch(wide_kernel<BN, ROWS>, rq, p, 128, 128, dim3(grid), kWideThreads,
-                C::kPair ? kWideRegs : 0, C::kLaunch, cluster, stream, tune.pdl != 0);
+  return launch(wide_kernel<BN, ROWS>, rq, p, 128, C::kRowsW, dim3(grid), C::kThreads, C::kRegs,
+                C::kLaunch, cluster, stream, tune.pdl != 0);
 }
 
 }  // namespace
