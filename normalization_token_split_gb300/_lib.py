@@ -1,17 +1,20 @@
-"""ctypes loader of the in-tree libnts.so.  There is no fallback: if the
-library has not been built (``normalization_token_split_gb300.build``) every
-call raises."""
+"""Loader of the in-tree libnts.so (ctypes) and of the extension that passes
+torch tensors to it (marshal_nts.so).  There is no fallback: if they have not
+been built (``normalization_token_split_gb300.build``) every call raises."""
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libnts.so")
+MARSHAL_PATH = os.path.join(_HERE, "_build", "marshal_nts.so")
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
 
 NTS_OK = 0
 STATUS_NAMES = {0: "NTS_OK", 1: "NTS_ERR_INVALID_ARG", 2: "NTS_ERR_UNSUPPORTED",
@@ -95,6 +98,27 @@ def lib():
             _declare(handle)
             _lib = handle
         return _lib
+
+
+def marshal():
+    """The loaded extension; raises if it was never built."""
+    global _marshal
+    if _marshal is not None:
+        return _marshal
+    lib()
+    with _lock:
+        if _marshal is None:
+            if not os.path.exists(MARSHAL_PATH):
+                raise RuntimeError(
+                    f"marshal_nts.so is not built ({MARSHAL_PATH} missing); run "
+                    "`python -m normalization_token_split_gb300.build`")
+            import torch  # noqa: F401  (its libraries come first)
+            spec = importlib.util.spec_from_file_location("marshal_nts", MARSHAL_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.set_check(check)
+            _marshal = module
+        return _marshal
 
 
 def check(status: int) -> None:

@@ -1,5 +1,6 @@
 """Builds libnts.so in-tree (normalization_token_split_gb300/_build/) with
-nvcc for sm_103a.  Translation units compile in parallel; a unit is rebuilt
+nvcc for sm_103a, and the Python extension beside it (marshal_nts.so, from
+binding/) with g++.  Translation units compile in parallel; a unit is rebuilt
 only when it or a header is newer than its object.
 
     python -m normalization_token_split_gb300.build [--force] [--verbose]
@@ -8,10 +9,12 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libnts.so")
+BINDING = os.path.join(PKG, "binding", "marshal.cpp")
+MARSHAL = os.path.join(BUILD, "marshal_nts.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -53,6 +58,20 @@ def _compile_cmd(src: str, obj: str, nvcc: str, cuda: str, verbose: bool):
     return cmd
 
 
+def _binding_cmds(obj: str, cuda: str):
+    """Compile and link commands of the Python extension (torch's headers and
+    libraries, this interpreter, libnts.so beside it)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                *[a for i in inc for a in ("-I", i)], "-c", BINDING, "-o", obj]
+    tmp = MARSHAL + f".{os.getpid()}.tmp"
+    link = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libnts.so", "-Wl,-rpath,$ORIGIN",
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return compile_, link, tmp
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
@@ -71,6 +90,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if stale:
             jobs.append(_compile_cmd(src, obj, nvcc, cuda, verbose))
 
+    # the binding: its object compiles along with the others, and links after libnts.so
+    obj = os.path.join(BUILD, "marshal.cpp.o")
+    bind, bind_link, bind_tmp = _binding_cmds(obj, cuda)
+    newest = max(os.path.getmtime(BINDING), os.path.getmtime(os.path.join(INCLUDE, "nts.h")))
+    stale = force or not os.path.exists(obj) or os.path.getmtime(obj) < newest
+    lib_jobs = len(jobs)
+    if stale:
+        jobs.append(bind)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -88,7 +116,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         msg = "\n\n".join(" ".join(c) + "\n" + o for c, o in failed)
         raise RuntimeError("libnts compilation failed:\n" + msg)
 
-    if jobs or not os.path.exists(LIB):
+    if lib_jobs or not os.path.exists(LIB):
         tmp = LIB + f".{os.getpid()}.tmp"
         link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
                 "-lpthread", "-ldl", "-lrt"]
@@ -96,6 +124,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("libnts link failed:\n" + " ".join(link) + "\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
+    if stale or not os.path.exists(MARSHAL):
+        r = subprocess.run(bind_link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("binding link failed:\n" + " ".join(bind_link) + "\n" + r.stdout +
+                               r.stderr)
+        os.replace(bind_tmp, MARSHAL)
     return LIB
 
 

@@ -24,8 +24,21 @@ namespace {
 
 constexpr int kCastThreads = 256;
 constexpr int kCastWarps = kCastThreads / 32;
+constexpr int64_t kRingValues = 4 << 20;   // values of X from which the ring kernel runs
 
-__device__ __forceinline__ float block_scale(float a) { return fmaxf(a, 0x1p-100f) / 448.0f; }
+// kStatusTimeout bits of these kernels.
+__device__ unsigned int g_cast_status;
+
+// fp32(max(a, 2^-100) / 448) by one multiply and two fmas (Brisebarre, Muller
+// and Raina, as div6_rn; the quotient is normal, and equal to the IEEE one for
+// every such a).  An infinite a stays infinite.
+__device__ __forceinline__ float block_scale(float a) {
+  a = fmaxf(a, 0x1p-100f);
+  const float z = 0x1.24924ap-9f;   // fl(1 / 448)
+  const float q = __fmul_rn(a, z);
+  const float s = __fmaf_rn(__fmaf_rn(-q, 448.0f, a), z, q);
+  return a <= 3.402823466e38f ? s : a;
+}
 
 // 16 bf16 (two 16-byte loads; p is 16-byte aligned).
 __device__ __forceinline__ void load16(uint4 (&v)[2], const __nv_bfloat16* p) {
@@ -73,6 +86,10 @@ struct CastParams {
   int segs;             // no norm: warp segments per row
   int64_t pitch;        // transpose: bytes per row of codes
   int tblocks;          // transpose: ceil(T / 128)
+  int64_t ring_units;   // ring: units per row (a whole matrix as one row when blocks never end early)
+  int seg;              // ring: units per warp's part of a row, a multiple of 8
+  uint64_t wait_limit_ns;
+  uint32_t missing_tx;  // test hook: bytes expected on a first stage but never sent
   float eps, inv_d;
 };
 
@@ -160,6 +177,159 @@ __global__ void __launch_bounds__(kCastThreads) blockcast_rows_kernel(const Cast
         if ((lane & 7) == 0) srow[u >> 3] = scale;
       }
     }
+  }
+}
+
+// The same for many rows: persistent warps, each with its own ring of kStages
+// shared-memory stages that its lane 0 keeps filled with 1-D bulk copies, so
+// that the next parts of rows are in flight while one is cast.  A warp's part
+// is at most 128 units (4 KB); with RMSNorm the wpr warps of a row add their
+// sums of squares through shared memory behind a named barrier, and the part
+// is read a second time from shared memory, not kept in registers.  A thread
+// reads the two vectors of its unit in the order that lets the 8 lanes of each
+// shared-memory phase hit distinct banks.
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <bool NORM>
+__global__ void __launch_bounds__(kCastThreads, 3) blockcast_ring_kernel(const CastParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t bars[kCastWarps][kStages];
+  __shared__ float part[2][kCastWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wpr = NORM ? p.wpr : 1;
+  const int rpc = kCastWarps / wpr;
+  const int slot = warp / wpr, sub = warp - slot * wpr;
+  const uint32_t stage = (uint32_t)p.seg * 32;
+  const unsigned char* ring = smem + warp * kStages * stage;
+  const uint32_t bar = smem_addr(&bars[warp][0]);
+  const int swap = (lane >> 2) & 1;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const uint64_t policy = l2_policy_evict_first();
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // items: rows (NORM) or parts of rows; this warp's: first, first + step, ...
+  const int64_t items = p.T * (NORM ? 1 : p.segs);
+  const int64_t first = (int64_t)blockIdx.x * rpc + slot, step = (int64_t)gridDim.x * rpc;
+  const int64_t mine = first < items ? (items - first - 1) / step + 1 : 0;
+  auto place = [&](int64_t n, int64_t* row, int64_t* unit) {
+    const int64_t item = first + n * step;
+    *row = NORM ? item : item / p.segs;
+    *unit = (NORM ? sub : item - *row * p.segs) * p.seg;
+    return (int)min64(p.seg, p.ring_units - *unit);   // units; <= 0: nothing for this warp
+  };
+  auto issue = [&](int64_t n) {
+    int64_t row, unit;
+    const int units = place(n, &row, &unit);
+    if (units <= 0 || lane != 0) return;
+    const int s = (int)(n % kStages);
+    mbar_arrive_expect_tx(bar + 8 * s, (uint32_t)units * 32 + (n == 0 ? p.missing_tx : 0u));
+    bulk_g2s(smem_addr(ring) + s * stage, p.x + (row * p.ring_units + unit) * 16,
+             (uint32_t)units * 32, bar + 8 * s, policy);
+  };
+  for (int64_t n = 0; n < min64(mine, kStages); ++n) issue(n);
+
+  bool dead = false;   // a wait gave up: the rest runs on without data, its barriers met
+  for (int64_t n = 0; n < mine; ++n) {
+    int64_t row, unit;
+    const int units = place(n, &row, &unit);
+    const int s = (int)(n % kStages);
+    if (units > 0 && !dead) {
+      int ok = 1;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(bar + 8 * s, (uint32_t)((n / kStages) & 1), p.wait_limit_ns);
+        if (!ok) {
+          atomicOr(&g_cast_status, kStatusTimeout);
+          for (int64_t j = n; j < min64(mine, n + kStages); ++j)   // copies in flight land
+            (void)mbar_wait_bounded(bar + 8 * (int)(j % kStages),
+                                    (uint32_t)((j / kStages) & 1), p.wait_limit_ns);
+        }
+      }
+      dead = __shfl_sync(0xFFFFFFFFu, ok, 0) == 0;
+    }
+    const unsigned char* x = ring + s * stage;
+    float rinv = 1.f;
+    if (NORM) {
+      uint64_t q0 = 0, q1 = 0;
+      for (int u = lane; u < units; u += 32) {
+        const uint4 a = lds128(x + 32 * u + 16 * swap), b = lds128(x + 32 * u + 16 * (swap ^ 1));
+        uint64_t f;
+        f = bf16x2_to_f2(a.x), q0 = f2_fma(f, f, q0);
+        f = bf16x2_to_f2(a.y), q1 = f2_fma(f, f, q1);
+        f = bf16x2_to_f2(a.z), q0 = f2_fma(f, f, q0);
+        f = bf16x2_to_f2(a.w), q1 = f2_fma(f, f, q1);
+        f = bf16x2_to_f2(b.x), q0 = f2_fma(f, f, q0);
+        f = bf16x2_to_f2(b.y), q1 = f2_fma(f, f, q1);
+        f = bf16x2_to_f2(b.z), q0 = f2_fma(f, f, q0);
+        f = bf16x2_to_f2(b.w), q1 = f2_fma(f, f, q1);
+      }
+      q0 = f2_add(q0, q1);
+      float ss = warp_sum(f2_lo(q0) + f2_hi(q0));
+      if (wpr > 1) {
+        const int buf = (int)(n & 1);   // the other buffer's readers are past this barrier
+        if (lane == 0) part[buf][warp] = ss;
+        named_barrier(1 + slot, 32 * wpr);
+        ss = 0.f;
+        for (int w = 0; w < wpr; ++w) ss += part[buf][slot * wpr + w];
+      }
+      rinv = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
+      if (p.rinv != nullptr && sub == 0 && lane == 0) p.rinv[row] = rinv;
+    }
+    uint8_t* codes = p.codes + (row * p.ring_units + unit) * 16;
+    float* scales = p.scales + row * ((p.ring_units + 7) / 8) + unit / 8;
+    const float* gamma = NORM && p.gamma != nullptr ? p.gamma + unit * 16 : nullptr;
+#pragma unroll 2
+    for (int i = 0; i < units; i += 32) {
+      const int u = i + lane;
+      const bool in = u < units;
+      float f[2][8];   // the unit's halves: values 8 (h ^ swap) .. + 7
+      float a = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int half = h ^ swap;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in) v = lds128(x + 32 * u + 16 * half);
+        bf16x8_to_f32(v, f[h]);
+        if (NORM) {
+          if (gamma != nullptr && in) {
+            const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + 16 * u + 8 * half));
+            const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma + 16 * u + 8 * half) + 1);
+            f[h][0] *= g0.x, f[h][1] *= g0.y, f[h][2] *= g0.z, f[h][3] *= g0.w;
+            f[h][4] *= g1.x, f[h][5] *= g1.y, f[h][6] *= g1.z, f[h][7] *= g1.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[h][j] *= rinv;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) a = fmax3(a, fabsf(f[h][j]), fabsf(f[h][j + 1]));
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+      const float scale = block_scale(a);
+      const float inv = __frcp_rn(scale);
+      uint2 c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        c[h] = make_uint2(
+            cvt_e4m3x4(f[h][0] * inv, f[h][1] * inv, f[h][2] * inv, f[h][3] * inv),
+            cvt_e4m3x4(f[h][4] * inv, f[h][5] * inv, f[h][6] * inv, f[h][7] * inv));
+      if (in) {
+        const uint2 lo = swap ? c[1] : c[0], hi = swap ? c[0] : c[1];
+        __stcs(reinterpret_cast<uint4*>(codes + 16 * u), make_uint4(lo.x, lo.y, hi.x, hi.y));
+        if ((lane & 7) == 0) scales[u >> 3] = scale;
+      }
+    }
+    fence_proxy_async_smem();   // the stage's reads come before the copy that refills it
+    __syncwarp();
+    if (!dead && n + kStages < mine) issue(n + kStages);
   }
 }
 
@@ -296,11 +466,13 @@ CastKernel pick_plain(int upt) {
   }
 }
 
-int launch(CastKernel kern, dim3 grid, const CastParams& p, cudaStream_t stream, bool pdl) {
+int launch(CastKernel kern, dim3 grid, const CastParams& p, cudaStream_t stream, bool pdl,
+           size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kCastThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
@@ -346,9 +518,42 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
                   tune.pdl != 0);
   }
 
+  // Many rows: the ring.  Up to a few MB the launch is over before a ring pays
+  // (its warps start with nothing in flight), and parts of rows below 2 KB
+  // cost more to hand out than to load.
+  const bool norm = rq.kind == kCastNorm;
+  const bool flat = !norm && rq.D % 128 == 0;   // one long row: no block ends early
+  const int64_t units = flat ? rq.T * (rq.D / 16) : p.units;
+  if (tune.force_stages > 0 || (rq.T * rq.D >= kRingValues && units >= 64)) {
+    p.ring_units = units;
+    if (flat) p.T = 1;
+    p.wpr = 1;
+    if (norm)
+      while (p.wpr < kCastWarps && p.units > p.wpr * 128) p.wpr *= 2;
+    const int64_t per = norm ? (p.units + p.wpr - 1) / p.wpr : std::min<int64_t>(units, 128);
+    p.seg = (int)((per + 7) / 8 * 8);
+    const int64_t segs = (units + p.seg - 1) / p.seg;
+    if (!norm && segs >= (1ll << 31)) return fail(NTS_ERR_UNSUPPORTED, "matrix too large");
+    p.segs = (int)segs;
+    p.wait_limit_ns = tune.wait_limit_ns;
+    p.missing_tx = tune.missing_tx;
+    const size_t smem = (size_t)kCastWarps * kStages * p.seg * 32;
+    const CastKernel kern = norm ? blockcast_ring_kernel<true> : blockcast_ring_kernel<false>;
+    int per_sm = 0;
+    int rc = prepare_kernel((const void*)kern, smem);
+    if (rc == NTS_OK) rc = blocks_per_sm((const void*)kern, kCastThreads, smem, &per_sm);
+    if (rc != NTS_OK) return rc;
+    const int rpc = kCastWarps / p.wpr;
+    const int64_t need = (p.T * (norm ? 1 : segs) + rpc - 1) / rpc;
+    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)per_sm * dev.sm_count);
+    log_launch(norm ? "rmsnorm_blockcast" : "blockcast", "T=%lld D=%d ring seg=%d wpr=%d grid=%u",
+               (long long)rq.T, p.D, p.seg, p.wpr, grid);
+    return launch(kern, dim3(grid), p, stream, tune.pdl != 0, smem);
+  }
+
   int upt;
   int64_t ctas;
-  if (rq.kind == kCastNorm) {
+  if (norm) {
     // The fewest units per thread that still fill the GPU: more threads per
     // row while the rows alone leave SMs idle.
     p.wpr = 1;
@@ -365,11 +570,21 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
     ctas = (p.T * p.segs + kCastWarps - 1) / kCastWarps;
   }
   const unsigned grid = (unsigned)std::min<int64_t>(ctas, 1 << 24);
-  log_launch(rq.kind == kCastNorm ? "rmsnorm_blockcast" : "blockcast",
+  log_launch(norm ? "rmsnorm_blockcast" : "blockcast",
              "T=%lld D=%d upt=%d wpr=%d segs=%d grid=%u", (long long)p.T, p.D, upt, p.wpr, p.segs,
              grid);
-  return launch(rq.kind == kCastNorm ? pick_norm(upt) : pick_plain(upt), dim3(grid), p, stream,
+  return launch(norm ? pick_norm(upt) : pick_plain(upt), dim3(grid), p, stream,
                 tune.pdl != 0);
+}
+
+int read_and_clear_cast_status(unsigned* out) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_cast_status, sizeof(v));
+  if (e != cudaSuccess) return fail_cuda(e, "reading the cast's status word");
+  if (v != 0) e = cudaMemcpyToSymbol(g_cast_status, &zero, sizeof(zero));
+  if (e != cudaSuccess) return fail_cuda(e, "clearing the cast's status word");
+  *out = v;
+  return NTS_OK;
 }
 
 }  // namespace nts

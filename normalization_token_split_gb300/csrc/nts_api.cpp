@@ -660,18 +660,21 @@ int nts_mxnorm_postround_cast(const void* X_dev, const float* gamma_dev, uint8_t
 int nts_check_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "synchronizing the stream");
-  unsigned qk = 0, mx = 0, gemm = 0, rope = 0;
+  unsigned qk = 0, mx = 0, cast = 0, gemm = 0, rope = 0;
   int rc = read_and_clear_qk_status(&qk);
   if (rc != NTS_OK) return rc;
   rc = read_and_clear_mx_status(&mx);
+  if (rc != NTS_OK) return rc;
+  rc = read_and_clear_cast_status(&cast);
   if (rc != NTS_OK) return rc;
   rc = read_and_clear_gemm_status(&gemm);
   if (rc != NTS_OK) return rc;
   rc = read_and_clear_rope_status(&rope);
   if (rc != NTS_OK) return rc;
-  if ((qk | mx | gemm) != 0)
-    return fail(NTS_ERR_TIMEOUT, "a kernel gave up on a bounded wait (qk=%u mx=%u gemm=%u)", qk, mx,
-                gemm);
+  if ((qk | mx | cast | gemm | (rope & kStatusTimeout)) != 0)
+    return fail(NTS_ERR_TIMEOUT,
+                "a kernel gave up on a bounded wait (qk=%u mx=%u cast=%u gemm=%u rotation=%u)", qk,
+                mx, cast, gemm, rope);
   if (rope != 0)
     return fail(NTS_ERR_INVALID_ARG, "a token position lay outside the rotation table");
   return NTS_OK;

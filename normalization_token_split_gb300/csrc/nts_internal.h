@@ -11,6 +11,10 @@
 
 namespace nts {
 
+// Status bits a kernel ORs into its device status word.
+constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusPosition = 2u;   // a token position outside the rotation table
+
 // A CTA has up to 480 consumer threads (the threads that own data) plus one
 // producer warp that only issues the TMA copies.  512 threads leave up to
 // 128 registers per thread.
@@ -214,6 +218,7 @@ struct GemmRequest {
 };
 int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
 
+int read_and_clear_cast_status(unsigned* out);
 int read_and_clear_rope_status(unsigned* out);
 int read_and_clear_gemm_status(unsigned* out);
 int read_and_clear_qk_status(unsigned* out);

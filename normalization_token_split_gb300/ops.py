@@ -6,12 +6,11 @@ and the current CUDA stream through the C ABI.  Names follow the C ABI
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import check, lib
+from ._lib import check, lib, marshal
 
 FMT_E4M3 = 0
 FMT_E2M1 = 1
@@ -291,8 +290,6 @@ def mxnorm_postround_cast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
 
 # ------------------------------------------ the operators around a projection
 
-BLOCK = 128    # values per scale of the block-scaled 8-bit operands
-
 
 class BlockOut(NamedTuple):
     codes: torch.Tensor     # uint8 [T, D], or [D, Tp] transposed
@@ -300,91 +297,9 @@ class BlockOut(NamedTuple):
     rinv: Optional[torch.Tensor]   # fp32 [T]
 
 
-def _blocks(n: int) -> int:
-    return -(-n // BLOCK)
-
-
-# These calls serve single tokens too, where the host's share of a call is the
-# larger one, so each tensor is looked at once: type, device, layout, address.
-
-def _device(name: str, t: torch.Tensor) -> int:
-    """The current device's index; t has to live there."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _refuse(name: str, t: torch.Tensor, dtype, dev: int) -> None:
-    _need_cuda(name, t, dtype)
-    raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
-
-
-def _flat(name: str, t: torch.Tensor, dtype, dev: int) -> int:
-    """Address of a contiguous tensor on the call's device."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, dtype, dev)
-    return t.data_ptr()
-
-
-def _out(name: str, t: Optional[torch.Tensor], shape: tuple, dtype, dev: int) -> torch.Tensor:
-    """The caller's output buffer, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, device=dev, dtype=dtype)
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, dtype, dev)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
-
-
-def _rows(name: str, t: torch.Tensor, dev: int, shape=None) -> int:
-    """Row stride of a bf16 matrix whose rows are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        _refuse(name, t, torch.bfloat16, dev)
-    if shape is None and t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix [T, heads * head_dim], got {tuple(t.shape)}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    T, H = t.shape
-    row, col = t.stride()
-    if col != 1 and H > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return row if T > 1 else H
-
-
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    def _raw_stream(stream, dev: int) -> int:
-        return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-else:
-    def _raw_stream(stream, dev: int) -> int:
-        return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-
-def _rope_args(q, k, gamma_q, gamma_k, positions, table, d, dev):
-    """What a rotation and its gradient share, checked: (gamma_q's, gamma_k's,
-    positions' and table's addresses, P, T, nheads_q, nheads_k, rot_dim)."""
-    T, hq = q.shape
-    Tk, hk = k.shape
-    if d <= 0 or hq % d != 0 or hk % d != 0:
-        raise ValueError("q and k must hold whole heads of head_dim values")
-    if Tk != T:
-        raise ValueError("q and k must have the same number of tokens")
-    if table.dim() != 2:
-        raise ValueError("table must be a matrix [P, rot_dim]")
-    P, rot = table.shape
-    gq = _flat("gamma_q", gamma_q, torch.float32, dev)
-    gk = _flat("gamma_k", gamma_k, torch.float32, dev)
-    if gamma_q.numel() != d or gamma_k.numel() != d:
-        raise ValueError(f"gamma_q and gamma_k must hold head_dim = {d} values")
-    pos = _flat("positions", positions, torch.int64, dev)
-    if positions.numel() != T:
-        raise ValueError("positions must hold one position per token")
-    return gq, gk, pos, _flat("table", table, torch.float32, dev), P, T, hq // d, hk // d, rot
-
+# The checks, missing outputs and the call itself are in binding/marshal.cpp:
+# these operators serve single tokens, where Python's share of a call would be
+# the larger part of it.
 
 def rope_table(P: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """The rotation table of qknorm_rope: fp32 [P, rot_dim], row pos the
@@ -405,29 +320,8 @@ def qknorm_rope(q: torch.Tensor, gamma_q: torch.Tensor, k: torch.Tensor, gamma_k
     buffer) with the rotary position embedding of positions (int64 [T],
     negative: padding row, zeros out) by table (rope_table).  out_q may be q,
     out_k may be k.  Returns (yq, yk, rinv_q or None, rinv_k or None)."""
-    d = int(head_dim)
-    dev = _device("q", q)
-    ldq, ldk = _rows("q", q, dev), _rows("k", k, dev)
-    gq, gk, pos, tab, P, T, nq, nk, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, d,
-                                                     dev)
-    if out_q is None:
-        out_q, ldyq = torch.empty((T, nq * d), device=dev, dtype=torch.bfloat16), nq * d
-    else:
-        ldyq = _rows("out_q", out_q, dev, q.shape)
-    if out_k is None:
-        out_k, ldyk = torch.empty((T, nk * d), device=dev, dtype=torch.bfloat16), nk * d
-    else:
-        ldyk = _rows("out_k", out_k, dev, k.shape)
-    if want_rinv or rinv_q is not None:
-        rinv_q = _out("rinv_q", rinv_q, (T, nq), torch.float32, dev)
-    if want_rinv or rinv_k is not None:
-        rinv_k = _out("rinv_k", rinv_k, (T, nk), torch.float32, dev)
-    check(lib().nts_qknorm_rope(
-        q.data_ptr(), ldq, gq, out_q.data_ptr(), ldyq,
-        None if rinv_q is None else rinv_q.data_ptr(), k.data_ptr(), ldk, gk, out_k.data_ptr(),
-        ldyk, None if rinv_k is None else rinv_k.data_ptr(), pos, tab, P, T, nq, nk, d, rot,
-        1 if interleaved else 0, eps, _raw_stream(stream, dev)))
-    return out_q, out_k, rinv_q, rinv_k
+    return marshal().qknorm_rope(q, gamma_q, k, gamma_k, positions, table, head_dim, eps,
+                                 interleaved, out_q, out_k, rinv_q, rinv_k, want_rinv, stream)
 
 
 def qknorm_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor,
@@ -444,36 +338,11 @@ def qknorm_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor,
     Returns (dq, dk, dgamma_q, dgamma_k), the gains' gradients in fp32
     [head_dim].  Without a workspace (uint8, rope_backward_workspace bytes)
     one is taken from torch's allocator for the call."""
-    d = int(head_dim)
-    dev = _device("q", q)
-    ldq, ldk = _rows("q", q, dev), _rows("k", k, dev)
-    gq, gk, pos, tab, P, T, nq, nk, rot = _rope_args(q, k, gamma_q, gamma_k, positions, table, d,
-                                                     dev)
-    lddyq, lddyk = _rows("dyq", dyq, dev, q.shape), _rows("dyk", dyk, dev, k.shape)
-    if out_dq is None:
-        out_dq, lddq = torch.empty((T, nq * d), device=dev, dtype=torch.bfloat16), nq * d
-    else:
-        lddq = _rows("out_dq", out_dq, dev, q.shape)
-    if out_dk is None:
-        out_dk, lddk = torch.empty((T, nk * d), device=dev, dtype=torch.bfloat16), nk * d
-    else:
-        lddk = _rows("out_dk", out_dk, dev, k.shape)
-    dgamma_q = _out("dgamma_q", dgamma_q, (d,), torch.float32, dev)
-    dgamma_k = _out("dgamma_k", dgamma_k, (d,), torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(rope_backward_workspace(d), device=dev, dtype=torch.uint8)
-        if stream is not None:
-            workspace.record_stream(stream)   # torch may hand it on only after the call has run
-    ws = _flat("workspace", workspace, torch.uint8, dev)
-    check(lib().nts_qknorm_rope_backward(
-        dyq.data_ptr(), lddyq, dyk.data_ptr(), lddyk, q.data_ptr(), ldq, gq, k.data_ptr(), ldk, gk,
-        pos, tab, P, out_dq.data_ptr(), lddq, out_dk.data_ptr(), lddk, dgamma_q.data_ptr(),
-        dgamma_k.data_ptr(), ws, workspace.numel(), T, nq, nk, d, rot, 1 if interleaved else 0, eps,
-        _raw_stream(stream, dev)))
-    return out_dq, out_dk, dgamma_q, dgamma_k
+    return marshal().qknorm_rope_backward(dyq, dyk, q, gamma_q, k, gamma_k, positions, table,
+                                          head_dim, eps, interleaved, out_dq, out_dk, dgamma_q,
+                                          dgamma_k, workspace, stream)
 
 
-@functools.lru_cache(maxsize=None)
 def rope_backward_workspace(head_dim: int) -> int:
     """Workspace bytes of qknorm_rope_backward."""
     n = ctypes.c_int64()
@@ -487,22 +356,8 @@ def rmsnorm_blockcast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps
     """RMSNorm of x [T, D] (bf16) fused with the cast to E4M3 codes with an
     fp32 scale per 128 values: BlockOut(codes [T, D], scales [T, ceil(D/128)],
     rinv or None)."""
-    dev = _device("x", x)
-    px = _flat("x", x, torch.bfloat16, dev)
-    T, D = x.shape
-    pg = None
-    if gamma is not None:
-        pg = _flat("gamma", gamma, torch.float32, dev)
-        if gamma.numel() != D:
-            raise ValueError(f"gamma must hold D = {D} values, got {gamma.numel()}")
-    codes = _out("codes", codes, (T, D), torch.uint8, dev)
-    scales = _out("scales", scales, (T, _blocks(D)), torch.float32, dev)
-    if want_rinv or rinv is not None:
-        rinv = _out("rinv", rinv, (T,), torch.float32, dev)
-    check(lib().nts_rmsnorm_blockcast(px, pg, codes.data_ptr(), scales.data_ptr(),
-                                      None if rinv is None else rinv.data_ptr(), T, D, eps,
-                                      _raw_stream(stream, dev)))
-    return BlockOut(codes, scales, rinv)
+    return BlockOut(*marshal().rmsnorm_blockcast(x, gamma, eps, codes, scales, rinv, want_rinv,
+                                                 stream))
 
 
 def blockcast(x: torch.Tensor, block_rows: int = 1, codes=None, scales=None,
@@ -510,37 +365,14 @@ def blockcast(x: torch.Tensor, block_rows: int = 1, codes=None, scales=None,
     """Cast of x [T, D] (bf16) to E4M3 codes with an fp32 scale per block of
     block_rows x 128 values (1: activations, 128: weights):
     BlockOut(codes [T, D], scales [ceil(T/block_rows), ceil(D/128)], None)."""
-    dev = _device("x", x)
-    px = _flat("x", x, torch.bfloat16, dev)
-    T, D = x.shape
-    if block_rows not in (1, 128):
-        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
-    codes = _out("codes", codes, (T, D), torch.uint8, dev)
-    scales = _out("scales", scales, (-(-T // block_rows), _blocks(D)), torch.float32, dev)
-    check(lib().nts_blockcast(px, codes.data_ptr(), scales.data_ptr(), T, D, block_rows,
-                              _raw_stream(stream, dev)))
-    return BlockOut(codes, scales, None)
+    return BlockOut(*marshal().blockcast(x, block_rows, codes, scales, stream))
 
 
 def blockcast_t(x: torch.Tensor, codes=None, scales=None, stream=None) -> BlockOut:
     """The transpose of x [T, D] (bf16) as E4M3 codes with an fp32 scale per
     128 tokens of a column: BlockOut(codes [D, Tp], scales [D, ceil(T/128)],
     None), Tp = T rounded up to a multiple of 16 (zero codes beyond T)."""
-    dev = _device("x", x)
-    px = _flat("x", x, torch.bfloat16, dev)
-    T, D = x.shape
-    codes = _out("codes", codes, (D, -(-T // 16) * 16), torch.uint8, dev)
-    scales = _out("scales", scales, (D, _blocks(T)), torch.float32, dev)
-    check(lib().nts_blockcast_t(px, codes.data_ptr(), scales.data_ptr(), T, D,
-                                _raw_stream(stream, dev)))
-    return BlockOut(codes, scales, None)
-
-
-def _codes(name: str, t: torch.Tensor, dev: int) -> int:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    return _flat(name, t, torch.float8_e4m3fn if t.dtype is torch.float8_e4m3fn else torch.uint8,
-                 dev)
+    return BlockOut(*marshal().blockcast_t(x, codes, scales, stream))
 
 
 def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
@@ -549,34 +381,11 @@ def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: tor
     """Y = A W^T of E4M3 operands (uint8 or float8_e4m3fn) with an fp32 scale
     per 128 values along K: a_codes [M, K] with a_scales [M, ceil(K/128)],
     w_codes [N, K] with w_scales [ceil(N/128), ceil(K/128)] (128 x 128 blocks)
-    or [N, ceil(K/128)].  Returns Y [M, N], bf16 or fp32."""
-    dev = _device("a_codes", a_codes)
-    pa, pw = _codes("a_codes", a_codes, dev), _codes("w_codes", w_codes, dev)
-    M, K = a_codes.shape
-    N, Kw = w_codes.shape
-    if Kw != K:
-        raise ValueError("a_codes and w_codes must have the same K")
-    psa = _flat("a_scales", a_scales, torch.float32, dev)
-    psw = _flat("w_scales", w_scales, torch.float32, dev)
-    kb = _blocks(K)
-    if a_scales.shape != (M, kb):
-        raise ValueError(f"a_scales must have shape {(M, kb)}, got {tuple(a_scales.shape)}")
-    if w_scales.shape == (_blocks(N), kb):
-        rows = 128
-    elif w_scales.shape == (N, kb):
-        rows = 1
-    else:
-        raise ValueError(f"w_scales must have shape {(_blocks(N), kb)} or {(N, kb)}, "
-                         f"got {tuple(w_scales.shape)}")
-    if out is not None:
-        out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    or [N, ceil(K/128)].  Returns Y [M, N], bf16 or fp32 (out_dtype, or out's)."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
-    out = _out("out", out, (M, N), out_dtype, dev)
-    check(lib().nts_gemm_blockscaled(pa, psa, pw, psw, rows, out.data_ptr(),
-                                     1 if out_dtype is torch.float32 else 0, M, N, K,
-                                     _raw_stream(stream, dev)))
-    return out
+    return marshal().gemm_blockscaled(a_codes, a_scales, w_codes, w_scales, out,
+                                      out_dtype is torch.float32, stream)
 
 
 def mxnorm_correction(B: int, p: int) -> float:

@@ -68,6 +68,51 @@ def test_blockcast_t(T, D):
     assert torch.equal(o.codes.cpu(), ref.block_codes(xt, scales, 1))
 
 
+@pytest.mark.parametrize("T,D", SHAPES + [(127, 112), (129, 272), (2, 65536 + 16), (3001, 2048)])
+def test_ring_kernel_on_any_shape(T, D):
+    """The kernel of large calls, forced: equal to the small calls' bit for bit."""
+    x = rows(T, D, T + D + 3).to(DEV)
+    gamma = 1.0 + 0.1 * torch.randn(D, generator=torch.Generator().manual_seed(2)).to(DEV)
+    try:
+        nts.set_tuning(stages=2)
+        plain = nts.blockcast(x)
+        normed = [nts.rmsnorm_blockcast(x, g, want_rinv=True) for g in (None, gamma)] \
+            if D <= 32768 else []
+        nts.check_status()
+    finally:
+        nts.set_tuning()
+    scales = ref.block_scales(x.float().cpu(), 1)
+    assert torch.equal(plain.scales.cpu(), scales)
+    assert torch.equal(plain.codes.cpu(), ref.block_codes(x.float().cpu(), scales, 1))
+    for o, g in zip(normed, (None, gamma)):
+        rinv = o.rinv.cpu()
+        want = (x.cpu().double().square().mean(1) + EPS).rsqrt()
+        assert torch.all((rinv.double() - want).abs() <= (D / 2 + 4) * ref.U32 * want)
+        w = (x.float() if g is None else x.float() * g).cpu() * rinv[:, None]
+        scales = ref.block_scales(w, 1)
+        assert torch.equal(o.scales.cpu(), scales)
+        assert torch.equal(o.codes.cpu(), ref.block_codes(w, scales, 1))
+
+
+def test_missing_copy_times_out_and_the_context_lives():
+    x = rows(700, 5120, 1).to(DEV)
+    want = nts.rmsnorm_blockcast(x)
+    nts.check_status()
+    nts.set_wait_limit_ns(20_000_000)
+    nts.set_missing_tx(16)
+    nts.set_tuning(stages=2)
+    try:
+        nts.rmsnorm_blockcast(x)
+        with pytest.raises(nts.NtsError, match="TIMEOUT"):
+            nts.check_status()
+    finally:
+        nts.set_tuning()
+        nts.set_missing_tx(0)
+        nts.set_wait_limit_ns(0)
+    assert torch.equal(nts.rmsnorm_blockcast(x).codes, want.codes)
+    nts.check_status()
+
+
 def test_zero_tiny_and_huge_blocks():
     x = torch.zeros(4, 512)
     x[1, 128:256] = 2.0 ** -120              # below the floor of the absmax

@@ -99,6 +99,47 @@ def test_backward(T, hq, hk, d, rot, packed, pad, il):
         assert torch.all((dg.cpu().double() - wg).abs() <= bg)
 
 
+@pytest.mark.parametrize("rows,stages", [(1, 2), (2, 3), (5, 1)])
+@pytest.mark.parametrize("T,hq,hk,d,rot,packed,pad", SHAPES)
+def test_ring_kernels_on_any_shape(T, hq, hk, d, rot, packed, pad, rows, stages):
+    """The kernels of large calls, forced with other rings."""
+    c = make(T, hq, hk, d, rot, seed=3 * T + d, packed=packed, pad=pad)
+    il = (T + d) % 2 == 0
+    try:
+        nts.set_tuning(rows=rows, stages=stages)
+        yq, yk, _, _ = forward(c, d, il)
+        dq, dk, dgq, dgk = backward(c, d, il)
+        nts.check_status()
+    finally:
+        nts.set_tuning()
+    for y, dx, dg, dy, x, g in ((yq, dq, dgq, c["dyq"], c["q"], c["gq"]),
+                                (yk, dk, dgk, c["dyk"], c["k"], c["gk"])):
+        want, _, bound = ref.rope_forward(x, g, c["pos"], c["table"], d, EPS, il)
+        assert torch.all((y.cpu().double() - want).abs() <= bound)
+        wx, wg, bx, bg = ref.rope_backward(dy, x, g, c["pos"], c["table"], d, EPS, il)
+        assert torch.all((dx.cpu().double() - wx).abs() <= bx)
+        assert torch.all((dg.cpu().double() - wg).abs() <= bg)
+
+
+def test_missing_copy_times_out_and_the_context_lives():
+    c = make(50, 8, 2, 128, 128, seed=2)
+    want = forward(c, 128, False)
+    for fn in (forward, backward):
+        nts.set_wait_limit_ns(20_000_000)
+        nts.set_missing_tx(16)
+        nts.set_tuning(rows=1, stages=2)
+        try:
+            fn(c, 128, False)
+            with pytest.raises(nts.NtsError, match="TIMEOUT"):
+                nts.check_status()
+        finally:
+            nts.set_tuning()
+            nts.set_missing_tx(0)
+            nts.set_wait_limit_ns(0)
+    assert torch.equal(forward(c, 128, False)[0], want[0])
+    nts.check_status()
+
+
 def test_backward_against_differences():
     """Central differences of the fp64 forward formula, in every input value."""
     T, hq, hk, d, rot, il = 3, 2, 1, 32, 16, True
