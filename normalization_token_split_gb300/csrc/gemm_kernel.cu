@@ -50,7 +50,6 @@ struct GemmParams {
   int kblocks;
   int tiles_m, tiles_n;  // wide
   int fp32_out;
-  int vec_out;           // rows of y start on 32-byte boundaries
   uint64_t wait_limit_ns;
   uint32_t missing_tx;   // test hook: bytes expected on the first stage but never sent
 };
@@ -82,6 +81,13 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
 
 constexpr int kGroupM = 16;   // tiles of A walked before the next tile of W
 
+// Rows of Y that do not start on 32-byte boundaries leave through a little
+// shared memory, 32 rows x 8 columns a warp at a time, so that a warp stores 8
+// neighbouring values of four rows: each thread storing its own row's values
+// one by one touched 32 sectors a store ([2048, 1696] x [5881, 1696]: 139 us
+// then, 42 now).
+constexpr int kOutPitch = 9, kOutWarp = 32 * kOutPitch;   // floats
+
 // BN = 256: a pair of CTAs works on 256 rows of A by 256 rows of W.  Each CTA
 // holds its 128 rows of A and half of W's rows, so an SM stores and reads 32 KB
 // per K block for 512 cycles of matrix instructions.  BN = 128: one CTA, 128
@@ -107,7 +113,8 @@ struct Wide {
   static constexpr int kBufs = kPair ? 2 : 3;             // at most 512 columns; divides kStages
   static constexpr int kScales = 128 + (ROWS ? BN : 4);   // floats per K block
   static constexpr uint32_t kScaleOff = kStages * kStage;
-  static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
+  static constexpr uint32_t kOutOff = kScaleOff + kPieces * kChunk * kScales * 4;
+  static constexpr uint32_t kBarOff = kOutOff + 8 * kOutWarp * 4;
   static constexpr uint32_t kBytes = kBarOff + 256;
   static constexpr uint32_t kLaunch = kBytes + 1024;      // the base is rounded up to 1024
 };
@@ -121,7 +128,9 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int64_t tile, int* 
   *tm = (int)(g * kGroupM + (in - (int64_t)*tn * rows));
 }
 
-template <int BN, bool ROWS>
+// VEC: rows of Y start on 32-byte boundaries (a template parameter: with both
+// ways out in one kernel the aligned one was 4 % slower).
+template <int BN, bool ROWS, bool VEC>
 __global__ void __launch_bounds__(Wide<BN, ROWS>::kThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
             const GemmParams p) {
@@ -359,39 +368,60 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
       }
       if (late) break;
-      const int64_t m = (int64_t)tm * C::kTileM + rank * 128 + row;
+      const int64_t m0 = (int64_t)tm * C::kTileM + rank * 128 + (warp & 3) * 32;
       const int64_t n0 = (int64_t)tn * BN + COLS * group;
-      const int cols = (int)min64(COLS, p.N - n0);   // may be <= 0
-      if (m < p.M) {
-        if (p.fp32_out) {
-          float* y = static_cast<float*>(p.y) + m * p.N + n0;
+      const int rows = (int)min64(32, p.M - m0), cols = (int)min64(COLS, p.N - n0);   // may be <= 0
+      float* yf = static_cast<float*>(p.y) + m0 * p.N + n0;
+      __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + m0 * p.N + n0;
+      if (VEC) {
+        // N a multiple of 8 (fp32) or 16: whole 32-byte pieces
+        if (lane < rows) {
+          if (p.fp32_out) {
 #pragma unroll
-          for (int j = 0; j < COLS; j += 8) {
-            const float* a = acc + j;
-            if (p.vec_out && j + 8 <= cols)
-              st_global_v8(y + j, __float_as_uint(a[0]), __float_as_uint(a[1]),
-                           __float_as_uint(a[2]), __float_as_uint(a[3]), __float_as_uint(a[4]),
-                           __float_as_uint(a[5]), __float_as_uint(a[6]), __float_as_uint(a[7]));
-            else
+            for (int j = 0; j < COLS; j += 8) {
+              const float* a = acc + j;
+              if (j < cols)
+                st_global_v8(yf + lane * p.N + j, __float_as_uint(a[0]), __float_as_uint(a[1]),
+                             __float_as_uint(a[2]), __float_as_uint(a[3]), __float_as_uint(a[4]),
+                             __float_as_uint(a[5]), __float_as_uint(a[6]), __float_as_uint(a[7]));
+            }
+          } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (j + i < cols) y[j + i] = a[i];
+            for (int j = 0; j < COLS; j += 16) {
+              const float* a = acc + j;
+              if (j < cols)
+                st_global_v8(yh + lane * p.N + j, pack_bf16x2_rn(a[0], a[1]),
+                             pack_bf16x2_rn(a[2], a[3]), pack_bf16x2_rn(a[4], a[5]),
+                             pack_bf16x2_rn(a[6], a[7]), pack_bf16x2_rn(a[8], a[9]),
+                             pack_bf16x2_rn(a[10], a[11]), pack_bf16x2_rn(a[12], a[13]),
+                             pack_bf16x2_rn(a[14], a[15]));
+            }
           }
-        } else {
-          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + m * p.N + n0;
+        }
+      } else {
+        float* out = reinterpret_cast<float*>(smem + C::kOutOff) + (warp - 4) * kOutWarp;
+        const int c = lane & 7;
 #pragma unroll
-          for (int j = 0; j < COLS; j += 16) {
-            const float* a = acc + j;
-            if (p.vec_out && j + 16 <= cols)
-              st_global_v8(y + j, pack_bf16x2_rn(a[0], a[1]), pack_bf16x2_rn(a[2], a[3]),
-                           pack_bf16x2_rn(a[4], a[5]), pack_bf16x2_rn(a[6], a[7]),
-                           pack_bf16x2_rn(a[8], a[9]), pack_bf16x2_rn(a[10], a[11]),
-                           pack_bf16x2_rn(a[12], a[13]), pack_bf16x2_rn(a[14], a[15]));
-            else
+        for (int j = 0; j < COLS; j += 8) {
+          if (j >= cols) break;
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (j + i < cols) y[j + i] = __float2bfloat16_rn(a[i]);
+          for (int i = 0; i < 8; ++i) out[lane * kOutPitch + i] = acc[j + i];
+          __syncwarp();
+          if (j + c < cols) {
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 4) {
+              const int r = r0 + (lane >> 3);
+              const float v = out[r * kOutPitch + c];
+              const int64_t at = r * p.N + j + c;
+              if (r < rows) {
+                if (p.fp32_out)
+                  yf[at] = v;
+                else
+                  yh[at] = __float2bfloat16_rn(v);
+              }
+            }
           }
+          __syncwarp();
         }
       }
     }
@@ -416,19 +446,25 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 
 constexpr int kNarrowThreads = 256;   // TMA, MMA, 2 scale warps, 4 epilogue warps
 
+// A stage holds two K blocks: a role's waits and arrivals cost several hundred
+// cycles whatever a stage holds, more than the copies and instructions of one
+// block.  Two CTAs share an SM: its 512 columns of tensor memory, and shared
+// memory for three stages each (TN = 16) or two.
 template <int TN, bool ROWS>
 struct Narrow {
-  static constexpr int kBufs = 4;                         // two CTAs share an SM's 512 columns
-  static constexpr uint32_t kBufCols = TN < 32 ? 32 : TN;
-  static constexpr uint32_t kCols = kBufCols * kBufs;
-  static constexpr uint32_t kW = 128 * 128;
-  static constexpr uint32_t kStage = kW + TN * 128;
-  static constexpr int kStages = 98304 / (int)kStage;     // 4 (TN = 64) or 5
+  static constexpr int kPer = 2;                          // K blocks per stage
+  static constexpr uint32_t kBufCols = kPer * TN;
+  static constexpr int kBufs = TN == 64 ? 2 : 4;
+  static constexpr uint32_t kCols = kBufCols * kBufs;     // 128 or 256
+  static constexpr uint32_t kW = 128 * 128, kA = TN * 128;
+  static constexpr uint32_t kStage = kPer * (kW + kA);
+  static constexpr int kStages = 110592 / (int)kStage;
   static constexpr int kScales = TN + (ROWS ? 128 : 4);
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
-  static constexpr uint32_t kBytes = kBarOff + 512;
+  static constexpr uint32_t kBytes = kBarOff + 256;
   static constexpr uint32_t kLaunch = kBytes + 1024;
+  static_assert(kChunk % kPer == 0, "a stage's scales lie in one piece");
   static_assert(kScaleOff >= TN * 128 * 4, "the sums for the other CTAs fit the ring");
 };
 
@@ -455,8 +491,10 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   const int rank = (int)cluster_ctarank();
   const int tn = (int)blockIdx.x / split;
   const int tm = (int)blockIdx.y;
-  const int kb0 = (int)((int64_t)p.kblocks * rank / split);
-  const int kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
+  // this CTA's stages: pairs of K blocks; the last pair may lack its second
+  // one, whose copies read zeros behind the matrices' end
+  const int pairs = (p.kblocks + 1) / 2;
+  const int u0 = pairs * rank / split, u1 = pairs * (rank + 1) / split;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -492,14 +530,18 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   float acc[TN];
   if (warp == 0) {
     RingSlot<S> st;
-    for (int kb = kb0; kb < kb1 && !late; ++kb, st.advance()) {
+    for (int u = u0; u < u1 && !late; ++u, st.advance()) {
       const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
       bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       if (leader) {
-        mbar_arrive_expect_tx(bar, C::kStage + (kb == kb0 ? p.missing_tx : 0u));
-        tma_load_2d<false>(at, &map_w, kb * 128, tn * 128, bar);
-        tma_load_2d<false>(at + C::kW, &map_a, kb * 128, tm * TN, bar);
-        *issued = kb + 1 - kb0;
+        mbar_arrive_expect_tx(bar, C::kStage + (u == u0 ? p.missing_tx : 0u));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          tma_load_2d<false>(at + i * C::kW, &map_w, (2 * u + i) * 128, tn * 128, bar);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          tma_load_2d<false>(at + 2 * C::kW + i * C::kA, &map_a, (2 * u + i) * 128, tm * TN, bar);
+        *issued = u + 1 - u0;
       }
       __syncwarp();
     }
@@ -507,16 +549,18 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     constexpr uint32_t instr = e4m3_instr(128, TN);
     RingSlot<S> st;
     RingSlot<NB> tb;
-    for (int kb = kb0; kb < kb1 && !late; ++kb, st.advance(), tb.advance()) {
+    for (int u = u0; u < u1 && !late; ++u, st.advance(), tb.advance()) {
       const uint32_t dw = operand_desc(sbase + st.i * C::kStage);
-      const uint32_t da = operand_desc(sbase + st.i * C::kStage + C::kW);
+      const uint32_t da = operand_desc(sbase + st.i * C::kStage + 2 * C::kW);
       const uint32_t d = tmem + tb.i * C::kBufCols;
       const uint32_t release = empty + 8 * st.i, ready = tfull + 8 * tb.i;
       bar_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       bar_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop_at, late);
       tcgen05_fence_after();
       if (leader) {
-        mma_block<false>(d, dw, da, instr);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          mma_block<false>(d + i * TN, dw + i * (C::kW >> 4), da + i * (C::kA >> 4), instr);
         mma_commit<false>(ready);
         mma_commit<false>(release);
       }
@@ -525,10 +569,10 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   } else if (warp < 4) {
     const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
     RingSlot<kPieces> pc;
-    for (int k0 = kb0; k0 < kb1 && !late; k0 += kChunk, pc.advance()) {
+    for (int k0 = 2 * u0; k0 < 2 * u1 && !late; k0 += kChunk, pc.advance()) {
       bar_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
-      const bool in = k0 + kl < kb1;
+      const bool in = k0 + kl < min(2 * u1, p.kblocks);
 #pragma unroll 4
       for (int r = sub; r < TN; r += 8) {
         const int64_t m = (int64_t)tm * TN + r;
@@ -551,31 +595,40 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     RingSlot<NB> tb;
     RingSlot<kPieces> pc;
     const float* sc = nullptr;
-    for (int n = 0; n < kb1 - kb0 && !late; ++n, tb.advance(), sc += C::kScales) {
-      if (n % kChunk == 0) {
+    for (int u = 0; u < u1 - u0 && !late; ++u, tb.advance(), sc += 2 * C::kScales) {
+      constexpr int kTurn = kChunk / 2;   // stages per piece of scales
+      if (u % kTurn == 0) {
         bar_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop_at, late);
         sc = scales + pc.i * kChunk * C::kScales;
       }
       bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late);
       __syncwarp();
       tcgen05_fence_after();
-      const float sw = sc[TN + (ROWS ? row : 0)];
       const uint32_t at = tmem + tb.i * C::kBufCols + lanes;
+      constexpr int STEPS = 2 * TN / 16;   // the two blocks' columns, 16 at a time
       uint32_t v[2][16];
       tmem_load(v[0], at);
+      const float sw[2] = {sc[TN + (ROWS ? row : 0)], sc[C::kScales + TN + (ROWS ? row : 0)]};
 #pragma unroll
-      for (int j = 0; j < TN / 16; ++j) {
+      for (int j = 0; j < STEPS; ++j) {
+        const int half = j / (STEPS / 2), col = 16 * (j % (STEPS / 2));
         tmem_wait(v[j & 1]);
-        if (j + 1 < TN / 16) tmem_load(v[(j + 1) & 1], at + 16 * (j + 1));
+        if (j + 1 < STEPS) tmem_load(v[(j + 1) & 1], at + 16 * (j + 1));
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          acc[16 * j + i] =
-              fmaf(__uint_as_float(v[j & 1][i]), sw * sc[16 * j + i], acc[16 * j + i]);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(sc + half * C::kScales + col + i);
+          const uint32_t* x = &v[j & 1][i];
+          float* a = acc + col + i;
+          a[0] = fmaf(__uint_as_float(x[0]), sw[half] * s.x, a[0]);
+          a[1] = fmaf(__uint_as_float(x[1]), sw[half] * s.y, a[1]);
+          a[2] = fmaf(__uint_as_float(x[2]), sw[half] * s.z, a[2]);
+          a[3] = fmaf(__uint_as_float(x[3]), sw[half] * s.w, a[3]);
+        }
       }
       tcgen05_fence_before();
       __syncwarp();
       arrive_if<false>(tempty + 8 * tb.i, lane == 0);
-      if (n % kChunk == kChunk - 1) {
+      if (u % kTurn == kTurn - 1) {
         arrive_if<false>(sempty + 8 * pc.i, lane == 0);
         pc.advance();
       }
@@ -729,9 +782,12 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
   p.tiles_n = (int)((p.N + BN - 1) / BN);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   const int cluster = C::kPair ? 2 : 1;
+  const int64_t row_bytes = p.N * (p.fp32_out ? 4 : 2);
+  const bool vec = row_bytes % 32 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
+  const GemmKernel kern = vec ? wide_kernel<BN, ROWS, true> : wide_kernel<BN, ROWS, false>;
   int64_t most = dev.sm_count;
   if (C::kPair) {
-    int rc = prepare_kernel((const void*)wide_kernel<BN, ROWS>, C::kLaunch);
+    int rc = prepare_kernel((const void*)kern, C::kLaunch);
     if (rc != NTS_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = cluster_attribute(cluster);
@@ -739,13 +795,13 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
     cfg.dynamicSmemBytes = C::kLaunch;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    rc = max_active_clusters((const void*)wide_kernel<BN, ROWS>, cfg, cluster, &most);
+    rc = max_active_clusters((const void*)kern, cfg, cluster, &most);
     if (rc != NTS_OK) return rc;
   }
   const unsigned grid = (unsigned)(std::min(tiles, most) * cluster);
   log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide %dx%d grid=%u", (long long)p.M,
              (long long)p.N, (long long)rq.K, C::kTileM, BN, grid);
-  return launch(wide_kernel<BN, ROWS>, rq, p, 128, C::kRowsW, dim3(grid), C::kThreads, C::kRegs,
+  return launch(kern, rq, p, 128, C::kRowsW, dim3(grid), C::kThreads, C::kRegs,
                 C::kLaunch, cluster, stream, tune.pdl != 0);
 }
 
@@ -763,15 +819,36 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.N = rq.N;
   p.kblocks = (int)((rq.K + 127) / 128);
   p.fp32_out = rq.fp32_out;
-  const int64_t row_bytes = p.N * (p.fp32_out ? 4 : 2);
-  p.vec_out = row_bytes % 32 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
   p.wait_limit_ns = tune.wait_limit_ns;
   p.missing_tx = tune.missing_tx;
-  if (p.M <= 16) return launch_narrow<16>(rq, p, stream, dev, tune);
-  if (p.M <= 32) return launch_narrow<32>(rq, p, stream, dev, tune);
-  if (p.M <= 128) return launch_narrow<64>(rq, p, stream, dev, tune);
-  const int64_t pairs = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (2 * pairs >= dev.sm_count)
+  enum { kAuto, kNarrow, kWide, kPair };
+  int kind = tune.force_vpt;   // debug: one of these
+  if (kind == kAuto) {
+    // Few tiles of 128 x 128: their K loops leave SMs idle, and narrow_kernel
+    // splits K (us, narrow / one CTA: [200, 4096] x [1024, 4096] 7.9 / 12.7,
+    // [100, 4096] x [4096, 4096] 11.1 / 13.0; the other way round from 40 tiles,
+    // [128, 5120] x [5120, 5120] 18.3 / 15.5).  Up to 64 rows of A it reads W
+    // with less waste and holds out longer ([64, 5120] x [5120, 5120] 12.1 /
+    // 14.8, [64, 5120] x [15360, 5120] 20.7 / 16.7), up to 32 always.
+    const int64_t ones = (p.M + 127) / 128 * ((p.N + 127) / 128);
+    const int64_t pairs = (p.M + 255) / 256 * ((p.N + 255) / 256);
+    const int64_t sms = dev.sm_count;
+    if (p.M <= 32 || 4 * ones <= sms || (p.M <= 64 && 2 * ones <= sms)) {
+      kind = kNarrow;
+    } else {
+      // A K block takes a pair ~1.5 times as long as one CTA: by the rounds of
+      // tiles ([333, 5120] x [5120, 5120] one CTA 16.0, pair 24.1; [512, 5120]
+      // 28.7 and 24.1, as 160 tiles take two rounds).
+      const int64_t rounds = (ones + sms - 1) / sms, rounds2 = (pairs + sms / 2 - 1) / (sms / 2);
+      kind = 2 * rounds <= 3 * rounds2 ? kWide : kPair;
+    }
+  }
+  if (kind == kNarrow) {
+    if (p.M <= 16) return launch_narrow<16>(rq, p, stream, dev, tune);
+    if (p.M <= 32) return launch_narrow<32>(rq, p, stream, dev, tune);
+    return launch_narrow<64>(rq, p, stream, dev, tune);
+  }
+  if (kind == kPair)
     return rq.w_rows == 1 ? launch_wide<256, true>(rq, p, stream, dev, tune)
                           : launch_wide<256, false>(rq, p, stream, dev, tune);
   return rq.w_rows == 1 ? launch_wide<128, true>(rq, p, stream, dev, tune)

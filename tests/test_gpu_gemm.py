@@ -49,6 +49,23 @@ def test_product(M, N, K, rows, dtype):
     check(y, a, sa, w, sw, rows)
 
 
+@pytest.mark.parametrize("kernel", [1, 2, 3])
+@pytest.mark.parametrize("rows", [128, 1])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (3, 130, 144), (64, 384, 512), (130, 257, 1040),
+                                   (300, 1000, 528), (513, 2305, 640), (700, 1537, 2192)])
+def test_every_kernel_on_any_shape(M, N, K, rows, kernel):
+    """The kernels of few rows, of single CTAs and of pairs, forced."""
+    a, sa, w, sw = operands(M, N, K, rows, seed=M + N + K + 1)
+    for dtype in (torch.bfloat16, torch.float32):
+        try:
+            nts.set_tuning(vpt=kernel)
+            y = nts.gemm_blockscaled(a, sa, w, sw, out_dtype=dtype)
+            nts.check_status()
+        finally:
+            nts.set_tuning()
+        check(y, a, sa, w, sw, rows)
+
+
 def test_whole_numbers_are_exact():
     """Small whole numbers: every sum is exact in fp32."""
     g = torch.Generator(device=DEV).manual_seed(3)
