@@ -37,6 +37,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
 constexpr int kDirectItems = 16;     // warp items per SM up to which nothing is staged
+constexpr int kFusedSums = 1 << 15;  // partial sums up to which the last CTA adds them up
 constexpr int kForwardRounds = 4, kForwardStages = 2;
 constexpr int kBackwardRounds = 2, kBackwardStages = 2;
 
@@ -68,6 +69,9 @@ struct RopeParams {
   uint32_t missing_tx;       // test hook: bytes expected on a first stage but never sent
   float* partial;            // backward: [CTAs, d] sums for the gains' gradients
   unsigned ctas_q;           // backward: CTAs of Q; the others take K
+  float* dgamma[2];          // backward
+  unsigned int* sched;       // backward: zeroed counter pair of the launch (its second
+                             // word counts CTAs), or nullptr: a launch of its own sums
 };
 
 // A lane's place: the element offsets of its two vectors, whether it rotates
@@ -334,8 +338,18 @@ __device__ __forceinline__ void backward_head(const RopeParams& p, const RopeLan
   x1 = pack8(x.b);
 }
 
+// Threads along the columns of the sum of the CTAs' rows by one CTA (at most 32
+// rows of threads are left).
+__host__ __device__ __forceinline__ int sum_columns(int d) {
+  int wide = kRopeThreads / 32;
+  while (4 * wide < d) wide *= 2;
+  return wide;
+}
+
 // The CTA's row of partial sums for dgamma: over the heads of a warp, then
-// over its warps.  red: [warps][d].
+// over its warps; and, by the last CTA to get here, the sum of the CTAs' rows.
+// Every sum has a fixed order, whichever CTA comes last.  red: [warps][d] at
+// least, and [32][8] floats.
 __device__ __forceinline__ void reduce_gain_grad(const RopeParams& p, const RopeLane& l, int lanes,
                                                  const RopeValues& sum, float* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -358,6 +372,42 @@ __device__ __forceinline__ void reduce_gain_grad(const RopeParams& p, const Rope
     float v = 0.f;
     for (int w = 0; w < kRopeWarps; ++w) v += red[w * p.d + j];
     p.partial[(int64_t)blockIdx.x * p.d + j] = v;
+  }
+  if (p.sched == nullptr) return;
+
+  __shared__ int last;
+  __threadfence();   // this thread's values of the row are visible before it is counted
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(p.sched + 1, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  if (threadIdx.x == 0) atomicExch(p.sched + 1, 0u);   // ready for the next launch
+  __threadfence();
+  // four columns per thread, the rows strided over the threads, both tensors at once
+  const int wide = sum_columns(p.d);
+  const int c = threadIdx.x & (wide - 1), r0 = threadIdx.x / wide, rows = kRopeThreads / wide;
+  float4* part = reinterpret_cast<float4*>(red);         // [kRopeThreads]
+  for (int i = 0; i < 2; ++i) {
+    const unsigned begin = i ? p.ctas_q : 0, end = i ? gridDim.x : p.ctas_q;
+    const float4* row = reinterpret_cast<const float4*>(p.partial) + c;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (4 * c < p.d)
+#pragma unroll 8
+      for (unsigned r = begin + r0; r < end; r += rows) {
+        const float4 x = __ldcg(row + (int64_t)r * (p.d / 4));
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+    __syncthreads();
+    part[threadIdx.x] = v;
+    __syncthreads();
+    if (r0 == 0 && 4 * c < p.d) {
+      for (int w = 1; w < rows; ++w) {
+        const float4 x = part[w * wide + c];
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      float* out = p.dgamma[i] + 4 * c;
+      out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+    }
   }
 }
 
@@ -694,12 +744,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(con
   reduce_gain_grad(p, l, lanes, sum, reinterpret_cast<float*>(smem));
 }
 
-// dgamma = the sum of the CTAs' rows, in a fixed order: block (32 columns) x
-// (32 strided rows), blockIdx.y the tensor.
+// dgamma = the sum of the CTAs' rows as a launch of its own, for many rows (one
+// CTA would take longer than the launch) and inside a graph: block (32 columns)
+// x (strided rows), blockIdx.y the tensor.  A sum that the last CTA of an eager
+// call would make gets that one's number of rows, and so its order and its bits.
 __global__ void __launch_bounds__(1024) rope_gain_grad_kernel(const float* partial, unsigned nq,
                                                               unsigned n, int d, float* dgamma_q,
                                                               float* dgamma_k) {
-  __shared__ float red[32][33];
+  __shared__ float red[32][32];
   const int col = blockIdx.x * 32 + threadIdx.x;
   const unsigned r0 = blockIdx.y ? nq : 0, r1 = blockIdx.y ? n : nq;
   grid_dependency_wait();
@@ -707,12 +759,12 @@ __global__ void __launch_bounds__(1024) rope_gain_grad_kernel(const float* parti
   float v = 0.f;
   if (col < d)
 #pragma unroll 8
-    for (unsigned r = r0 + threadIdx.y; r < r1; r += 32) v += partial[(int64_t)r * d + col];
+    for (unsigned r = r0 + threadIdx.y; r < r1; r += blockDim.y) v += partial[(int64_t)r * d + col];
   red[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = warp_sum(red[threadIdx.x][threadIdx.y]);
-  const int out = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && out < d) (blockIdx.y ? dgamma_k : dgamma_q)[out] = v;
+  if (threadIdx.y != 0 || col >= d) return;
+  for (int w = 1; w < (int)blockDim.y; ++w) v += red[w][threadIdx.x];
+  (blockIdx.y ? dgamma_k : dgamma_q)[col] = v;
 }
 
 using RopeKernel = void (*)(RopeParams);
@@ -773,7 +825,7 @@ size_t set_ring(RopeParams* p, int copies, int stages) {
   p->stages = stages;
   p->stage_bytes = (uint32_t)(p->heads * p->d * 2 * copies);
   const size_t ring = (size_t)kRopeWarps * stages * (p->stage_bytes + 8);
-  return std::max(ring, (size_t)kRopeWarps * p->d * sizeof(float));   // the sums at the end
+  return std::max(ring, (size_t)kRopeWarps * std::max(p->d, 128) * sizeof(float));   // the sums
 }
 
 template <typename... A>
@@ -835,7 +887,7 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   int rc = set_items(&p, 1, items);
   if (rc != NTS_OK) return rc;
   const bool ring = tune.force_rows > 0 || items[0] + items[1] > (uint64_t)dev.sm_count * kDirectItems;
-  size_t smem = (size_t)kRopeWarps * p.d * sizeof(float);
+  size_t smem = (size_t)kRopeWarps * std::max(p.d, 128) * sizeof(float);
   RopeKernel kern = rq.interleaved ? rope_backward_kernel<true> : rope_backward_kernel<false>;
   if (ring) {
     kern = rq.interleaved ? rope_backward_ring_kernel<true> : rope_backward_ring_kernel<false>;
@@ -852,7 +904,8 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   // CTAs in proportion to the tensors' items, one at least for each
   const uint64_t nq = (items[0] + kRopeWarps - 1) / kRopeWarps;
   const uint64_t nk = (items[1] + kRopeWarps - 1) / kRopeWarps;
-  const uint64_t most = std::min<uint64_t>((uint64_t)per_sm * dev.sm_count, kRopePartials);
+  const uint64_t most =
+      std::min<uint64_t>((uint64_t)(ring ? per_sm : 1) * dev.sm_count, kRopePartials);
   uint64_t gq = nq, gk = nk;
   if (gq + gk > most) {
     const uint64_t all = items[0] + items[1];
@@ -862,14 +915,28 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   }
   p.ctas_q = (unsigned)gq;
   p.partial = workspace;
+  p.dgamma[0] = dgamma_q;
+  p.dgamma[1] = dgamma_k;
   const unsigned grid = (unsigned)(gq + gk);
+  // Few rows: the last CTA sums them, and the call is one launch ([333, 32 + 8
+  // heads of 64], back to back from the host: 9.4 us a call, 11.4 with two).  In
+  // a graph, where a launch costs less than the last CTA's latencies, two (7.2
+  // us, one 8.4).
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) (void)cudaGetLastError();
+  const bool few = (int64_t)grid * p.d <= kFusedSums;
+  const bool wide = reinterpret_cast<uintptr_t>(workspace) % 16 == 0;   // float4 loads
+  p.sched = tune.dynamic && few && wide && capture == cudaStreamCaptureStatusNone
+                ? sched_counters(stream)
+                : nullptr;
   log_launch("qknorm_rope_backward",
              "T=%u heads=%d+%d d=%d rot=%d ring=%d per item=%d S=%d smem=%zu grid=%u (%u for Q)",
              p.T, p.ten[0].nheads, p.ten[1].nheads, p.d, p.rot, ring, p.heads, p.stages, smem, grid,
              p.ctas_q);
   rc = launch(kern, dim3(grid), dim3(kRopeThreads), smem, stream, tune.pdl != 0, p);
-  if (rc != NTS_OK) return rc;
-  return launch(rope_gain_grad_kernel, dim3((p.d + 31) / 32, 2), dim3(32, 32), 0, stream,
+  if (rc != NTS_OK || p.sched != nullptr) return rc;
+  const int rows = few ? kRopeThreads / sum_columns(p.d) : 32;
+  return launch(rope_gain_grad_kernel, dim3((p.d + 31) / 32, 2), dim3(32, rows), 0, stream,
                 tune.pdl != 0, (const float*)workspace, (unsigned)gq, grid, p.d, dgamma_q,
                 dgamma_k);
 }

@@ -316,6 +316,26 @@ def test_equal_calls_give_equal_bits_on_streams_and_in_graphs():
     nts.check_status()
 
 
+@pytest.mark.parametrize("T,d", [(1, 16), (9, 16), (300, 48), (2000, 64), (257, 128), (40, 512)])
+def test_the_gains_gradients_have_one_order_however_they_are_summed(T, d):
+    """The last CTA's sum, a launch of its own in a graph, and a workspace that
+    starts off a vector boundary."""
+    c = make(T, 5, 2, d, d, seed=41)
+    want = backward(c, d, False)
+    ws = torch.empty(nts.rope_backward_workspace(d) + 4, dtype=torch.uint8, device=DEV)
+    odd = backward(c, d, False, workspace=ws[4:])
+    D = {k: to_dev(v) for k, v in c.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = nts.qknorm_rope_backward(D["dyq"], D["dyk"], D["q"], D["gq"], D["k"], D["gk"],
+                                       D["pos"], D["table"], head_dim=d, eps=EPS)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, g in zip(want, odd, cap):
+        assert torch.equal(a, b) and torch.equal(a, g)
+    nts.check_status()
+
+
 def test_canaries():
     T, hq, hk, d = 41, 5, 2, 96
     c = make(T, hq, hk, d, 64, seed=31, packed=True, pad=2)
