@@ -8,7 +8,7 @@
 // rotation took 13 of a call's 17 us, against 4 in the library with the launch.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -77,8 +77,7 @@ const at::Tensor& matrix(const char* name, const at::Tensor& t) {
 }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape,
-                   at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (int8_t)dev)));
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (int8_t)dev), std::nullopt);
 }
 
 // The caller's output buffer, checked, or a new one.

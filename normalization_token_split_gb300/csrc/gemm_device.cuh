@@ -285,6 +285,19 @@ __device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t addr) {
                : "r"(addr));
 }
 
+// 32 columns of 16 lanes (the lanes of `addr` on), as the fragments of a matrix
+// product lie: r[4 g + 2 h + e] is lane 8 h + t / 4, column 8 g + 2 (t % 4) + e,
+// for the warp's thread t.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+               "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15 "
+               "}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                 "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+
 // Waits for this thread's tensor-memory loads; names their registers so that
 // no use of them moves above the wait.
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {

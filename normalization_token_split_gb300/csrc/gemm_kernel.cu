@@ -77,6 +77,29 @@ __device__ __forceinline__ void drain(uint32_t full, uint32_t done, int64_t issu
   }
 }
 
+// A lane's share of staging the scales of N rows, from row0 on (of `rows` there
+// are), for one K block: rows sub + 8 i, each to its place (linear over sub and
+// 8 i) after dst.  Zeros where there is no row, or !in.  The addresses go from
+// row to row by one step: formed anew for each copy they took the two warps 220
+// cycles a copy beside the epilogue's arithmetic, more than the K blocks take
+// when W has a scale per row ([4096, 4112] x [4096, 4112] to fp32: 128 us then,
+// 106 so).
+template <int N, typename Place>
+__device__ __forceinline__ void stage_scales(uint32_t dst, const float* scales, int64_t row0,
+                                             int64_t rows, int64_t kb, int64_t kblocks, bool in,
+                                             int sub, Place place) {
+  const int left = in ? (int)min64(N, rows - row0) : 0;
+  const float* src = sub < left ? scales + (row0 + sub) * kblocks + kb : scales;
+  dst += 4 * place(sub);
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    if (N % 8 != 0 && sub >= N) break;
+    const bool here = sub + i < left;
+    copy_async_f32(dst + 4 * place(i), src, here);
+    if (here) src += 8 * kblocks;
+  }
+}
+
 // ---------------------------------------------------------------- wide
 
 constexpr int kGroupM = 16;   // tiles of A walked before the next tile of W
@@ -126,6 +149,19 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int64_t tile, int* 
   const int rows = (int)min64(kGroupM, p.tiles_m - g * kGroupM);
   *tn = (int)(in / rows);
   *tm = (int)(g * kGroupM + (in - (int64_t)*tn * rows));
+}
+
+// With a scale for each row of W too, a thread reads fragments of 16 rows by 32
+// columns (tmem_load_fragments): 32 rows and COLS columns take 4 row scales and
+// COLS / 4 column scales a thread, where a thread with a row of its own needs
+// all COLS of them from shared memory ([4096, 4112] x [4096, 4112] to fp32:
+// 123 us then, 106 now).  The scales lie in shared memory in the order in
+// which a thread needs them, four at a time.
+__device__ __forceinline__ int row_place(int r) {
+  return (r & ~31) + (r & 7) * 4 + (r >> 3 & 3);
+}
+__device__ __forceinline__ int column_place(int r) {
+  return (r & ~31) + (r >> 1 & 3) * 8 + (r >> 3 & 3) * 2 + (r & 1);
 }
 
 // VEC: rows of Y start on 32-byte boundaries (a template parameter: with both
@@ -262,19 +298,16 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         for (int k0 = 0; k0 < p.kblocks && !late; k0 += kChunk) {
           bar_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop_at, late);
           const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
-          const bool in = k0 + kl < p.kblocks;
-#pragma unroll 4
-          for (int r = sub; r < 128; r += 8) {
-            const bool here = in && m0 + r < p.M;
-            copy_async_f32(dst + 4 * r, here ? p.sa + (m0 + r) * p.kblocks + k0 + kl : p.sa, here);
-          }
-#pragma unroll 4
-          for (int r = sub; r < (ROWS ? BN : BN / 128); r += 8) {
-            const int64_t n = n0 + (ROWS ? r : 128 * r);
-            const bool here = in && n < p.N;
-            const int64_t w = ROWS ? n : n / 128;
-            copy_async_f32(dst + 4 * (128 + r), here ? p.sw + w * p.kblocks + k0 + kl : p.sw, here);
-          }
+          const int64_t at = k0 + kl;
+          const bool in = at < p.kblocks;
+          stage_scales<128>(dst, p.sa, m0, p.M, at, p.kblocks, in, sub, [](int r) {
+            return ROWS ? row_place(r) : r;
+          });
+          if constexpr (ROWS)
+            stage_scales<BN>(dst + 4 * 128, p.sw, n0, p.N, at, p.kblocks, in, sub, column_place);
+          else
+            stage_scales<BN / 128>(dst + 4 * 128, p.sw, n0 / 128, (p.N + 127) / 128, at, p.kblocks,
+                                   in, sub, [](int r) { return r; });
           copy_async_arrive(sfull + 8 * pc.i);
           pc.advance();
         }
@@ -282,22 +315,48 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
   } else {
     if (PAIR) registers_up<C::kRegsUp>();
-    constexpr int COLS = C::kCols, STEPS = COLS / 32;   // even: a block's first load goes to v[0]
+    constexpr int COLS = C::kCols;
+    constexpr int LOADED = ROWS ? 16 : 32, STEPS = COLS * 32 / (32 * LOADED);   // even
     const int group = (warp - 4) >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32u << 16) + COLS * group;
+    const int quarter = (warp & 3) * 32, row = quarter + lane;
+    const uint32_t mine = tmem + ((uint32_t)quarter << 16) + COLS * group;
     const int wblock = ROWS ? COLS * group : COLS * group / 128;
     const uint32_t drained = PAIR ? map_to_rank(tempty, 0) : tempty;
     RingSlot<NB> tb;
     RingSlot<kPieces> pc;
-    uint32_t v[2][32];
-    // the block in buffer tb is there: its first columns are on their way
-    const float* sc = nullptr;
+    uint32_t v[2][LOADED];
+    // step j of a block: its columns 32 j .. + 31; ROWS: its columns 32 (j / 2)
+    // .. + 31, the upper 16 rows and then the lower
+    auto load = [&](int j) {
+      const uint32_t at = mine + tb.i * BN;
+      if constexpr (ROWS)
+        tmem_load_fragments(v[j & 1], at + 32 * (j >> 1) + ((uint32_t)(j & 1) << 20));
+      else
+        tmem_load(v[j & 1], at + 32 * j);
+    };
+    // the block in buffer tb is there: its first step is on its way
     auto begin = [&](uint32_t ready) {
       bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late, ready);
       __syncwarp();
       tcgen05_fence_after();
-      tmem_load(v[0], mine + tb.i * BN);
+      load(0);
+    };
+    const float* sc = nullptr;   // the scales of the block to come
+    // the scales of a block (ROWS: and of its first columns) are asked for a block
+    // ahead: shared memory is busy
+    float scale = 0.f;
+    float4 rows4 = make_float4(0.f, 0.f, 0.f, 0.f), columns[2][2];
+    auto ask_rows = [&] {
+      if constexpr (ROWS)
+        rows4 = *reinterpret_cast<const float4*>(sc + quarter + (lane >> 2) * 4);
+      else
+        scale = sc[row] * sc[128 + wblock];
+    };
+    auto ask_columns = [&](const float* of, int c) {   // ROWS: columns 32 c .. + 31
+      const float4* w =
+          reinterpret_cast<const float4*>(of + 128 + wblock + 32 * c + (lane & 3) * 8);
+      columns[c & 1][0] = w[0];
+      columns[c & 1][1] = w[1];
     };
     for (int64_t tile = first; tile < tiles && !late; tile += step) {
       int tm, tn;
@@ -305,16 +364,16 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      // a block's scales are asked for a block ahead: shared memory is busy
-      auto scale = [&] { return ROWS ? sc[row] : sc[row] * sc[128 + wblock]; };
       bar_wait(sfull + 8 * pc.i, pc.parity, p.wait_limit_ns, stop_at, late);
       __syncwarp();
       sc = scales + pc.i * kChunk * C::kScales;
-      float next = scale();
+      ask_rows();
+      if constexpr (ROWS) ask_columns(sc, 0);
       begin(0);
       for (int kb = 0; kb < p.kblocks; ++kb) {
-        const float s = next;
-        const float* scw = sc + 128 + wblock;
+        const float s = scale;
+        const float r4[4] = {rows4.x, rows4.y, rows4.z, rows4.w};
+        const float* here = sc;
         const bool more = kb + 1 < p.kblocks, turn = (kb & (kChunk - 1)) == kChunk - 1;
         const int piece = pc.i;
         sc += C::kScales;
@@ -326,14 +385,13 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             sc = scales + pc.i * kChunk * C::kScales;
           }
         }
-        if (more) next = scale();
-        const uint32_t at = mine + tb.i * BN;
+        if (more) ask_rows();
         uint32_t ready = 0;
 #pragma unroll
         for (int j = 0; j < STEPS; ++j) {
           tmem_wait(v[j & 1]);
           if (j + 1 < STEPS) {
-            tmem_load(v[(j + 1) & 1], at + 32 * (j + 1));
+            load(j + 1);
             if (j + 2 == STEPS) {
               RingSlot<NB> nx = tb;
               nx.advance();
@@ -345,21 +403,27 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             tb.advance();
             if (more) begin(ready);
           }
-          // one fma per value: in pairs (f32x2) the loaded registers are no operands
-          // without two moves for each pair, 121 instructions for 64 values
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 w = make_float4(s, s, s, s);
-            if (ROWS) {
-              w = *reinterpret_cast<const float4*>(scw + 32 * j + i);
-              w.x *= s, w.y *= s, w.z *= s, w.w *= s;
+          const uint32_t* x = v[j & 1];
+          float* a = acc + LOADED * j;
+          if constexpr (ROWS) {
+            const int c = j >> 1;
+            const float4 w0 = columns[c & 1][0], w1 = columns[c & 1][1];
+            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            if ((j & 1) == 0) {
+              if (c + 1 < COLS / 32)
+                ask_columns(here, c + 1);
+              else if (more)
+                ask_columns(sc, 0);   // COLS / 32 is even
             }
-            const uint32_t* x = &v[j & 1][i];
-            float* a = acc + 32 * j + i;
-            a[0] = fmaf(__uint_as_float(x[0]), w.x, a[0]);
-            a[1] = fmaf(__uint_as_float(x[1]), w.y, a[1]);
-            a[2] = fmaf(__uint_as_float(x[2]), w.z, a[2]);
-            a[3] = fmaf(__uint_as_float(x[3]), w.w, a[3]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              a[i] = fmaf(__uint_as_float(x[i]),
+                          r4[2 * (j & 1) + (i >> 1 & 1)] * w[(i >> 2) * 2 + (i & 1)], a[i]);
+          } else {
+            // one fma per value: in pairs (f32x2) the loaded registers are no operands
+            // without two moves for each pair, 121 instructions for 64 values
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(x[i]), s, a[i]);
           }
         }
         if (turn || !more) {
@@ -373,7 +437,20 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       const int rows = (int)min64(32, p.M - m0), cols = (int)min64(COLS, p.N - n0);   // may be <= 0
       float* yf = static_cast<float*>(p.y) + m0 * p.N + n0;
       __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + m0 * p.N + n0;
-      if (VEC) {
+      if (VEC && ROWS) {
+        // whole 32-byte pieces of a row (bf16: halves) by four lanes
+#pragma unroll
+        for (int i = 0; i < COLS; i += 2) {
+          const int r = (i >> 4 & 1) * 16 + (i >> 1 & 1) * 8 + (lane >> 2);
+          const int c = (i >> 5) * 32 + (i >> 2 & 3) * 8 + (lane & 3) * 2;
+          if (r < rows && c < cols) {
+            if (p.fp32_out)
+              *reinterpret_cast<float2*>(yf + r * p.N + c) = make_float2(acc[i], acc[i + 1]);
+            else
+              *reinterpret_cast<uint32_t*>(yh + r * p.N + c) = pack_bf16x2_rn(acc[i], acc[i + 1]);
+          }
+        }
+      } else if (VEC) {
         // N a multiple of 8 (fp32) or 16: whole 32-byte pieces
         if (lane < rows) {
           if (p.fp32_out) {
@@ -405,7 +482,13 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         for (int j = 0; j < COLS; j += 8) {
           if (j >= cols) break;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) out[lane * kOutPitch + i] = acc[j + i];
+          for (int i = 0; i < 8; ++i) {
+            if (ROWS)   // fragment values of the upper rows, then of the lower
+              out[((i >> 2) * 16 + (i >> 1 & 1) * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 2 +
+                  (i & 1)] = acc[(j >> 5) * 32 + (i >> 2) * 16 + (j >> 3 & 3) * 4 + (i & 3)];
+            else
+              out[lane * kOutPitch + i] = acc[j + i];
+          }
           __syncwarp();
           if (j + c < cols) {
 #pragma unroll
@@ -572,19 +655,12 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     for (int k0 = 2 * u0; k0 < 2 * u1 && !late; k0 += kChunk, pc.advance()) {
       bar_wait(sempty + 8 * pc.i, pc.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       const uint32_t dst = sbase + C::kScaleOff + 4 * (pc.i * kChunk + kl) * C::kScales;
-      const bool in = k0 + kl < min(2 * u1, p.kblocks);
-#pragma unroll 4
-      for (int r = sub; r < TN; r += 8) {
-        const int64_t m = (int64_t)tm * TN + r;
-        const bool here = in && m < p.M;
-        copy_async_f32(dst + 4 * r, here ? p.sa + m * p.kblocks + k0 + kl : p.sa, here);
-      }
-#pragma unroll 4
-      for (int r = sub; r < (ROWS ? 128 : 1); r += 8) {
-        const int64_t w = ROWS ? (int64_t)tn * 128 + r : tn;
-        const bool here = in && (!ROWS || w < p.N);
-        copy_async_f32(dst + 4 * (TN + r), here ? p.sw + w * p.kblocks + k0 + kl : p.sw, here);
-      }
+      const int64_t at = k0 + kl;
+      const bool in = at < min(2 * u1, p.kblocks);
+      const auto place = [](int r) { return r; };
+      stage_scales<TN>(dst, p.sa, (int64_t)tm * TN, p.M, at, p.kblocks, in, sub, place);
+      stage_scales<ROWS ? 128 : 1>(dst + 4 * TN, p.sw, (int64_t)tn * (ROWS ? 128 : 1),
+                                   ROWS ? p.N : tn + 1, at, p.kblocks, in, sub, place);
       copy_async_arrive(sfull + 8 * pc.i);
     }
   } else {
