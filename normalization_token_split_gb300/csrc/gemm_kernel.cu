@@ -133,7 +133,10 @@ struct Wide {
   static constexpr uint32_t kA = 128 * 128;
   static constexpr uint32_t kStage = kA + kRowsW * 128;
   static constexpr int kStages = 196608 / (int)kStage;    // 6
-  static constexpr int kBufs = kPair ? 2 : 3;             // at most 512 columns; divides kStages
+  static constexpr int kHalves = kPair && !ROWS ? 2 : 1;  // accumulators per K block
+  static constexpr int kBufCols = BN / kHalves;           // columns of an accumulator
+  static constexpr int kRing = kPair ? 2 : 3;             // K blocks in tensor memory
+  static constexpr int kBufs = kRing * kHalves;           // at most 512 columns in all
   static constexpr int kScales = 128 + (ROWS ? BN : 4);   // floats per K block
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kOutOff = kScaleOff + kPieces * kChunk * kScales * 4;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(Wide<BN, ROWS>::kThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
             const GemmParams p) {
   using C = Wide<BN, ROWS>;
-  constexpr int S = C::kStages, NB = C::kBufs;
+  constexpr int S = C::kStages, NB = C::kBufs, H = C::kHalves;
   constexpr bool PAIR = C::kPair;
   extern __shared__ unsigned char raw[];
   const uint32_t sbase = (smem_addr(raw) + 1023u) & ~1023u;
@@ -192,7 +195,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, PAIR ? 16 : 8);
+      mbar_init(tempty + 8 * i, (PAIR ? 16 : 8) / H);   // warps that drain it
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(sfull + 8 * i, 64);
@@ -232,7 +235,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       for (int64_t tile = first; tile < tiles && !late; tile += step) {
         int tm, tn;
         tile_at(p, tile, &tm, &tn);
-        const int ya = tm * C::kTileM + rank * 128, yw = tn * BN + rank * C::kRowsW;
+        const int ya = tm * C::kTileM + rank * 128, yw = tn * BN + rank * (C::kRowsW / H);
         for (int k0 = 0; k0 < p.kblocks && !late; k0 += kChunk) {
           const int k1 = min(k0 + kChunk, p.kblocks);
           for (int kb = k0; kb < k1; ++kb, st.advance()) {
@@ -246,7 +249,10 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     bar, C::kStage * (PAIR ? 2 : 1) +
                              (tile == first && kb == 0 ? p.missing_tx : 0u));
               tma_load_2d<PAIR>(at, &map_a, kb * 128, ya, counts);
-              tma_load_2d<PAIR>(at + C::kA, &map_w, kb * 128, yw, counts);
+#pragma unroll
+              for (int h = 0; h < H; ++h)
+                tma_load_2d<PAIR>(at + C::kA + h * (C::kRowsW / H) * 128, &map_w, kb * 128,
+                                  yw + h * C::kBufCols, counts);
             }
             __syncwarp();
           }
@@ -258,32 +264,38 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       // One K block after the other, whatever tile it belongs to: every block
       // begins its sums anew.  S blocks a turn, so that slots, buffers and
       // descriptors are constants.
-      constexpr uint32_t instr = e4m3_instr(C::kTileM, BN);
-      static_assert(S % NB == 0, "a turn goes round both rings");
-      constexpr uint32_t flips = S / NB % 2;   // whether a turn flips the buffers' parity
+      constexpr uint32_t instr = e4m3_instr(C::kTileM, C::kBufCols);
+      static_assert(S * H % NB == 0, "a turn goes round both rings");
+      constexpr uint32_t flips = S * H / NB % 2;   // whether a turn flips the buffers' parity
       const uint32_t da = operand_desc(sbase), dw = operand_desc(sbase + C::kA);
       const int64_t blocks = first < tiles ? ((tiles - first + step - 1) / step) * p.kblocks : 0;
-      uint32_t parity = 0, stored = 0, drained = 1;   // answers on the block to come
+      uint32_t parity = 0, stored = 0, drained = 1;   // answers on what comes next
       for (int64_t n = 0; n < blocks && !late; n += S, parity ^= 1u) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           if (n + i >= blocks) break;
-          bar_wait(tempty + 8 * (i % NB), (parity & flips) ^ (i / NB & 1) ^ 1u, p.wait_limit_ns,
-                   stop_at, late, drained);
-          bar_wait(full + 8 * i, parity, p.wait_limit_ns, stop_at, late, stored);
-          constexpr int kLast = S - 1;
-          const int j = i == kLast ? 0 : i + 1;
-          const uint32_t turn = i == kLast ? parity ^ 1u : parity;
-          stored = bar_test(full + 8 * j, turn);
-          drained = bar_test(tempty + 8 * (j % NB), (turn & flips) ^ (j / NB & 1) ^ 1u);
-          tcgen05_fence_after();
-          if (leader) {
-            constexpr uint32_t kNext = C::kStage >> 4;
-            mma_block<PAIR>(tmem + i % NB * BN, da + i * kNext, dw + i * kNext, instr);
-            mma_commit<PAIR>(tfull + 8 * (i % NB));
-            mma_commit<PAIR>(empty + 8 * i);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            constexpr int kLast = S * H - 1;
+            const int u = i * H + h, b = u % NB;
+            bar_wait(tempty + 8 * b, (parity & flips) ^ (u / NB & 1) ^ 1u, p.wait_limit_ns,
+                     stop_at, late, drained);
+            if (h == 0)
+              bar_wait(full + 8 * i, parity, p.wait_limit_ns, stop_at, late, stored);
+            const int v = u == kLast ? 0 : u + 1;
+            const uint32_t turn = u == kLast ? parity ^ 1u : parity;
+            if (h == H - 1) stored = bar_test(full + 8 * (v / H), turn);
+            drained = bar_test(tempty + 8 * (v % NB), (turn & flips) ^ (v / NB & 1) ^ 1u);
+            tcgen05_fence_after();
+            if (leader) {
+              constexpr uint32_t kNext = C::kStage >> 4, kHalf = C::kRowsW / H * 128 >> 4;
+              mma_block<PAIR>(tmem + b * C::kBufCols, da + i * kNext, dw + i * kNext + h * kHalf,
+                              instr);
+              mma_commit<PAIR>(tfull + 8 * b);
+              if (h == H - 1) mma_commit<PAIR>(empty + 8 * i);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
     } else if (warp > 1) {
@@ -322,9 +334,10 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const uint32_t mine = tmem + ((uint32_t)quarter << 16) + COLS * group;
     const int wblock = ROWS ? COLS * group : COLS * group / 128;
     const uint32_t drained = PAIR ? map_to_rank(tempty, 0) : tempty;
-    RingSlot<NB> tb;
+    RingSlot<C::kRing> tb;   // this group's buffers, or both groups'
     RingSlot<kPieces> pc;
     uint32_t v[2][LOADED];
+    auto bar_of = [&](int i) { return 8 * (H * i + (H == 2 ? group : 0)); };
     // step j of a block: its columns 32 j .. + 31; ROWS: its columns 32 (j / 2)
     // .. + 31, the upper 16 rows and then the lower
     auto load = [&](int j) {
@@ -336,7 +349,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     };
     // the block in buffer tb is there: its first step is on its way
     auto begin = [&](uint32_t ready) {
-      bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late, ready);
+      bar_wait(tfull + bar_of(tb.i), tb.parity, p.wait_limit_ns, stop_at, late, ready);
       __syncwarp();
       tcgen05_fence_after();
       load(0);
@@ -393,13 +406,13 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           if (j + 1 < STEPS) {
             load(j + 1);
             if (j + 2 == STEPS) {
-              RingSlot<NB> nx = tb;
+              RingSlot<C::kRing> nx = tb;
               nx.advance();
-              ready = bar_test(tfull + 8 * nx.i, nx.parity);
+              ready = bar_test(tfull + bar_of(nx.i), nx.parity);
             }
           } else {   // all in registers: the buffer is free, the next block begins
             tcgen05_fence_before();
-            arrive_if<PAIR>(drained + 8 * tb.i, lane == 0);
+            arrive_if<PAIR>(drained + bar_of(tb.i), lane == 0);
             tb.advance();
             if (more) begin(ready);
           }
@@ -527,6 +540,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 
 // -------------------------------------------------------------- narrow
 
+constexpr int kMostSplit = 8;         // CTAs of a cluster, which share a tile's K
 constexpr int kNarrowThreads = 256;   // TMA, MMA, 2 scale warps, 4 epilogue warps
 
 // A stage holds two K blocks: a role's waits and arrivals cost several hundred
@@ -541,12 +555,13 @@ struct Narrow {
   static constexpr uint32_t kCols = kBufCols * kBufs;     // 128 or 256
   static constexpr uint32_t kW = 128 * 128, kA = TN * 128;
   static constexpr uint32_t kStage = kPer * (kW + kA);
-  static constexpr int kStages = 110592 / (int)kStage;
   static constexpr int kScales = TN + (ROWS ? 128 : 4);
+  static constexpr int kStages = (112640 - kPieces * kChunk * kScales * 4) / (int)kStage;
   static constexpr uint32_t kScaleOff = kStages * kStage;
   static constexpr uint32_t kBarOff = kScaleOff + kPieces * kChunk * kScales * 4;
   static constexpr uint32_t kBytes = kBarOff + 256;
   static constexpr uint32_t kLaunch = kBytes + 1024;
+  static_assert(kLaunch <= 233472 / 2 - 1024, "two CTAs per SM");
   static_assert(kChunk % kPer == 0, "a stage's scales lie in one piece");
   static_assert(kScaleOff >= TN * 128 * 4, "the sums for the other CTAs fit the ring");
 };
@@ -732,15 +747,36 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   cluster_arrive_release();
   cluster_wait_acquire();
   const int rows = (int)min64(TN, p.M - (int64_t)tm * TN);
-  for (int i = rank * kNarrowThreads + threadIdx.x; i < rows * 128; i += split * kNarrowThreads) {
-    const int64_t m = (int64_t)tm * TN + (i >> 7), nn = (int64_t)tn * 128 + (i & 127);
-    float v = 0.f;
-    for (int r = 0; r < split; ++r) v += ld_cluster_f32(map_to_rank(sbase + 4 * i, (uint32_t)r));
-    if (nn < p.N) {
-      if (p.fp32_out)
-        static_cast<float*>(p.y)[m * p.N + nn] = v;
-      else
-        static_cast<__nv_bfloat16*>(p.y)[m * p.N + nn] = __float2bfloat16_rn(v);
+  const bool whole = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+  for (int i = rank * kNarrowThreads + threadIdx.x; i < rows * 32; i += split * kNarrowThreads) {
+    const int64_t m = (int64_t)tm * TN + (i >> 5), nn = (int64_t)tn * 128 + 4 * (i & 31);
+    float4 x[kMostSplit];
+#pragma unroll
+    for (int r = 0; r < kMostSplit; ++r)
+      if (r < split) x[r] = ld_cluster_f32x4(map_to_rank(sbase + 16 * i, (uint32_t)r));
+    float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+    for (int r = 1; r < kMostSplit; ++r)
+      if (r < split) v[0] += x[r].x, v[1] += x[r].y, v[2] += x[r].z, v[3] += x[r].w;
+    float* yf = static_cast<float*>(p.y) + m * p.N + nn;
+    __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + m * p.N + nn;
+    if (whole) {
+      if (nn < p.N) {
+        if (p.fp32_out)
+          *reinterpret_cast<float4*>(yf) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(yh) =
+              make_uint2(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (nn + j < p.N) {
+          if (p.fp32_out)
+            yf[j] = v[j];
+          else
+            yh[j] = __float2bfloat16_rn(v[j]);
+        }
     }
   }
   // no CTA leaves while another reads its sums
@@ -835,7 +871,7 @@ int launch_narrow(const GemmRequest& rq, const GemmParams& p, cudaStream_t strea
                   const DeviceInfo& dev, const LaunchTuning& tune) {
   const int64_t tiles_n = (p.N + 127) / 128, tiles_m = (p.M + TN - 1) / TN;
   int split = 1;
-  while (split < 8 && 4 * split <= p.kblocks && tiles_n * tiles_m * split <= dev.sm_count)
+  while (split < kMostSplit && 4 * split <= p.kblocks && tiles_n * tiles_m * split <= dev.sm_count)
     split *= 2;
   const int64_t gx = tiles_n * split;
   if (gx > 0x7fffffffll || tiles_m > 65535)
@@ -877,7 +913,7 @@ int launch_wide(const GemmRequest& rq, GemmParams p, cudaStream_t stream, const 
   const unsigned grid = (unsigned)(std::min(tiles, most) * cluster);
   log_launch("gemm_blockscaled", "M=%lld N=%lld K=%lld wide %dx%d grid=%u", (long long)p.M,
              (long long)p.N, (long long)rq.K, C::kTileM, BN, grid);
-  return launch(kern, rq, p, 128, C::kRowsW, dim3(grid), C::kThreads, C::kRegs,
+  return launch(kern, rq, p, 128, C::kRowsW / C::kHalves, dim3(grid), C::kThreads, C::kRegs,
                 C::kLaunch, cluster, stream, tune.pdl != 0);
 }
 
