@@ -9,12 +9,15 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <optional>
 
 #include "nts.h"
 
@@ -76,15 +79,54 @@ const at::Tensor& matrix(const char* name, const at::Tensor& t) {
   return t;
 }
 
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (int8_t)dev), std::nullopt);
+// The stream of a call.  What the call makes belongs to that stream, so that
+// memory that torch hands out again is free there; when it is not the current
+// one, torch also waits for the current stream, where the results are used, before
+// it hands an output on.
+struct On {
+  int dev;
+  void* handle;
+  bool foreign = false;
+  std::optional<c10::cuda::CUDAStream> user;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+
+  On(PyObject* o, int device) : dev(device) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
+    handle = current.stream();
+    if (!given(o)) return;
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (h == nullptr) throw PyError();
+    handle = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (handle == nullptr && PyErr_Occurred()) throw PyError();
+    const cudaStream_t s = static_cast<cudaStream_t>(handle);
+    if (s == current.stream()) return;
+    foreign = s == cudaStreamLegacy || s == cudaStreamPerThread;   // no stream of torch's
+    if (foreign) return;
+    user = current;
+    guard.reset_stream(s == nullptr
+                           ? c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev)
+                           : c10::cuda::getStreamFromExternal(s, (c10::DeviceIndex)dev));
+  }
+};
+
+at::Tensor scratch(at::IntArrayRef shape, at::ScalarType type, const On& on) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (int8_t)on.dev),
+                                           std::nullopt));
+}
+
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const On& on) {
+  at::Tensor t = scratch(shape, type, on);
+  if (on.user && t.numel() != 0)
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *on.user);
+  return t;
 }
 
 // The caller's output buffer, checked, or a new one.
 at::Tensor output(const char* name, PyObject* o, at::IntArrayRef shape, at::ScalarType type,
-                  int dev) {
-  if (!given(o)) return fresh(shape, type, dev);
-  const at::Tensor& t = flat(name, o, type, dev);
+                  const On& on) {
+  if (!given(o)) return fresh(shape, type, on);
+  const at::Tensor& t = flat(name, o, type, on.dev);
   if (t.sizes() != shape) refuse("%s has the wrong shape", name);
   return t;
 }
@@ -104,9 +146,9 @@ Rows rows(const char* name, PyObject* o, int dev, const at::Tensor* like = nullp
   return {t, t.size(0) > 1 ? t.stride(0) : t.size(1)};
 }
 
-Rows rows_out(const char* name, PyObject* o, int dev, const at::Tensor& like) {
-  if (given(o)) return rows(name, o, dev, &like);
-  return {fresh(like.sizes(), at::kBFloat16, dev), like.size(1)};
+Rows rows_out(const char* name, PyObject* o, const On& on, const at::Tensor& like) {
+  if (given(o)) return rows(name, o, on.dev, &like);
+  return {fresh(like.sizes(), at::kBFloat16, on), like.size(1)};
 }
 
 int64_t integer(PyObject* o) {
@@ -125,16 +167,6 @@ bool truth(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw PyError();
   return v != 0;
-}
-
-void* stream_of(PyObject* o, int dev) {
-  if (!given(o)) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (h == nullptr) throw PyError();
-  void* s = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (s == nullptr && PyErr_Occurred()) throw PyError();
-  return s;
 }
 
 // Runs a call of the library without the interpreter lock; NtsError on a failure.
@@ -227,16 +259,16 @@ PyObject* qknorm_rope(PyObject* const* a) {
   const RopeArgs r(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
   const float eps = real(a[7]);
   const int il = truth(a[8]);
-  const Rows yq = rows_out("out_q", a[9], r.dev, r.q.t), yk = rows_out("out_k", a[10], r.dev, r.k.t);
+  const On on(a[14], r.dev);
+  const Rows yq = rows_out("out_q", a[9], on, r.q.t), yk = rows_out("out_k", a[10], on, r.k.t);
   const bool want = truth(a[13]);
   at::Tensor rq, rk;
-  if (want || given(a[11])) rq = output("rinv_q", a[11], {r.T, r.nq}, at::kFloat, r.dev);
-  if (want || given(a[12])) rk = output("rinv_k", a[12], {r.T, r.nk}, at::kFloat, r.dev);
-  void* stream = stream_of(a[14], r.dev);
+  if (want || given(a[11])) rq = output("rinv_q", a[11], {r.T, r.nq}, at::kFloat, on);
+  if (want || given(a[12])) rk = output("rinv_k", a[12], {r.T, r.nk}, at::kFloat, on);
   call([&] {
     return nts_qknorm_rope(ptr(r.q.t), r.q.ld, r.gq, ptr(yq.t), yq.ld, fptr(rq), ptr(r.k.t),
                            r.k.ld, r.gk, ptr(yk.t), yk.ld, fptr(rk), r.pos, r.table, r.P, r.T, r.nq,
-                           r.nk, r.d, r.rot, il, eps, stream);
+                           r.nk, r.d, r.rot, il, eps, on.handle);
   });
   return tuple_of(yq.t, yk.t, rq, rk);
 }
@@ -248,31 +280,25 @@ PyObject* qknorm_rope_backward(PyObject* const* a) {
   const float eps = real(a[9]);
   const int il = truth(a[10]);
   const Rows dyq = rows("dyq", a[0], r.dev, &r.q.t), dyk = rows("dyk", a[1], r.dev, &r.k.t);
-  const Rows dq = rows_out("out_dq", a[11], r.dev, r.q.t);
-  const Rows dk = rows_out("out_dk", a[12], r.dev, r.k.t);
-  const at::Tensor dgq = output("dgamma_q", a[13], {r.d}, at::kFloat, r.dev);
-  const at::Tensor dgk = output("dgamma_k", a[14], {r.d}, at::kFloat, r.dev);
+  const On on(a[16], r.dev);
+  const Rows dq = rows_out("out_dq", a[11], on, r.q.t);
+  const Rows dk = rows_out("out_dk", a[12], on, r.k.t);
+  const at::Tensor dgq = output("dgamma_q", a[13], {r.d}, at::kFloat, on);
+  const at::Tensor dgk = output("dgamma_k", a[14], {r.d}, at::kFloat, on);
   at::Tensor ws;
   if (given(a[15])) {
     ws = flat("workspace", a[15], at::kByte, r.dev);
   } else {
     int64_t bytes = 0;
     call([&] { return nts_qknorm_rope_backward_workspace(r.d, &bytes); });
-    ws = fresh({bytes}, at::kByte, r.dev);
-    if (given(a[16])) {   // torch may hand it on only after the call has run
-      PyObject* w = wrap(ws);
-      PyObject* done = PyObject_CallMethod(w, "record_stream", "O", a[16]);
-      Py_DECREF(w);
-      if (done == nullptr) throw PyError();
-      Py_DECREF(done);
-    }
+    if (on.foreign) refuse("a %s is needed on the legacy or per-thread stream", "workspace");
+    ws = scratch({bytes}, at::kByte, on);
   }
-  void* stream = stream_of(a[16], r.dev);
   call([&] {
     return nts_qknorm_rope_backward(ptr(dyq.t), dyq.ld, ptr(dyk.t), dyk.ld, ptr(r.q.t), r.q.ld,
                                     r.gq, ptr(r.k.t), r.k.ld, r.gk, r.pos, r.table, r.P, ptr(dq.t),
                                     dq.ld, ptr(dk.t), dk.ld, fptr(dgq), fptr(dgk), ptr(ws),
-                                    ws.numel(), r.T, r.nq, r.nk, r.d, r.rot, il, eps, stream);
+                                    ws.numel(), r.T, r.nq, r.nk, r.d, r.rot, il, eps, on.handle);
   });
   return tuple_of(dq.t, dk.t, dgq, dgk);
 }
@@ -293,14 +319,14 @@ PyObject* rmsnorm_blockcast(PyObject* const* a) {
     gamma = fptr(g);
   }
   const float eps = real(a[2]);
-  const at::Tensor codes = output("codes", a[3], {T, D}, at::kByte, dev);
-  const at::Tensor scales = output("scales", a[4], {T, blocks(D)}, at::kFloat, dev);
+  const On on(a[7], dev);
+  const at::Tensor codes = output("codes", a[3], {T, D}, at::kByte, on);
+  const at::Tensor scales = output("scales", a[4], {T, blocks(D)}, at::kFloat, on);
   at::Tensor rinv;
-  if (truth(a[6]) || given(a[5])) rinv = output("rinv", a[5], {T}, at::kFloat, dev);
-  void* stream = stream_of(a[7], dev);
+  if (truth(a[6]) || given(a[5])) rinv = output("rinv", a[5], {T}, at::kFloat, on);
   call([&] {
     return nts_rmsnorm_blockcast(ptr(x), gamma, static_cast<uint8_t*>(ptr(codes)), fptr(scales),
-                                 fptr(rinv), T, D, eps, stream);
+                                 fptr(rinv), T, D, eps, on.handle);
   });
   return tuple_of(codes, scales, rinv);
 }
@@ -311,12 +337,12 @@ PyObject* blockcast(PyObject* const* a) {
   const at::Tensor& x = matrix("x", flat("x", a[0], at::kBFloat16, dev));
   const int64_t T = x.size(0), D = x.size(1), per = integer(a[1]);
   if (per != 1 && per != kBlock) refuse("%s must be 1 or 128", "block_rows");
-  const at::Tensor codes = output("codes", a[2], {T, D}, at::kByte, dev);
-  const at::Tensor scales = output("scales", a[3], {blocks(T, per), blocks(D)}, at::kFloat, dev);
-  void* stream = stream_of(a[4], dev);
+  const On on(a[4], dev);
+  const at::Tensor codes = output("codes", a[2], {T, D}, at::kByte, on);
+  const at::Tensor scales = output("scales", a[3], {blocks(T, per), blocks(D)}, at::kFloat, on);
   call([&] {
     return nts_blockcast(ptr(x), static_cast<uint8_t*>(ptr(codes)), fptr(scales), T, D, (int)per,
-                         stream);
+                         on.handle);
   });
   return tuple_of(codes, scales, at::Tensor());
 }
@@ -326,11 +352,11 @@ PyObject* blockcast_t(PyObject* const* a) {
   const int dev = device_of("x", tensor("x", a[0]));
   const at::Tensor& x = matrix("x", flat("x", a[0], at::kBFloat16, dev));
   const int64_t T = x.size(0), D = x.size(1);
-  const at::Tensor codes = output("codes", a[1], {D, (T + 15) / 16 * 16}, at::kByte, dev);
-  const at::Tensor scales = output("scales", a[2], {D, blocks(T)}, at::kFloat, dev);
-  void* stream = stream_of(a[3], dev);
+  const On on(a[3], dev);
+  const at::Tensor codes = output("codes", a[1], {D, (T + 15) / 16 * 16}, at::kByte, on);
+  const at::Tensor scales = output("scales", a[2], {D, blocks(T)}, at::kFloat, on);
   call([&] {
-    return nts_blockcast_t(ptr(x), static_cast<uint8_t*>(ptr(codes)), fptr(scales), T, D, stream);
+    return nts_blockcast_t(ptr(x), static_cast<uint8_t*>(ptr(codes)), fptr(scales), T, D, on.handle);
   });
   return tuple_of(codes, scales, at::Tensor());
 }
@@ -366,12 +392,12 @@ PyObject* gemm_blockscaled(PyObject* const* a) {
     if (t != at::kFloat && t != at::kBFloat16) refuse("%s must be bfloat16 or float32", "out");
     fp32 = t == at::kFloat;
   }
-  const at::Tensor y = output("out", a[4], {M, N}, fp32 ? at::kFloat : at::kBFloat16, dev);
-  void* stream = stream_of(a[6], dev);
+  const On on(a[6], dev);
+  const at::Tensor y = output("out", a[4], {M, N}, fp32 ? at::kFloat : at::kBFloat16, on);
   call([&] {
     return nts_gemm_blockscaled(static_cast<uint8_t*>(ptr(x)), fptr(sx),
                                 static_cast<uint8_t*>(ptr(w)), fptr(sw), per, ptr(y),
-                                fp32 ? NTS_OUT_FP32 : NTS_OUT_BF16, M, N, K, stream);
+                                fp32 ? NTS_OUT_FP32 : NTS_OUT_BF16, M, N, K, on.handle);
   });
   return wrap(y);
 }
