@@ -24,7 +24,12 @@ namespace {
 
 constexpr int kCastThreads = 256;
 constexpr int kCastWarps = kCastThreads / 32;
-constexpr int64_t kRingValues = 4 << 20;   // values of X from which the ring kernel runs
+// Values of X from which the ring kernel runs: below, its warps start with
+// nothing in flight and the launch is over before that pays (us in a graph: with
+// the norm, [256, 4096] 2.9 direct, 3.6 by the ring, [400, 5120] 3.7 and 4.1,
+// [800, 5120] 6.8 and 6.5, [1000, 4096] 6.8 and 5.1; without, [1000, 4096] 3.8 and
+// 4.3, [2048, 4096] 6.5 by the ring).
+constexpr int64_t kRingValues = 4 << 20, kNormRingValues = 3 << 20;
 
 // kStatusTimeout bits of these kernels.
 __device__ unsigned int g_cast_status;
@@ -547,13 +552,12 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
                   tune.pdl != 0);
   }
 
-  // Many rows: the ring.  Up to a few MB the launch is over before a ring pays
-  // (its warps start with nothing in flight), and parts of rows below 2 KB
-  // cost more to hand out than to load.
+  // Many rows: the ring.  Parts of rows below 2 KB cost more to hand out than to
+  // load ([32768, 512] 12.1 us direct, 14.9 by the ring).
   const bool norm = rq.kind == kCastNorm;
   const bool flat = !norm && rq.D % 128 == 0;   // one long row: no block ends early
   const int64_t units = flat ? rq.T * (rq.D / 16) : p.units;
-  if (tune.force_stages > 0 || (rq.T * rq.D >= kRingValues && units >= 64)) {
+  if (tune.force_stages > 0 || (rq.T * rq.D >= (norm ? kNormRingValues : kRingValues) && units >= 64)) {
     p.ring_units = units;
     if (flat) p.T = 1;
     p.wpr = 1;

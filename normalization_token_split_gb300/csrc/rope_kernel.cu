@@ -36,7 +36,11 @@ __device__ unsigned int g_rope_status;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
-constexpr int kDirectItems = 16;     // warp items per SM up to which nothing is staged
+// Warp items per SM up to which nothing is staged: a launch that small is over
+// before a ring of copies pays (32 + 8 heads of 128, us in a graph: forward, T =
+// 120: 2.1 direct, 3.6 by the ring; 300: 3.7 both; backward, T = 30: 4.6 and
+// 5.3; 60: 5.9 and 5.2, 120: 7.5 and 6.8).
+constexpr int kDirectItems = 16, kBackwardDirectItems = 3;
 constexpr int kFusedSums = 1 << 15;  // partial sums up to which the last CTA adds them up
 constexpr int kForwardRounds = 4, kForwardStages = 2;
 constexpr int kBackwardRounds = 2, kBackwardStages = 2;
@@ -391,12 +395,24 @@ __device__ __forceinline__ void reduce_gain_grad(const RopeParams& p, const Rope
     const unsigned begin = i ? p.ctas_q : 0, end = i ? gridDim.x : p.ctas_q;
     const float4* row = reinterpret_cast<const float4*>(p.partial) + c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (4 * c < p.d)
-#pragma unroll 8
-      for (unsigned r = begin + r0; r < end; r += rows) {
-        const float4 x = __ldcg(row + (int64_t)r * (p.d / 4));
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-      }
+    // 32 strided sums per column, this thread's four at a time
+    for (int w0 = r0; w0 < 32 && 4 * c < p.d; w0 += 4 * rows) {
+      float4 a[4] = {};
+#pragma unroll 4
+      for (unsigned r = begin; r < end; r += 32)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned at = r + w0 + k * rows;
+          if (w0 + k * rows < 32 && at < end) {
+            const float4 x = __ldcg(row + (int64_t)at * (p.d / 4));
+            a[k].x += x.x, a[k].y += x.y, a[k].z += x.z, a[k].w += x.w;
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (w0 + k * rows < 32)
+          v.x += a[k].x, v.y += a[k].y, v.z += a[k].z, v.w += a[k].w;
+    }
     __syncthreads();
     part[threadIdx.x] = v;
     __syncthreads();
@@ -746,25 +762,50 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(con
 
 // dgamma = the sum of the CTAs' rows as a launch of its own, for many rows (one
 // CTA would take longer than the launch) and inside a graph: block (32 columns)
-// x (strided rows), blockIdx.y the tensor.  A sum that the last CTA of an eager
-// call would make gets that one's number of rows, and so its order and its bits.
-__global__ void __launch_bounds__(1024) rope_gain_grad_kernel(const float* partial, unsigned nq,
-                                                              unsigned n, int d, float* dgamma_q,
-                                                              float* dgamma_k) {
+// x (8 threads with four of 32 strided sums each), blockIdx.y the tensor.  The
+// strided sums are added in the order of the last CTA of an eager call, whose
+// threads have ROWS rows: equal bits.
+template <int ROWS>
+__global__ void __launch_bounds__(256) rope_gain_grad_kernel(const float* partial, unsigned nq,
+                                                             unsigned n, int d, float* dgamma_q,
+                                                             float* dgamma_k) {
   __shared__ float red[32][32];
   const int col = blockIdx.x * 32 + threadIdx.x;
   const unsigned r0 = blockIdx.y ? nq : 0, r1 = blockIdx.y ? n : nq;
   grid_dependency_wait();
   allow_dependent_launch();
-  float v = 0.f;
+  float v[4] = {};
   if (col < d)
-#pragma unroll 8
-    for (unsigned r = r0 + threadIdx.y; r < r1; r += blockDim.y) v += partial[(int64_t)r * d + col];
-  red[threadIdx.y][threadIdx.x] = v;
+#pragma unroll 4
+    for (unsigned r = r0 + threadIdx.y; r < r1; r += 32)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r + 8 * k < r1) v[k] += partial[(int64_t)(r + 8 * k) * d + col];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) red[threadIdx.y + 8 * k][threadIdx.x] = v[k];
   __syncthreads();
   if (threadIdx.y != 0 || col >= d) return;
-  for (int w = 1; w < (int)blockDim.y; ++w) v += red[w][threadIdx.x];
-  (blockIdx.y ? dgamma_k : dgamma_q)[col] = v;
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < ROWS; ++w) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = w; k < 32; k += ROWS) t += red[k][threadIdx.x];
+    sum = w == 0 ? t : sum + t;
+  }
+  (blockIdx.y ? dgamma_k : dgamma_q)[col] = sum;
+}
+
+using GainGradKernel = void (*)(const float*, unsigned, unsigned, int, float*, float*);
+
+GainGradKernel pick_gain_grad(int rows) {
+  switch (rows) {
+    case 2: return rope_gain_grad_kernel<2>;
+    case 4: return rope_gain_grad_kernel<4>;
+    case 8: return rope_gain_grad_kernel<8>;
+    case 16: return rope_gain_grad_kernel<16>;
+    default: return rope_gain_grad_kernel<32>;
+  }
 }
 
 using RopeKernel = void (*)(RopeParams);
@@ -886,7 +927,8 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   uint64_t items[2];
   int rc = set_items(&p, 1, items);
   if (rc != NTS_OK) return rc;
-  const bool ring = tune.force_rows > 0 || items[0] + items[1] > (uint64_t)dev.sm_count * kDirectItems;
+  const bool ring = tune.force_rows > 0 ||
+                    items[0] + items[1] > (uint64_t)dev.sm_count * kBackwardDirectItems;
   size_t smem = (size_t)kRopeWarps * std::max(p.d, 128) * sizeof(float);
   RopeKernel kern = rq.interleaved ? rope_backward_kernel<true> : rope_backward_kernel<false>;
   if (ring) {
@@ -905,7 +947,7 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   const uint64_t nq = (items[0] + kRopeWarps - 1) / kRopeWarps;
   const uint64_t nk = (items[1] + kRopeWarps - 1) / kRopeWarps;
   const uint64_t most =
-      std::min<uint64_t>((uint64_t)(ring ? per_sm : 1) * dev.sm_count, kRopePartials);
+      std::min<uint64_t>((uint64_t)per_sm * dev.sm_count, kRopePartials);
   uint64_t gq = nq, gk = nk;
   if (gq + gk > most) {
     const uint64_t all = items[0] + items[1];
@@ -935,10 +977,9 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
              p.ctas_q);
   rc = launch(kern, dim3(grid), dim3(kRopeThreads), smem, stream, tune.pdl != 0, p);
   if (rc != NTS_OK || p.sched != nullptr) return rc;
-  const int rows = few ? kRopeThreads / sum_columns(p.d) : 32;
-  return launch(rope_gain_grad_kernel, dim3((p.d + 31) / 32, 2), dim3(32, rows), 0, stream,
-                tune.pdl != 0, (const float*)workspace, (unsigned)gq, grid, p.d, dgamma_q,
-                dgamma_k);
+  return launch(pick_gain_grad(kRopeThreads / sum_columns(p.d)), dim3((p.d + 31) / 32, 2),
+                dim3(32, 8), 0, stream, tune.pdl != 0, (const float*)workspace, (unsigned)gq, grid,
+                p.d, dgamma_q, dgamma_k);
 }
 
 int read_and_clear_rope_status(unsigned* out) {
