@@ -21,9 +21,15 @@ extern "C" {
  * Override the automatic launch shape.  Each argument 0 means automatic.
  *   vpt        QK kernel: 16-byte vectors per thread, one of {1,2,3,4,5,6,8};
  *              MX kernels: MX blocks per thread (halves of 64-value
- *              blocks for B = 64), 1..8 with at most 16 vectors per thread
- *   rows       token rows per tile (rows * threads-per-row <= 480)
- *   stages     shared-memory ring stages (>= 1)
+ *              blocks for B = 64), 1..8 with at most 16 vectors per thread;
+ *              nts_gemm_blockscaled: the kernel, 1 = of few rows, 2 = of single
+ *              CTAs, 3 = of CTA pairs (other values: automatic)
+ *   rows       token rows per tile (rows * threads-per-row <= 480);
+ *              nts_qknorm_rope and its gradient: the ring kernel, with at most
+ *              this many rounds of heads per stage
+ *   stages     shared-memory ring stages (>= 1); with rows, those of the
+ *              rotation's ring; nts_rmsnorm_blockcast and nts_blockcast (block_rows
+ *              1): any value forces the ring kernel
  *   grid       CTAs (MX kernels) or clusters (QK kernel) of the persistent grid
  *   smem_budget bytes a CTA's ring aims to stay under (default 102400)
  * Errors: INVALID_ARG for negative values or vpt > 8.  A shape the

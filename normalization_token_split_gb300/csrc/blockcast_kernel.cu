@@ -10,7 +10,11 @@
 // blocks of zeros and of values that no sum with others would show.
 // RMSNorm: rinv = 1 / sqrt((1/D) sum x^2 + eps), w = fp32(fp32(x gamma) rinv).
 //
-// All of these are bound by HBM: 2 bytes read and 1 + 4/128 written per value.
+// All of these are bound by HBM, 2 bytes read and 1 + 4/128 written per value,
+// as far as their instructions allow.  Measured (us, back to back in a graph; of the copy's rate): with the
+// norm [16384, 4096] 37.5, 0.80, issue slots 65 % busy with 16 warps an SM;
+// [64, 4096] 2.4; without, [16384, 4096] 33.2, 0.91; weights [10240, 5120] 24.8,
+// 0.94; the transpose of [4099, 5120] 12.3, 0.77.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -18,7 +18,14 @@
 // two neighbouring vectors of the unrotated rest beyond.  d/16 lanes, rounded
 // up to a power of two, hold a head, so the row sums are xor-shuffles inside
 // a warp and nothing crosses a warp.  A warp takes a few heads of one token at
-// a time, with one read of the table row and the gain for all of them.
+// a time, with one read of the table row and the gain for all of them: that read
+// and the position's latency are what a round of heads costs beside its data.
+//
+// Measured (us, back to back in a graph; of the copy's rate): forward [8192, 40
+// + 40 heads of 128] 53.4, 0.94; [1237, 20 + 4 heads of 96, 64 turned] 5.8; one
+// token of 32 + 32 heads 1.9 (an empty launch 1.0 to 1.5).  Backward [8192, 40 +
+// 40] 89.6, 0.84: two values in for each out, and 127 registers leave 16 warps
+// an SM to cover the ring's latencies; [333, 32 + 8 heads of 64] 5.5.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,7 +48,14 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 // 120: 2.1 direct, 3.6 by the ring; 300: 3.7 both; backward, T = 30: 4.6 and
 // 5.3; 60: 5.9 and 5.2, 120: 7.5 and 6.8).
 constexpr int kDirectItems = 16, kBackwardDirectItems = 3;
-constexpr int kFusedSums = 1 << 15;  // partial sums up to which the last CTA adds them up
+// Partial sums up to which the last CTA of an eager backward call adds them up:
+// one CTA's loads take longer than a second launch from there on ([240, 32 + 8
+// heads of 128], 38912 sums: 14.6 us a call by one CTA, 9.9 by a launch).
+constexpr int kFusedSums = 1 << 15;
+// Rounds of heads per ring stage, and stages per warp.  Fewer rounds pay the
+// token's reads more often ([4096, 32 + 8 heads of 128], us: forward 27.5 with one
+// round, 20.0 with two, 16.4 with four; backward 34.8 and 30.2); more rounds and
+// more stages measured no faster.
 constexpr int kForwardRounds = 4, kForwardStages = 2;
 constexpr int kBackwardRounds = 2, kBackwardStages = 2;
 
