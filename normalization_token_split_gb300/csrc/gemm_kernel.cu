@@ -254,7 +254,8 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // a pair's copies all count on the first CTA's barrier
             const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
             bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
-            if (leader) {
+            n += late ^ 1u;
+            if (leader && !late) {   // a second arrival in a phase would be one too many
               if (rank == 0)
                 mbar_arrive_expect_tx(
                     bar, C::kStage * (PAIR ? 2 : 1) +
@@ -267,7 +268,6 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
             __syncwarp();
           }
-          n += k1 - k0;
         }
       }
       if (lane == 0) *issued = n;
@@ -298,7 +298,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (h == H - 1) stored = bar_test(full + 8 * (v / H), turn);
             drained = bar_test(tempty + 8 * (v % NB), (turn & flips) ^ (v / NB & 1) ^ 1u);
             tcgen05_fence_after();
-            if (leader) {
+            if (leader && !late) {
               constexpr uint32_t kNext = C::kStage >> 4, kHalf = C::kRowsW / H * 128 >> 4;
               mma_block<PAIR>(tmem + b * C::kBufCols, da + i * kNext, dw + i * kNext + h * kHalf,
                               instr);
@@ -642,7 +642,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     for (int u = u0; u < u1 && !late; ++u, st.advance()) {
       const uint32_t at = sbase + st.i * C::kStage, bar = full + 8 * st.i;
       bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
-      if (leader) {
+      if (leader && !late) {   // a second arrival in a phase would be one too many
         mbar_arrive_expect_tx(bar, C::kStage + (u == u0 ? p.missing_tx : 0u));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -666,7 +666,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       bar_wait(tempty + 8 * tb.i, tb.parity ^ 1u, p.wait_limit_ns, stop_at, late);
       bar_wait(full + 8 * st.i, st.parity, p.wait_limit_ns, stop_at, late);
       tcgen05_fence_after();
-      if (leader) {
+      if (leader && !late) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           mma_block<false>(d + i * TN, dw + i * (C::kW >> 4), da + i * (C::kA >> 4), instr);
@@ -948,11 +948,11 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   int kind = tune.force_vpt <= kPair ? tune.force_vpt : kAuto;   // debug: one of these
   if (kind == kAuto) {
     // Few tiles of 128 x 128: their K loops leave SMs idle, and narrow_kernel
-    // splits K (us, narrow / one CTA: [200, 4096] x [1024, 4096] 7.9 / 12.7,
-    // [100, 4096] x [4096, 4096] 11.1 / 13.0; the other way round from 40 tiles,
-    // [128, 5120] x [5120, 5120] 18.3 / 15.5).  Up to 64 rows of A it reads W
-    // with less waste and holds out longer ([64, 5120] x [5120, 5120] 12.1 /
-    // 14.8, [64, 5120] x [15360, 5120] 20.7 / 16.7), up to 32 always.
+    // splits K (us, narrow / one CTA: [200, 4096] x [1024, 4096] 8.2 / 12.2,
+    // [100, 4096] x [4096, 4096] 10.1 / 12.6; [128, 5120] x [5120, 5120], 40
+    // tiles, 15.1 both; [128, 5120] x [15360, 5120] 26.6 / 17.4).  Up to 64 rows
+    // of A it reads W with less waste and holds out longer ([64, 5120] x [5120,
+    // 5120] 10.9 / 14.5, [64, 5120] x [15360, 5120] 17.9 / 16.9), up to 32 always.
     const int64_t ones = (p.M + 127) / 128 * ((p.N + 127) / 128);
     const int64_t pairs = (p.M + 255) / 256 * ((p.N + 255) / 256);
     const int64_t sms = dev.sm_count;
@@ -960,8 +960,8 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
       kind = kNarrow;
     } else {
       // A K block takes a pair ~1.5 times as long as one CTA: by the rounds of
-      // tiles ([333, 5120] x [5120, 5120] one CTA 16.0, pair 24.1; [512, 5120]
-      // 28.7 and 24.1, as 160 tiles take two rounds).
+      // tiles ([333, 5120] x [5120, 5120] one CTA 15.6, pair 22.5; [512, 5120]
+      // 27.8 and 22.8, as 160 tiles take two rounds).
       const int64_t rounds = (ones + sms - 1) / sms, rounds2 = (pairs + sms / 2 - 1) / (sms / 2);
       kind = 2 * rounds <= 3 * rounds2 ? kWide : kPair;
     }

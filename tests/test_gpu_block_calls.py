@@ -340,3 +340,32 @@ def test_far_positions_at_the_ends_of_their_type():
     with pytest.raises(nts.NtsError, match="rotation table"):
         nts.check_status()
     assert not y[3].any() and y[4].any()
+
+
+@pytest.mark.parametrize("kernel", [1, 2, 3])
+@pytest.mark.parametrize("rows", [128, 1])
+def test_a_copy_that_never_lands_ends_a_long_product(kernel, rows):
+    """More K blocks than the ring has stages: what gave up issues nothing more."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    M, N, K = 600, 520, 2048
+    a = torch.randint(0, 127, (M, K), generator=g, device=DEV).to(torch.uint8)
+    w = torch.randint(0, 127, (N, K), generator=g, device=DEV).to(torch.uint8)
+    sa = torch.rand(M, K // 128, generator=g, device=DEV)
+    sw = torch.rand(-(-N // rows), K // 128, generator=g, device=DEV)
+    try:
+        nts.set_tuning(vpt=kernel)
+        want = nts.gemm_blockscaled(a, sa, w, sw)
+        nts.check_status()
+        nts.set_wait_limit_ns(20_000_000)
+        nts.set_missing_tx(16)
+        nts.gemm_blockscaled(a, sa, w, sw)
+        with pytest.raises(nts.NtsError, match="TIMEOUT"):
+            nts.check_status()
+        nts.set_missing_tx(0)
+        nts.set_wait_limit_ns(0)
+        assert torch.equal(nts.gemm_blockscaled(a, sa, w, sw), want)
+        nts.check_status()
+    finally:
+        nts.set_missing_tx(0)
+        nts.set_wait_limit_ns(0)
+        nts.set_tuning()
