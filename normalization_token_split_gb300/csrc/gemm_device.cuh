@@ -30,9 +30,10 @@ __device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
 // branch they decide how fast it turns.  A wait that expires (limit_ns, or
 // another role of the CTA set *stop) sets *stop and `late`; once `late` is set
 // the waits that follow return at once, so a role may look at it only now and
-// then, as long as what it does meanwhile stays inside its own memory and makes
-// no copy, matrix instruction or arrival that counts bytes: the arrivals of such
-// a barrier's phase may all be there while bytes are missing.  The clock is read only after many tries: a read takes longer than most waits.
+// then, as long as what it does meanwhile stays inside its own memory and arrives
+// at no barrier that counts bytes: all arrivals of such a phase may be there
+// while bytes are missing, and one more is a fault.  The clock is read only after
+// many tries: a read takes longer than most waits.
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                          uint32_t stop, uint32_t& late, uint32_t done = 0) {
   asm volatile(

@@ -254,8 +254,11 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // a pair's copies all count on the first CTA's barrier
             const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
             bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
+            // *stop too: the matrix warp frees stages for the rest of a turn after its own
+            // wait gave up, whose full phase still has all its arrivals and misses bytes
+            late |= (uint32_t)*stop;
             n += late ^ 1u;
-            if (leader && !late) {   // a second arrival in a phase would be one too many
+            if (leader && !late) {
               if (rank == 0)
                 mbar_arrive_expect_tx(
                     bar, C::kStage * (PAIR ? 2 : 1) +
@@ -298,7 +301,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (h == H - 1) stored = bar_test(full + 8 * (v / H), turn);
             drained = bar_test(tempty + 8 * (v % NB), (turn & flips) ^ (v / NB & 1) ^ 1u);
             tcgen05_fence_after();
-            if (leader && !late) {
+            if (leader) {   // (a look at `late` here costs 2 % of a product)
               constexpr uint32_t kNext = C::kStage >> 4, kHalf = C::kRowsW / H * 128 >> 4;
               mma_block<PAIR>(tmem + b * C::kBufCols, da + i * kNext, dw + i * kNext + h * kHalf,
                               instr);
