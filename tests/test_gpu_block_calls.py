@@ -207,6 +207,28 @@ def test_what_a_call_makes_belongs_to_its_stream():
     nts.check_status()
 
 
+def test_two_graphs_replayed_at_once_beside_eager_calls():
+    runs = [everything(i) for i in range(3)]
+    want = [r() for r in runs]
+    graphs, caps = [], []
+    for r in runs[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            caps.append(r())
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        eager = runs[2]()
+    torch.cuda.synchronize()
+    for got, w in zip(caps + [eager], want):
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+    nts.check_status()
+
+
 class Handle:
     def __init__(self, handle):
         self.cuda_stream = handle
