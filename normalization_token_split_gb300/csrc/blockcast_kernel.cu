@@ -191,16 +191,19 @@ __global__ void __launch_bounds__(kCastThreads) blockcast_rows_kernel(const Cast
 
 // The same for many rows: persistent warps, each with its own ring of kStages
 // shared-memory stages that its lane 0 keeps filled with 1-D bulk copies, so
-// that the next parts of rows are in flight while one is cast.  A warp's part
-// is at most 128 units (4 KB); with RMSNorm the wpr warps of a row add their
-// sums of squares through shared memory behind a named barrier, and the part
-// is read a second time from shared memory, not kept in registers.  A thread
-// reads the two vectors of its unit in the order that lets the 8 lanes of each
-// shared-memory phase hit distinct banks.  GAIN: a thread meets the same four
-// units of the gain on every row and keeps them in registers (from L1, a warp's
-// 64-byte steps take 16 passes a load: [16384, 4096] 45.2 us, 37.2 so).
+// that the next parts of rows are in flight while one is cast.  With RMSNorm the
+// wpr warps of a row add their sums of squares through shared memory behind a
+// named barrier, and the part is read a second time from shared memory, not kept
+// in registers.  The barrier is what parts cost, so they are as large as the
+// gain's registers allow: 160 units (5 KB; [16384, 4096] by four warps a row in
+// place of two 50.3 us, 37.5 so); without the norm 128.  A thread reads the two
+// vectors of its unit in the order that lets the 8 lanes of each shared-memory
+// phase hit distinct banks.  GAIN: a thread meets the same units of the gain on
+// every row and keeps the first four in registers (all from L1, where a warp's
+// 64-byte steps take 16 passes a load: [16384, 4096] 45.2 us); a fifth is read
+// from L1 ([8192, 5120] 26.8 us, 32.7 by four warps a row).
 constexpr int kStages = 2;
-constexpr int kPartUnits = 128;
+constexpr int kPartUnits = 160, kHeldUnits = 128;
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -250,10 +253,10 @@ blockcast_ring_kernel(const CastParams p) {
   };
   for (int64_t n = 0; n < min64(mine, kStages); ++n) issue(n);
 
-  float gain[GAIN ? kPartUnits / 32 : 1][2][8];   // halves in this lane's order
+  float gain[GAIN ? kHeldUnits / 32 : 1][2][8];   // halves in this lane's order
   if (GAIN)
 #pragma unroll
-    for (int i = 0; i < kPartUnits / 32; ++i)
+    for (int i = 0; i < kHeldUnits / 32; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int u = sub * p.seg + 32 * i + lane;
@@ -359,8 +362,22 @@ blockcast_ring_kernel(const CastParams p) {
     };
     if (GAIN) {
 #pragma unroll
-      for (int i = 0; i < kPartUnits / 32; ++i)
+      for (int i = 0; i < kHeldUnits / 32; ++i)
         if (32 * i < units) cast_unit(32 * i + lane, gain[i]);
+      if (units > kHeldUnits) {
+        float g[2][8] = {};
+        const int u = kHeldUnits + lane;
+        if (u < units)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4* at =
+                reinterpret_cast<const float4*>(p.gamma + (unit + u) * 16 + 8 * (h ^ swap));
+            const float4 a = __ldg(at), b = __ldg(at + 1);
+            g[h][0] = a.x, g[h][1] = a.y, g[h][2] = a.z, g[h][3] = a.w;
+            g[h][4] = b.x, g[h][5] = b.y, g[h][6] = b.z, g[h][7] = b.w;
+          }
+        cast_unit(u, g);
+      }
     } else {
 #pragma unroll 2
       for (int i = 0; i < units; i += 32) cast_unit(i + lane, gain[0]);
@@ -567,7 +584,7 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
     p.wpr = 1;
     if (norm)
       while (p.wpr < kCastWarps && p.units > p.wpr * kPartUnits) p.wpr *= 2;
-    const int64_t per = norm ? (p.units + p.wpr - 1) / p.wpr : std::min<int64_t>(units, kPartUnits);
+    const int64_t per = norm ? (p.units + p.wpr - 1) / p.wpr : std::min<int64_t>(units, kHeldUnits);
     p.seg = (int)((per + 7) / 8 * 8);
     const int64_t segs = (units + p.seg - 1) / p.seg;
     if (!norm && segs >= (1ll << 31)) return fail(NTS_ERR_UNSUPPORTED, "matrix too large");
@@ -575,7 +592,7 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
     p.wait_limit_ns = tune.wait_limit_ns;
     p.missing_tx = tune.missing_tx;
     const size_t smem = (size_t)kCastWarps * kStages * p.seg * 32;
-    const bool gain = norm && p.gamma != nullptr && p.seg <= kPartUnits;   // D <= 16384
+    const bool gain = norm && p.gamma != nullptr && p.seg <= kPartUnits;   // D <= 20480
     const CastKernel kern = gain   ? blockcast_ring_kernel<true, true>
                             : norm ? blockcast_ring_kernel<true, false>
                                    : blockcast_ring_kernel<false, false>;

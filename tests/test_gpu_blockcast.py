@@ -94,6 +94,29 @@ def test_ring_kernel_on_any_shape(T, D):
         assert torch.equal(o.codes.cpu(), ref.block_codes(w, scales, 1))
 
 
+@pytest.mark.parametrize("D", [2048, 2064, 2304, 2560, 2576, 4096, 4112, 5104, 5120, 5136, 10240,
+                               16384, 16400, 20480, 20496])
+def test_ring_kernel_at_the_ends_of_its_parts(D):
+    """Widths at which a row goes to more warps, and at which a warp's part
+    outgrows the gains that it keeps in registers."""
+    T = 40
+    x = rows(T, D, D).to(DEV)
+    gamma = 1.0 + 0.1 * torch.randn(D, generator=torch.Generator().manual_seed(3)).to(DEV)
+    try:
+        nts.set_tuning(stages=2)
+        o = nts.rmsnorm_blockcast(x, gamma, want_rinv=True)
+        nts.check_status()
+    finally:
+        nts.set_tuning()
+    rinv = o.rinv.cpu()
+    want = (x.cpu().double().square().mean(1) + EPS).rsqrt()
+    assert torch.all((rinv.double() - want).abs() <= (D / 2 + 4) * ref.U32 * want)
+    w = (x.float() * gamma).cpu() * rinv[:, None]
+    scales = ref.block_scales(w, 1)
+    assert torch.equal(o.scales.cpu(), scales)
+    assert torch.equal(o.codes.cpu(), ref.block_codes(w, scales, 1))
+
+
 def test_missing_copy_times_out_and_the_context_lives():
     x = rows(700, 5120, 1).to(DEV)
     want = nts.rmsnorm_blockcast(x)
