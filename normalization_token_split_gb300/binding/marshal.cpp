@@ -82,11 +82,16 @@ const at::Tensor& matrix(const char* name, const at::Tensor& t) {
 // The stream of a call.  What the call makes belongs to that stream, so that
 // memory that torch hands out again is free there; when it is not the current
 // one, torch also waits for the current stream, where the results are used, before
-// it hands an output on.
+// it hands an output on.  The legacy handle is the default stream under another
+// name.  The per-thread stream has no pool of torch's: what a call makes there
+// would come from the current stream's pool, where earlier work may still use
+// the memory and later work may be given it while the kernel writes.  Only when
+// the current stream is the default one does CUDA order the two both ways;
+// otherwise the call makes nothing (`pool` is false).
 struct On {
   int dev;
   void* handle;
-  bool foreign = false;
+  bool foreign = false, pool = true;
   std::optional<c10::cuda::CUDAStream> user;
   c10::cuda::OptionalCUDAStreamGuard guard;
 
@@ -100,11 +105,13 @@ struct On {
     Py_DECREF(h);
     if (handle == nullptr && PyErr_Occurred()) throw PyError();
     const cudaStream_t s = static_cast<cudaStream_t>(handle);
-    if (s == current.stream()) return;
-    foreign = s == cudaStreamLegacy || s == cudaStreamPerThread;   // no stream of torch's
+    const bool main = s == nullptr || s == cudaStreamLegacy;
+    if (s == current.stream() || (main && current.stream() == nullptr)) return;
+    foreign = s == cudaStreamPerThread;
+    pool = !foreign || current.stream() == nullptr;
     if (foreign) return;
     user = current;
-    guard.reset_stream(s == nullptr
+    guard.reset_stream(main
                            ? c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev)
                            : c10::cuda::getStreamFromExternal(s, (c10::DeviceIndex)dev));
   }
@@ -115,7 +122,10 @@ at::Tensor scratch(at::IntArrayRef shape, at::ScalarType type, const On& on) {
                                            std::nullopt));
 }
 
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const On& on) {
+at::Tensor fresh(const char* name, at::IntArrayRef shape, at::ScalarType type, const On& on) {
+  if (!on.pool)
+    refuse("%s is needed on the per-thread stream, as another than the default stream is current",
+           name);
   at::Tensor t = scratch(shape, type, on);
   if (on.user && t.numel() != 0)
     c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *on.user);
@@ -125,7 +135,7 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const On& on) {
 // The caller's output buffer, checked, or a new one.
 at::Tensor output(const char* name, PyObject* o, at::IntArrayRef shape, at::ScalarType type,
                   const On& on) {
-  if (!given(o)) return fresh(shape, type, on);
+  if (!given(o)) return fresh(name, shape, type, on);
   const at::Tensor& t = flat(name, o, type, on.dev);
   if (t.sizes() != shape) refuse("%s has the wrong shape", name);
   return t;
@@ -148,7 +158,7 @@ Rows rows(const char* name, PyObject* o, int dev, const at::Tensor* like = nullp
 
 Rows rows_out(const char* name, PyObject* o, const On& on, const at::Tensor& like) {
   if (given(o)) return rows(name, o, on.dev, &like);
-  return {fresh(like.sizes(), at::kBFloat16, on), like.size(1)};
+  return {fresh(name, like.sizes(), at::kBFloat16, on), like.size(1)};
 }
 
 int64_t integer(PyObject* o) {
@@ -291,7 +301,7 @@ PyObject* qknorm_rope_backward(PyObject* const* a) {
   } else {
     int64_t bytes = 0;
     call([&] { return nts_qknorm_rope_backward_workspace(r.d, &bytes); });
-    if (on.foreign) refuse("a %s is needed on the legacy or per-thread stream", "workspace");
+    if (on.foreign) refuse("a %s is needed on the per-thread stream", "workspace");
     ws = scratch({bytes}, at::kByte, on);
   }
   call([&] {

@@ -300,6 +300,10 @@ class BlockOut(NamedTuple):
 # The checks, missing outputs and the call itself are in binding/marshal.cpp:
 # these operators serve single tokens, where Python's share of a call would be
 # the larger part of it.
+#
+# stream: the current one when None.  What a call makes belongs to its stream.
+# On CUDA's per-thread stream, which torch has no pool for, the workspace is the
+# caller's, and the outputs too unless the default stream is current.
 
 def rope_table(P: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """The rotation table of qknorm_rope: fp32 [P, rot_dim], row pos the

@@ -391,3 +391,57 @@ def test_a_copy_that_never_lands_ends_a_long_product(kernel, rows):
         nts.set_missing_tx(0)
         nts.set_wait_limit_ns(0)
         nts.set_tuning()
+
+
+def test_outputs_on_the_per_thread_stream_beside_a_side_stream():
+    """A side stream does not wait for the per-thread stream, nor that one for it:
+    memory of the side stream's pool is not the call's to write."""
+    x = bf16(4, 256)
+    u8, s = torch.zeros(4, 256, dtype=torch.uint8, device=DEV), f32(4, 2)
+    ws = torch.empty(nts.rope_backward_workspace(D), dtype=torch.uint8, device=DEV)
+    want = [t.clone() for t in backward()]
+    outs = dict(out_dq=bf16(T, HQ * D), out_dk=bf16(T, HK * D), dgamma_q=f32(D), dgamma_k=f32(D))
+    a = rope_args()
+    torch.cuda.synchronize()
+    per_thread = Handle(2)
+    calls = {"out_q": lambda **k: forward(stream=per_thread, **k),
+             "codes": lambda **k: nts.blockcast(x, stream=per_thread, **k),
+             "out": lambda **k: nts.gemm_blockscaled(u8, s, u8, s[:1], stream=per_thread, **k)}
+    for fn in (nts.rmsnorm_blockcast, nts.blockcast_t):
+        with torch.cuda.stream(torch.cuda.Stream()), pytest.raises(ValueError, match="codes is needed"):
+            fn(x, stream=per_thread)
+    for name, fn in calls.items():
+        fn()                                      # the default stream waits for it, and it for that
+        with torch.cuda.stream(torch.cuda.Stream()), \
+                pytest.raises(ValueError, match=f"{name} is needed on the per-thread stream"):
+            fn()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for name in outs:
+            some = {k: v for k, v in outs.items() if k != name}
+            with pytest.raises(ValueError, match=f"{name} is needed on the per-thread stream"):
+                nts.qknorm_rope_backward(**a, workspace=ws, stream=per_thread, **some)
+        got = nts.qknorm_rope_backward(**a, workspace=ws, stream=per_thread, **outs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    nts.check_status()
+
+
+def test_the_legacy_handle_is_the_default_stream():
+    """What a call on it makes comes from the default stream's pool, a workspace too."""
+    want = [t.clone() for t in backward()]
+    a = rope_args()
+    torch.cuda.synchronize()
+    legacy = Handle(1)
+    got = nts.qknorm_rope_backward(**a, stream=legacy)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = nts.qknorm_rope_backward(**a, stream=legacy)
+        held = {b["address"] for seg in torch.cuda.memory_snapshot()
+                if seg["stream"] == side.cuda_stream for b in seg["blocks"]
+                if b["state"] == "active_allocated"}
+        assert not held & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    nts.check_status()
