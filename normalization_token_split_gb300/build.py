@@ -1,7 +1,9 @@
 """Builds libnts.so in-tree (normalization_token_split_gb300/_build/) with
 nvcc for sm_103a, and the Python extension beside it (marshal_nts.so, from
 binding/) with g++.  Translation units compile in parallel; a unit is rebuilt
-only when it or a header is newer than its object.
+only when it or a header is newer than its object, and a library is linked anew
+when it is older than one of its objects: what an earlier run compiled and did
+not come to link is linked by the next.
 
     python -m normalization_token_split_gb300.build [--force] [--verbose]
 """
@@ -72,6 +74,12 @@ def _binding_cmds(obj: str, cuda: str):
     return compile_, link, tmp
 
 
+def _stale(target: str, *inputs: str) -> bool:
+    """Whether target is missing or older than one of its inputs."""
+    return not os.path.exists(target) or \
+        os.path.getmtime(target) < max(map(os.path.getmtime, inputs))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
@@ -93,10 +101,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # the binding: its object compiles along with the others, and links after libnts.so
     obj = os.path.join(BUILD, "marshal.cpp.o")
     bind, bind_link, bind_tmp = _binding_cmds(obj, cuda)
-    newest = max(os.path.getmtime(BINDING), os.path.getmtime(os.path.join(INCLUDE, "nts.h")))
-    stale = force or not os.path.exists(obj) or os.path.getmtime(obj) < newest
-    lib_jobs = len(jobs)
-    if stale:
+    if force or _stale(obj, BINDING, os.path.join(INCLUDE, "nts.h")):
         jobs.append(bind)
 
     def run(cmd):
@@ -116,7 +121,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         msg = "\n\n".join(" ".join(c) + "\n" + o for c, o in failed)
         raise RuntimeError("libnts compilation failed:\n" + msg)
 
-    if lib_jobs or not os.path.exists(LIB):
+    if force or _stale(LIB, *objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
                 "-lpthread", "-ldl", "-lrt"]
@@ -124,7 +129,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("libnts link failed:\n" + " ".join(link) + "\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
-    if stale or not os.path.exists(MARSHAL):
+    if force or _stale(MARSHAL, obj):
         r = subprocess.run(bind_link, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("binding link failed:\n" + " ".join(bind_link) + "\n" + r.stdout +
