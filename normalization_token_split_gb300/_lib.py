@@ -1,5 +1,5 @@
 """Loader of the in-tree libnts.so (ctypes) and of the extension that passes
-torch tensors to it (marshal_nts.so).  There is no fallback: if they have not
+torch tensors to it (marshal_nts.*.so, of this interpreter and this torch).  There is no fallback: if they have not
 been built (``normalization_token_split_gb300.build``) every call raises."""
 from __future__ import annotations
 
@@ -8,9 +8,11 @@ import importlib.util
 import os
 import threading
 
+from ._abi import marshal_name
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libnts.so")
-MARSHAL_PATH = os.path.join(_HERE, "_build", "marshal_nts.so")
+MARSHAL_PATH = os.path.join(_HERE, "_build", marshal_name())
 
 _lock = threading.Lock()
 _lib = None
@@ -110,7 +112,8 @@ def marshal():
         if _marshal is None:
             if not os.path.exists(MARSHAL_PATH):
                 raise RuntimeError(
-                    f"marshal_nts.so is not built ({MARSHAL_PATH} missing); run "
+                    "the extension for this Python and this torch is not built "
+                    f"({MARSHAL_PATH} missing); run "
                     "`python -m normalization_token_split_gb300.build`")
             import torch  # noqa: F401  (its libraries come first)
             spec = importlib.util.spec_from_file_location("marshal_nts", MARSHAL_PATH)

@@ -1,5 +1,5 @@
 """Builds libnts.so in-tree (normalization_token_split_gb300/_build/) with
-nvcc for sm_103a, and the Python extension beside it (marshal_nts.so, from
+nvcc for sm_103a, and the Python extension beside it (marshal_nts.*.so, from
 binding/) with g++.  Translation units compile in parallel; a unit is rebuilt
 only when it or a header is newer than its object, and a library is linked anew
 when it is older than one of its objects: what an earlier run compiled and did
@@ -11,13 +11,14 @@ from __future__ import annotations
 
 import argparse
 import glob
-import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+from ._abi import marshal_name, torch_dir
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libnts.so")
 BINDING = os.path.join(PKG, "binding", "marshal.cpp")
-MARSHAL = os.path.join(BUILD, "marshal_nts.so")
+MARSHAL = os.path.join(BUILD, marshal_name())
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -63,7 +64,7 @@ def _compile_cmd(src: str, obj: str, nvcc: str, cuda: str, verbose: bool):
 def _binding_cmds(obj: str, cuda: str):
     """Compile and link commands of the Python extension (torch's headers and
     libraries, this interpreter, libnts.so beside it)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = torch_dir()
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
@@ -99,7 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             jobs.append(_compile_cmd(src, obj, nvcc, cuda, verbose))
 
     # the binding: its object compiles along with the others, and links after libnts.so
-    obj = os.path.join(BUILD, "marshal.cpp.o")
+    obj = MARSHAL[:-len("so")] + "o"
     bind, bind_link, bind_tmp = _binding_cmds(obj, cuda)
     if force or _stale(obj, BINDING, os.path.join(INCLUDE, "nts.h")):
         jobs.append(bind)

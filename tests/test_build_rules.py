@@ -6,6 +6,7 @@ import types
 
 import pytest
 
+from normalization_token_split_gb300 import _abi, _lib
 from normalization_token_split_gb300 import build as nts_build
 
 
@@ -107,3 +108,28 @@ def test_a_failed_link_is_tried_again(tree):
         tree.broken = set()
         assert broken in tree.build()
         assert tree.build() == []
+
+
+def test_the_extension_is_of_one_python_and_one_torch(monkeypatch):
+    import torch
+
+    name = os.path.basename(_lib.MARSHAL_PATH)
+    assert _lib.MARSHAL_PATH == nts_build.MARSHAL and name == _abi.marshal_name()
+    assert _abi.torch_version() == torch.__version__ and torch.__version__ in name
+    monkeypatch.setattr(_abi, "torch_version", lambda: "0.0")
+    assert _abi.marshal_name() != name
+    monkeypatch.undo()
+    monkeypatch.setattr(_abi.sysconfig, "get_config_var", lambda _: "cpython-399")
+    assert _abi.marshal_name() != name
+
+
+def test_another_abi_s_extension_is_neither_kept_nor_loaded(tree, monkeypatch):
+    tree.build()
+    other = str(tree.root / "_build" / "marshal_nts.another.so")
+    monkeypatch.setattr(nts_build, "MARSHAL", other)
+    assert tree.build() == ["link marshal", "marshal.cpp"]
+    assert os.path.exists(other)
+    monkeypatch.setattr(_lib, "_marshal", None)
+    monkeypatch.setattr(_lib, "MARSHAL_PATH", str(tree.root / "_build" / "marshal_nts.third.so"))
+    with pytest.raises(RuntimeError, match="this torch is not built"):
+        _lib.marshal()
