@@ -3,7 +3,9 @@ nvcc for sm_103a, and the Python extension beside it (marshal_nts.*.so, from
 binding/) with g++.  Translation units compile in parallel; a unit is rebuilt
 only when it or a header is newer than its object, and a library is linked anew
 when it is older than one of its objects: what an earlier run compiled and did
-not come to link is linked by the next.
+not come to link is linked by the next.  libnts.so needs neither torch nor
+Python: without their headers it is built alone, with a warning, and the
+operators that need the extension raise.
 
     python -m normalization_token_split_gb300.build [--force] [--verbose]
 """
@@ -61,6 +63,19 @@ def _compile_cmd(src: str, obj: str, nvcc: str, cuda: str, verbose: bool):
     return cmd
 
 
+def _missing_for_binding():
+    """What the extension needs and this machine lacks, or None."""
+    torch = torch_dir()
+    if torch is None:
+        return "torch"
+    for path in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(torch, "include", "ATen", "ATen.h"),
+                 os.path.join(torch, "lib", "libc10_cuda.so")):
+        if not os.path.exists(path):
+            return path
+    return None
+
+
 def _binding_cmds(obj: str, cuda: str):
     """Compile and link commands of the Python extension (torch's headers and
     libraries, this interpreter, libnts.so beside it)."""
@@ -101,9 +116,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     # the binding: its object compiles along with the others, and links after libnts.so
     obj = MARSHAL[:-len("so")] + "o"
-    bind, bind_link, bind_tmp = _binding_cmds(obj, cuda)
-    if force or _stale(obj, BINDING, os.path.join(INCLUDE, "nts.h")):
-        jobs.append(bind)
+    missing = _missing_for_binding()
+    if missing is not None:
+        print(f"the extension is not built ({missing} is missing): the operators around a "
+              "projection will raise", file=sys.stderr)
+    else:
+        bind, bind_link, bind_tmp = _binding_cmds(obj, cuda)
+        if force or _stale(obj, BINDING, os.path.join(INCLUDE, "nts.h")):
+            jobs.append(bind)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -130,7 +150,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("libnts link failed:\n" + " ".join(link) + "\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
-    if force or _stale(MARSHAL, obj):
+    if missing is None and (force or _stale(MARSHAL, obj)):
         r = subprocess.run(bind_link, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("binding link failed:\n" + " ".join(bind_link) + "\n" + r.stdout +

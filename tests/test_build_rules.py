@@ -133,3 +133,18 @@ def test_another_abi_s_extension_is_neither_kept_nor_loaded(tree, monkeypatch):
     monkeypatch.setattr(_lib, "MARSHAL_PATH", str(tree.root / "_build" / "marshal_nts.third.so"))
     with pytest.raises(RuntimeError, match="this torch is not built"):
         _lib.marshal()
+
+
+@pytest.mark.parametrize("lacks", ["torch", "torch's headers", "Python's headers"])
+def test_the_library_is_built_without_what_the_extension_needs(tree, monkeypatch, capsys, lacks):
+    if lacks == "torch":
+        monkeypatch.setattr(nts_build, "torch_dir", lambda: None)
+    elif lacks == "torch's headers":
+        monkeypatch.setattr(nts_build, "torch_dir", lambda: str(tree.root))
+    else:
+        monkeypatch.setattr(nts_build.sysconfig, "get_paths",
+                            lambda: {"include": str(tree.root / "none")})
+    assert tree.build() == ["a.cu", "b.cu", "c.cpp", "link lib"]
+    assert "is missing" in capsys.readouterr().err
+    monkeypatch.undo()
+    assert not (tree.root / "_build" / "marshal_nts.so").exists()
