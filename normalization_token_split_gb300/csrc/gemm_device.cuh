@@ -32,8 +32,10 @@ __device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
 // the waits that follow return at once, so a role may look at it only now and
 // then, as long as what it does meanwhile stays inside its own memory and arrives
 // at no barrier that counts bytes: all arrivals of such a phase may be there
-// while bytes are missing, and one more is a fault.  The clock is read only after
-// many tries: a read takes longer than most waits.
+// while bytes are missing, and one more is a fault.  Every lane tries and reads
+// the clock by itself, so `late` is a lane's own: a loop that holds instructions
+// of the whole warp is left on any_late.  The clock is read only after many
+// tries: a read takes longer than most waits.
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                          uint32_t stop, uint32_t& late, uint32_t done = 0) {
   asm volatile(
@@ -69,6 +71,13 @@ __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, uint64_t
       : "+r"(late)
       : "r"(bar), "r"(parity), "l"(limit_ns), "r"(stop), "r"(done | late)
       : "memory");
+}
+
+// Whether a wait of any lane of the warp expired (a place where its lanes meet
+// again).  Lanes that left a role's loop by their own answers would meet the
+// others' warp-wide instructions at another place.
+__device__ __forceinline__ uint32_t any_late(uint32_t late) {
+  return __any_sync(0xFFFFFFFFu, late != 0) != 0;
 }
 
 // Arrive on `bar` from the lanes with on != 0, without a branch.  CLUSTER: a

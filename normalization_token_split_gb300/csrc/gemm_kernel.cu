@@ -271,9 +271,10 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
             __syncwarp();
           }
+          late = any_late(late);
         }
       }
-      if (lane == 0) *issued = n;
+      if (leader) *issued = n;
     } else if (warp == 1 && rank == 0) {
       // One K block after the other, whatever tile it belongs to: every block
       // begins its sums anew.  S blocks a turn, so that slots, buffers and
@@ -311,6 +312,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             __syncwarp();
           }
         }
+        late = any_late(late);
       }
     } else if (warp > 1) {
       // scale warps: lanes 8 r .. 8 r + 7 copy the eight scales of a row; of W
@@ -336,6 +338,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                                    in, sub, [](int r) { return r; });
           copy_async_arrive(sfull + 8 * pc.i);
           pc.advance();
+          late = any_late(late);
         }
       }
     }
@@ -458,6 +461,7 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           arrive_if<false>(sempty + 8 * piece, lane == 0);
         }
       }
+      late = any_late(late);
       if (late) break;
       const int64_t m0 = (int64_t)tm * C::kTileM + rank * 128 + (warp & 3) * 32;
       const int64_t n0 = (int64_t)tn * BN + COLS * group;
@@ -539,8 +543,8 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
-  if (late && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
-  if (*stop) {
+  if (*stop) {   // some lane's wait expired
+    if (threadIdx.x == 0) atomicOr(&g_gemm_status, kStatusTimeout);
     drain<S, PAIR>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
   }
@@ -655,7 +659,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
           tma_load_2d<false>(at + 2 * C::kW + i * C::kA, &map_a, (2 * u + i) * 128, tm * TN, bar);
         *issued = u + 1 - u0;
       }
-      __syncwarp();
+      late = any_late(late);
     }
   } else if (warp == 1) {
     constexpr uint32_t instr = e4m3_instr(128, TN);
@@ -676,7 +680,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         mma_commit<false>(ready);
         mma_commit<false>(release);
       }
-      __syncwarp();
+      late = any_late(late);
     }
   } else if (warp < 4) {
     const int sub = (warp - 2) * 4 + (lane >> 3), kl = lane & 7;
@@ -691,6 +695,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
       stage_scales<ROWS ? 128 : 1>(dst + 4 * TN, p.sw, (int64_t)tn * (ROWS ? 128 : 1),
                                    ROWS ? p.N : tn + 1, at, p.kblocks, in, sub, place);
       copy_async_arrive(sfull + 8 * pc.i);
+      late = any_late(late);
     }
   } else {
     const int row = (warp & 3) * 32 + lane;   // of W
@@ -707,6 +712,7 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
         sc = scales + pc.i * kChunk * C::kScales;
       }
       bar_wait(tfull + 8 * tb.i, tb.parity, p.wait_limit_ns, stop_at, late);
+      late = any_late(late);
       __syncwarp();
       tcgen05_fence_after();
       const uint32_t at = tmem + tb.i * C::kBufCols + lanes;
@@ -742,8 +748,8 @@ narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
-  if (late && lane == 0) atomicOr(&g_gemm_status, kStatusTimeout);
-  if (*stop) {
+  if (*stop) {   // some lane's wait expired
+    if (threadIdx.x == 0) atomicOr(&g_gemm_status, kStatusTimeout);
     drain<S, false>(full, done, *issued, p.wait_limit_ns);
     __syncthreads();
   }

@@ -214,3 +214,30 @@ def test_projection_run_forward_and_backward(T, hq, hk, d):
     check(dW, dYt.codes, dYt.scales, Xt.codes, Xt.scales, 1)
     assert dW.shape == w.shape
     nts.check_status()
+
+
+@pytest.mark.parametrize("kernel,M,N,K", [(1, 600, 2000, 2192), (2, 2500, 2600, 1168)])
+@pytest.mark.parametrize("rows", [128, 1])
+def test_a_wait_that_expires_ends_every_tile(kernel, M, N, K, rows):
+    """Several tiles for a CTA, or several pieces of scales for a tile: all roles
+    leave their loops, by whole warps, and the next product is right."""
+    a, sa, w, sw = operands(M, N, K, rows, seed=M)
+    try:
+        nts.set_tuning(vpt=kernel)
+        want = nts.gemm_blockscaled(a, sa, w, sw)
+        nts.check_status()
+        check(want, a, sa, w, sw, rows)
+        nts.set_wait_limit_ns(20_000_000)
+        nts.set_missing_tx(16)
+        for _ in range(3):
+            nts.gemm_blockscaled(a, sa, w, sw)
+            with pytest.raises(nts.NtsError, match="TIMEOUT"):
+                nts.check_status()
+        nts.set_missing_tx(0)
+        nts.set_wait_limit_ns(0)
+        assert torch.equal(nts.gemm_blockscaled(a, sa, w, sw), want)
+        nts.check_status()
+    finally:
+        nts.set_missing_tx(0)
+        nts.set_wait_limit_ns(0)
+        nts.set_tuning()
