@@ -255,7 +255,9 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint32_t counts = PAIR ? map_to_rank(bar, 0) : bar;
             bar_wait(empty + 8 * st.i, st.parity ^ 1u, p.wait_limit_ns, stop_at, late);
             // *stop too: the matrix warp frees stages for the rest of a turn after its own
-            // wait gave up, whose full phase still has all its arrivals and misses bytes
+            // wait gave up, whose full phase still has all its arrivals and misses bytes (a
+            // pair's second CTA arrives nowhere: what it copies meanwhile, a turn at most,
+            // takes the first one's byte count below zero, which a barrier has room for)
             late |= (uint32_t)*stop;
             n += late ^ 1u;
             if (leader && !late) {

@@ -66,6 +66,24 @@ def test_every_kernel_on_any_shape(M, N, K, rows, kernel):
         check(y, a, sa, w, sw, rows)
 
 
+@pytest.mark.parametrize("kernel", [2, 3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [128, 1])
+@pytest.mark.parametrize("M,N,K", [(2100, 5120, 1168), (2100, 5001, 2192), (4100, 3000, 1040)])
+def test_tiles_of_many_blocks_one_after_another(M, N, K, rows, dtype, kernel):
+    """A CTA or pair takes several tiles, whose K blocks (10, 18 and 9) end a tile in
+    the middle of a turn of the stages, of the accumulators' ring, or of the pieces
+    of scales."""
+    a, sa, w, sw = operands(M, N, K, rows, seed=M + N + K + 2)
+    try:
+        nts.set_tuning(vpt=kernel)
+        y = nts.gemm_blockscaled(a, sa, w, sw, out_dtype=dtype)
+        nts.check_status()
+    finally:
+        nts.set_tuning()
+    check(y, a, sa, w, sw, rows)
+
+
 def test_whole_numbers_are_exact():
     """Small whole numbers: every sum is exact in fp32."""
     g = torch.Generator(device=DEV).manual_seed(3)
@@ -216,7 +234,8 @@ def test_projection_run_forward_and_backward(T, hq, hk, d):
     nts.check_status()
 
 
-@pytest.mark.parametrize("kernel,M,N,K", [(1, 600, 2000, 2192), (2, 2500, 2600, 1168)])
+@pytest.mark.parametrize("kernel,M,N,K", [(1, 600, 2000, 2192), (2, 2500, 2600, 1168),
+                                          (3, 2100, 5120, 1168), (3, 600, 520, 4112)])
 @pytest.mark.parametrize("rows", [128, 1])
 def test_a_wait_that_expires_ends_every_tile(kernel, M, N, K, rows):
     """Several tiles for a CTA, or several pieces of scales for a tile: all roles
