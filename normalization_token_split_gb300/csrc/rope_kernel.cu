@@ -231,7 +231,8 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
 }
 
 // The table row of token t: false for a padding row (pos < 0) and for a
-// position outside the table, which is reported.
+// position outside the table, which is reported.  Such a row's outputs are set to
+// zero, not computed: neither row 0 of the table nor the gain has to be finite.
 __device__ __forceinline__ bool table_row(const RopeParams& p, unsigned t, int lane,
                                           const float** row) {
   const int64_t pos = __ldg(p.pos + t);
@@ -530,8 +531,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_backward_kernel(const RopeP
       load8(c, row + l.c0, row + l.c1);
       load8(s, row + p.rot / 2 + l.c0, row + p.rot / 2 + l.c1);
     }
-    if (!ok) x0 = x1 = y0 = y1 = make_uint4(0, 0, 0, 0);
-    backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, s, sum);
+    if (ok)   // of the whole warp
+      backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, s, sum);
+    else
+      x0 = x1 = make_uint4(0, 0, 0, 0);
     if (in) {
       __nv_bfloat16* o = tn.out + (int64_t)t * tn.ldout + at;
       st_global_v4_stream(o + l.e0, x0);
@@ -746,14 +749,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(con
     for (int h = lane >> p.lshift; h - (lane >> p.lshift) < it.heads; h += hps) {
       const bool in = l.active && h < it.heads;
       uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, y0 = x0, y1 = x0;
-      if (in && ok) {
+      if (in) {
         const unsigned char* at = stage + h * p.d * 2;
         x0 = lds128(at + l.e0 * 2);
         x1 = lds128(at + l.e1 * 2);
         y0 = lds128(at + half + l.e0 * 2);
         y1 = lds128(at + half + l.e1 * 2);
       }
-      backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, sn, sum);
+      if (ok)
+        backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, sn, sum);
+      else
+        x0 = x1 = make_uint4(0, 0, 0, 0);
       if (in) {
         st_global_v4_stream(o + (int64_t)h * p.d + l.e0, x0);
         st_global_v4_stream(o + (int64_t)h * p.d + l.e1, x1);

@@ -358,3 +358,37 @@ def test_canaries():
     nts.check_status()
     for n, (buf, _) in {**bufs, **grads}.items():
         assert bool((buf[:pad] == 0xA5).all()) and bool((buf[-pad:] == 0xA5).all()), n
+
+
+@pytest.mark.parametrize("ring", [False, True])
+@pytest.mark.parametrize("bad", ["gain", "row 0"])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_padding_rows_are_zeros_whatever_the_gain_and_the_table_hold(value, bad, ring):
+    """Zeros out, and nothing added to the gains' gradients, in rows that no value of
+    theirs decides: by choice, not by products with zero."""
+    T, hq, hk, d, rot = 21, 6, 2, 64, 48
+    c = make(T, hq, hk, d, rot, seed=11, pad=4)
+    c["pos"][:T - 4] = torch.arange(1, T - 3)     # row 0 belongs to no token
+    c["pos"][3] = c["table"].shape[0] + 5         # nor does a row beyond the table
+    wants = [ref.rope_backward(dy, x, g, c["pos"], c["table"], d, EPS, False)
+             for dy, x, g in ((c["dyq"], c["q"], c["gq"]), (c["dyk"], c["k"], c["gk"]))]
+    if bad == "gain":
+        c["gq"][5] = c["gk"][60] = value
+    else:
+        c["table"][0] = value
+    try:
+        if ring:
+            nts.set_tuning(rows=1, stages=2)
+        y = forward(c, d, False, want_rinv=True)
+        dq, dk, dgq, dgk = backward(c, d, False)
+        with pytest.raises(nts.NtsError, match="rotation table"):
+            nts.check_status()
+    finally:
+        nts.set_tuning()
+    empty = [3] + list(range(T - 4, T))
+    for t in (*y, dq, dk):
+        assert not t[empty].any()                 # a NaN counts as something
+    for dx, dg, (wx, wg, bx, bg) in ((dq, dgq, wants[0]), (dk, dgk, wants[1])):
+        assert torch.all((dg.cpu().double() - wg).abs() <= bg)   # no gain is part of it
+        if bad == "row 0":
+            assert torch.all((dx.cpu().double() - wx).abs() <= bx)
