@@ -390,7 +390,7 @@ NTS_API int nts_qknorm_rope(const void *Q_dev, int64_t ldq, const float *gamma_q
  *                   bytes, 4-byte aligned, contents arbitrary before and
  *                   after; calls that overlap in time need one each.
  * Other arguments, limits and errors as nts_qknorm_rope; INVALID_ARG also for
- * a missing or short workspace.
+ * a missing or short workspace, UNSUPPORTED for an eps below 2^-126.
  */
 NTS_API int nts_qknorm_rope_backward(const void *dYq_dev, int64_t lddyq, const void *dYk_dev,
                                      int64_t lddyk, const void *Q_dev, int64_t ldq,

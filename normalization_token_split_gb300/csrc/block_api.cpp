@@ -3,6 +3,7 @@
 // headwise QK-RMSNorm with rotation, and the rotation table on the host.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -162,6 +163,8 @@ int nts_qknorm_rope_backward(const void* dYq_dev, int64_t lddyq, const void* dYk
   if (rc == NTS_OK) rc = check_vec("gamma_q", gamma_q_dev, T, 16);
   if (rc == NTS_OK) rc = check_vec("gamma_k", gamma_k_dev, T, 16);
   if (rc == NTS_OK) rc = check_table(positions_dev, table_dev, T);
+  if (rc == NTS_OK && eps < FLT_MIN)   // rinv^2 of a row of zeros would overflow
+    rc = fail(NTS_ERR_UNSUPPORTED, "eps must be at least 2^-126 for the gradient");
   // the gains' gradients are written for an empty batch too
   if (rc == NTS_OK) rc = check_vec("dgamma_q", dgamma_q_dev, 1, 4);
   if (rc == NTS_OK) rc = check_vec("dgamma_k", dgamma_k_dev, 1, 4);

@@ -77,6 +77,8 @@ def test_rope_backward_refusals(lib):
     assert rope_bwd(lib, wsb=need.value - 1) == INVALID
     assert rope_bwd(lib, ws=None) == INVALID
     assert rope_bwd(lib, ws=MIS2) == UNSUPPORTED
+    assert rope_bwd(lib, eps=2.0 ** -127) == UNSUPPORTED     # rinv^2 beyond fp32
+    assert rope_bwd(lib, eps=2.0 ** -149, T=0) == UNSUPPORTED
     assert lib.nts_qknorm_rope_backward_workspace(0, ctypes.byref(need)) == INVALID
     assert lib.nts_qknorm_rope_backward_workspace(128, None) == INVALID
 

@@ -392,3 +392,25 @@ def test_padding_rows_are_zeros_whatever_the_gain_and_the_table_hold(value, bad,
         assert torch.all((dg.cpu().double() - wg).abs() <= bg)   # no gain is part of it
         if bad == "row 0":
             assert torch.all((dx.cpu().double() - wx).abs() <= bx)
+
+
+def test_gradient_of_zero_rows_at_the_smallest_eps():
+    T, hq, hk, d, rot, eps = 5, 2, 1, 32, 32, 2.0 ** -126
+    c = make(T, hq, hk, d, rot, seed=12)
+    c["q"][1] = 0
+    c["k"][2] = 0
+    c["dyq"] *= 2.0 ** -40                        # rinv is 2^63 there
+    c["dyk"] *= 2.0 ** -40
+    D = {k: to_dev(v) for k, v in c.items()}
+    got = nts.qknorm_rope_backward(D["dyq"], D["dyk"], D["q"], D["gq"], D["k"], D["gk"], D["pos"],
+                                   D["table"], head_dim=d, eps=eps)
+    nts.check_status()
+    for dx, dg, dy, x, g in ((got[0], got[2], c["dyq"], c["q"], c["gq"]),
+                             (got[1], got[3], c["dyk"], c["k"], c["gk"])):
+        wx, wg, bx, bg = ref.rope_backward(dy, x, g, c["pos"], c["table"], d, eps, False)
+        assert wx.abs().max() > 2.0 ** 20 and bool(torch.isfinite(dx).all())
+        assert torch.all((dx.cpu().double() - wx).abs() <= bx)
+        assert torch.all((dg.cpu().double() - wg).abs() <= bg)
+    with pytest.raises(nts.NtsError, match="UNSUPPORTED"):
+        nts.qknorm_rope_backward(D["dyq"], D["dyk"], D["q"], D["gq"], D["k"], D["gk"], D["pos"],
+                                 D["table"], head_dim=d, eps=2.0 ** -130)
