@@ -542,6 +542,7 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
   if (const int injected = take_injected_failure()) return injected;
   const DeviceInfo& dev = device_info();
   if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kCastUnit);
   CastParams p = {};
   p.x = static_cast<const __nv_bfloat16*>(rq.X);
   p.gamma = rq.gamma;

@@ -945,6 +945,7 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   if (const int injected = take_injected_failure()) return injected;
   const DeviceInfo& dev = device_info();
   if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kGemmUnit);
   GemmParams p = {};
   p.sa = rq.a_scales;
   p.sw = rq.w_scales;

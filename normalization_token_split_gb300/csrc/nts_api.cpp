@@ -58,6 +58,12 @@ void log_launch(const char* name, const char* fmt, ...) {
   std::fprintf(stderr, "[nts] %s: %s\n", name, buf);
 }
 
+namespace {
+std::atomic<bool> g_launched[kStatusUnits];
+}
+
+void note_launch(StatusUnit unit) { g_launched[unit].store(true, std::memory_order_relaxed); }
+
 LaunchTuning current_tuning() {
   std::lock_guard<std::mutex> lk(g_tune_mu);
   return g_tune;
@@ -660,17 +666,22 @@ int nts_mxnorm_postround_cast(const void* X_dev, const float* gamma_dev, uint8_t
 int nts_check_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "synchronizing the stream");
-  unsigned qk = 0, mx = 0, cast = 0, gemm = 0, rope = 0;
+  unsigned qk = 0, mx = 0, unit[kStatusUnits] = {};
   int rc = read_and_clear_qk_status(&qk);
   if (rc != NTS_OK) return rc;
   rc = read_and_clear_mx_status(&mx);
   if (rc != NTS_OK) return rc;
-  rc = read_and_clear_cast_status(&cast);
-  if (rc != NTS_OK) return rc;
-  rc = read_and_clear_gemm_status(&gemm);
-  if (rc != NTS_OK) return rc;
-  rc = read_and_clear_rope_status(&rope);
-  if (rc != NTS_OK) return rc;
+  int (*const read[kStatusUnits])(unsigned*) = {
+      read_and_clear_cast_status, read_and_clear_gemm_status, read_and_clear_rope_status};
+  int units = 0;
+  for (int i = 0; i < kStatusUnits; ++i) {
+    if (!g_launched[i].load(std::memory_order_relaxed)) continue;
+    ++units;
+    rc = read[i](&unit[i]);
+    if (rc != NTS_OK) return rc;
+  }
+  log_launch("check_status", "words of %d operators around a projection read", units);
+  const unsigned cast = unit[kCastUnit], gemm = unit[kGemmUnit], rope = unit[kRopeUnit];
   if ((qk | mx | cast | gemm | (rope & kStatusTimeout)) != 0)
     return fail(NTS_ERR_TIMEOUT,
                 "a kernel gave up on a bounded wait (qk=%u mx=%u cast=%u gemm=%u rotation=%u)", qk,

@@ -218,9 +218,14 @@ struct GemmRequest {
 };
 int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
 
+// The operators around a projection whose kernels this process has launched or
+// captured: nts_check_status reads the status words of those alone (a blocking
+// copy of ~13 us each), so the other operators' users do not pay for them.
+enum StatusUnit { kCastUnit, kGemmUnit, kRopeUnit, kStatusUnits };
+void note_launch(StatusUnit unit);
 int read_and_clear_cast_status(unsigned* out);
-int read_and_clear_rope_status(unsigned* out);
 int read_and_clear_gemm_status(unsigned* out);
+int read_and_clear_rope_status(unsigned* out);
 int read_and_clear_qk_status(unsigned* out);
 int read_and_clear_mx_status(unsigned* out);
 

@@ -911,6 +911,7 @@ int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& 
   if (const int injected = take_injected_failure()) return injected;
   const DeviceInfo& dev = device_info();
   if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kRopeUnit);
   RopeParams p = common_params(rq, tune);
   uint64_t items[2];
   int rc = set_items(&p, 1, items);
@@ -943,6 +944,7 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   if (const int injected = take_injected_failure()) return injected;
   const DeviceInfo& dev = device_info();
   if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kRopeUnit);
   RopeParams p = common_params(rq, tune);
   uint64_t items[2];
   int rc = set_items(&p, 1, items);

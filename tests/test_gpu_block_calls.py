@@ -2,6 +2,10 @@
 refuses on CUDA tensors, calls from several threads and streams, memory on
 other streams than the current one, offsets beyond 32 bits, outputs of odd
 widths with a scale per weight row."""
+import os
+import re
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -445,3 +449,38 @@ def test_the_legacy_handle_is_the_default_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(got, want))
     nts.check_status()
+
+
+STATUS_RUN = """
+import torch
+import normalization_token_split_gb300 as nts
+x = torch.ones(4, 256, dtype=torch.bfloat16, device="cuda")
+g, pos = torch.ones(64, device="cuda"), torch.arange(4, device="cuda")
+table = nts.rope_table(4, 64)
+nts.rmsnorm_mxcast(x)
+nts.check_status()                                # 0
+o = nts.blockcast(x)
+nts.check_status()                                # 1
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    nts.qknorm_rope(x, g, x, g, pos, table, 64)
+pos.fill_(9)
+graph.replay()
+try:
+    nts.check_status()                            # 2: a captured launch counts
+except nts.NtsError as e:
+    assert "rotation table" in str(e)
+else:
+    raise SystemExit("the position went unseen")
+nts.gemm_blockscaled(o.codes, o.scales, o.codes, o.scales)
+nts.check_status()                                # 3
+"""
+
+
+def test_check_status_reads_the_words_of_what_ran():
+    """Users of the other operators do not wait for copies of these ones' words."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", STATUS_RUN], cwd=root, capture_output=True, text=True,
+                       env={**os.environ, "NTS_LOG": "1"}, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert re.findall(r"words of (\d+) operators", r.stderr) == ["0", "1", "2", "3"]
