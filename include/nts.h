@@ -59,7 +59,8 @@ typedef enum {
                                 nts_check_status: a position outside the rotation table */
     NTS_ERR_UNSUPPORTED = 2, /* valid request this build cannot run: misaligned
                                 pointer, row too wide, cluster not launchable */
-    NTS_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
+    NTS_ERR_CUDA = 3,        /* a CUDA runtime call, a launch, or the host's own part
+                                of one failed */
     NTS_ERR_TIMEOUT = 4      /* a kernel's bounded wait expired (nts_check_status) */
 } nts_status;
 

@@ -71,8 +71,12 @@ NTS_API int nts_debug_set_host_chunks(int max_chunks, int64_t min_chunk_bytes);
  * NTS_ERR_TIMEOUT -- instead of launching, with nts_last_error() saying the
  * failure was injected; the device is not touched.  count = 0 turns the hook
  * off.  Lets callers' error handling be tested without a failing GPU.
+ * status NTS_DEBUG_THROW: the next `count` calls of the operators around a
+ * projection (nts_qknorm_rope to nts_gemm_blockscaled) meet a C++ exception in
+ * their launch instead, and return NTS_ERR_CUDA.
  * Errors: INVALID_ARG for count < 0 or another status.
  */
+#define NTS_DEBUG_THROW (-1)
 NTS_API int nts_debug_inject_failure(int status, int count);
 
 /*

@@ -6,6 +6,8 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <exception>
+#include <new>
 
 #include "nts.h"
 #include "nts_internal.h"
@@ -87,6 +89,25 @@ int check_cast(const void* X, const uint8_t* codes, const float* scales, int64_t
   return NTS_OK;
 }
 
+// Runs a launch; what it throws (the host out of memory, a lock that fails) ends
+// as a status, not in the caller's C frames.
+template <typename F>
+int guarded(F f) noexcept {
+  try {
+    if (take_injected_throw()) throw std::bad_alloc();
+    return f();
+  } catch (const std::exception& e) {
+    return fail(NTS_ERR_CUDA, "host failure in a launch: %s", e.what());
+  } catch (...) {
+    return fail(NTS_ERR_CUDA, "host failure in a launch");
+  }
+}
+
+int cast(const BlockcastRequest& rq, void* stream) {
+  return guarded(
+      [&] { return launch_blockcast(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,7 +154,8 @@ int nts_qknorm_rope(const void* Q_dev, int64_t ldq, const float* gamma_q_dev, vo
   const RopeRequest rq{{{Q_dev, nullptr, Yq_dev, gamma_q_dev, rinv_q_dev, ldq, 0, ldyq, nheads_q},
                         {K_dev, nullptr, Yk_dev, gamma_k_dev, rinv_k_dev, ldk, 0, ldyk, nheads_k}},
                        positions_dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps};
-  return launch_rope(rq, static_cast<cudaStream_t>(stream), current_tuning());
+  return guarded(
+      [&] { return launch_rope(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
 }
 
 int nts_qknorm_rope_backward_workspace(int64_t head_dim, int64_t* bytes_out) {
@@ -185,8 +207,10 @@ int nts_qknorm_rope_backward(const void* dYq_dev, int64_t lddyq, const void* dYk
   const RopeRequest rq{{{Q_dev, dYq_dev, dQ_dev, gamma_q_dev, nullptr, ldq, lddyq, lddq, nheads_q},
                         {K_dev, dYk_dev, dK_dev, gamma_k_dev, nullptr, ldk, lddyk, lddk, nheads_k}},
                        positions_dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps};
-  return launch_rope_backward(rq, dgamma_q_dev, dgamma_k_dev, static_cast<float*>(workspace_dev),
-                              s, current_tuning());
+  return guarded([&] {
+    return launch_rope_backward(rq, dgamma_q_dev, dgamma_k_dev, static_cast<float*>(workspace_dev),
+                                s, current_tuning());
+  });
 }
 
 int nts_rmsnorm_blockcast(const void* X_dev, const float* gamma_dev, uint8_t* codes_dev,
@@ -200,7 +224,7 @@ int nts_rmsnorm_blockcast(const void* X_dev, const float* gamma_dev, uint8_t* co
     return fail(NTS_ERR_UNSUPPORTED, "gamma must be 16-byte aligned, rinv 4-byte");
   if (T == 0) return NTS_OK;
   const BlockcastRequest rq{kCastNorm, X_dev, gamma_dev, codes_dev, scales_dev, rinv_dev, T, D, eps};
-  return launch_blockcast(rq, static_cast<cudaStream_t>(stream), current_tuning());
+  return cast(rq, stream);
 }
 
 int nts_blockcast(const void* X_dev, uint8_t* codes_dev, float* scales_dev, int64_t T, int64_t D,
@@ -212,7 +236,7 @@ int nts_blockcast(const void* X_dev, uint8_t* codes_dev, float* scales_dev, int6
   if (T == 0) return NTS_OK;
   const BlockcastRequest rq{block_rows == 1 ? kCastPlain : kCastTiles, X_dev, nullptr, codes_dev,
                             scales_dev, nullptr, T, D, 0.f};
-  return launch_blockcast(rq, static_cast<cudaStream_t>(stream), current_tuning());
+  return cast(rq, stream);
 }
 
 int nts_blockcast_t(const void* X_dev, uint8_t* codes_dev, float* scales_dev, int64_t T, int64_t D,
@@ -222,7 +246,7 @@ int nts_blockcast_t(const void* X_dev, uint8_t* codes_dev, float* scales_dev, in
   if (T == 0) return NTS_OK;
   const BlockcastRequest rq{kCastTranspose, X_dev, nullptr, codes_dev, scales_dev, nullptr, T, D,
                             0.f};
-  return launch_blockcast(rq, static_cast<cudaStream_t>(stream), current_tuning());
+  return cast(rq, stream);
 }
 
 int nts_gemm_blockscaled(const uint8_t* A_codes_dev, const float* a_scales_dev,
@@ -250,7 +274,8 @@ int nts_gemm_blockscaled(const uint8_t* A_codes_dev, const float* a_scales_dev,
   if (M == 0) return NTS_OK;
   const GemmRequest rq{A_codes_dev, a_scales_dev, W_codes_dev, w_scales_dev, w_block_rows, Y_dev,
                        out_type == NTS_OUT_FP32, M, N, K};
-  return launch_gemm(rq, static_cast<cudaStream_t>(stream), current_tuning());
+  return guarded(
+      [&] { return launch_gemm(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
 }
 
 }  // extern "C"

@@ -71,6 +71,14 @@ LaunchTuning current_tuning() {
 
 std::atomic<int> g_inject_left{0};
 std::atomic<int> g_inject_status{NTS_OK};
+std::atomic<int> g_throw_left{0};
+
+bool take_injected_throw() {
+  int left = g_throw_left.load();
+  while (left > 0 && !g_throw_left.compare_exchange_weak(left, left - 1)) {
+  }
+  return left > 0;
+}
 
 int take_injected_failure() {
   int left = g_inject_left.load();
@@ -880,8 +888,11 @@ int nts_debug_set_host_chunks(int max_chunks, int64_t min_chunk_bytes) {
 int nts_debug_inject_failure(int status, int count) {
   if (count < 0) return fail(NTS_ERR_INVALID_ARG, "count must be >= 0");
   if (count > 0 && status != NTS_ERR_CUDA && status != NTS_ERR_UNSUPPORTED &&
-      status != NTS_ERR_TIMEOUT)
-    return fail(NTS_ERR_INVALID_ARG, "status must be NTS_ERR_CUDA, _UNSUPPORTED or _TIMEOUT");
+      status != NTS_ERR_TIMEOUT && status != NTS_DEBUG_THROW)
+    return fail(NTS_ERR_INVALID_ARG,
+                "status must be NTS_ERR_CUDA, _UNSUPPORTED, _TIMEOUT or NTS_DEBUG_THROW");
+  g_throw_left = status == NTS_DEBUG_THROW ? count : 0;
+  if (status == NTS_DEBUG_THROW) return NTS_OK;
   g_inject_status = status;
   g_inject_left = count;
   return NTS_OK;

@@ -67,6 +67,8 @@ LaunchTuning current_tuning();
 // launch returns the injected status (with last-error text saying so)
 // instead of touching the device; otherwise NTS_OK.
 int take_injected_failure();
+// Whether this call is to meet a C++ exception (nts_debug_inject_failure).
+bool take_injected_throw();
 
 // The zeroed counter pair of `stream` for a dynamically scheduled launch
 // (sched.cu), or nullptr: schedule round-robin.

@@ -149,3 +149,20 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         nts.qknorm_rope(x, g, x, g, torch.zeros(4, dtype=torch.int64), torch.zeros(8, 128),
                         head_dim=128)
+
+
+def test_a_cpp_exception_ends_as_a_status(lib):
+    """Nothing is thrown through the C entries, whose callers cannot catch it."""
+    calls = [lambda: rope(lib), lambda: rope_bwd(lib),
+             lambda: lib.nts_rmsnorm_blockcast(A, None, A, A, None, 3, 256, 1e-6, None),
+             lambda: lib.nts_blockcast(A, A, A, 3, 256, 1, None),
+             lambda: lib.nts_blockcast(A, A, A, 3, 256, 128, None),
+             lambda: lib.nts_blockcast_t(A, A, A, 3, 256, None),
+             lambda: lib.nts_gemm_blockscaled(A, A, A, A, 128, A, 0, 4, 256, 256, None)]
+    try:
+        for call in calls:
+            assert lib.nts_debug_inject_failure(-1, 1) == OK
+            assert call() == 3                    # CUDA
+            assert b"host failure in a launch" in lib.nts_last_error()
+    finally:
+        assert lib.nts_debug_inject_failure(0, 0) == OK
