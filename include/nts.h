@@ -362,7 +362,9 @@ NTS_API int nts_rope_table_host(int64_t P, int64_t rot_dim, double base, float *
  * Errors: INVALID_ARG (null required pointer, bad sizes, eps, odd rot_dim or
  *         one beyond head_dim, a stride below the row), UNSUPPORTED (other
  *         head_dim or rot_dim, unaligned rows, T >= 2^31, more than 65536
- *         heads), CUDA.
+ *         heads, T times the warp items of a token from 2^31: a warp takes
+ *         32 / l heads of Q or of K, l the power of two from head_dim / 16
+ *         up), CUDA.
  */
 NTS_API int nts_qknorm_rope(const void *Q_dev, int64_t ldq, const float *gamma_q_dev,
                             void *Yq_dev, int64_t ldyq, float *rinv_q_dev, const void *K_dev,
@@ -437,7 +439,9 @@ NTS_API int nts_rmsnorm_blockcast(const void *X_dev, const float *gamma_dev, uin
  *   codes_dev   uint8 [T, D].
  *   scales_dev  fp32 [ceil(T / block_rows), ceil(D / 128)].
  *   D a multiple of 16; block_rows 1 or 128.
- * Errors: as nts_rmsnorm_blockcast; INVALID_ARG also for another block_rows.
+ * Errors: as nts_rmsnorm_blockcast, but D and T only have to stay below 2^31;
+ * INVALID_ARG also for another block_rows, UNSUPPORTED also for 2^31 blocks of
+ * 128 x 128 or more.
  */
 NTS_API int nts_blockcast(const void *X_dev, uint8_t *codes_dev, float *scales_dev, int64_t T,
                           int64_t D, int block_rows, void *stream);
@@ -449,8 +453,9 @@ NTS_API int nts_blockcast(const void *X_dev, uint8_t *codes_dev, float *scales_d
  *   codes_dev   uint8 [D, Tp], Tp = T rounded up to a multiple of 16; the
  *               codes of the Tp - T tokens beyond T are zero.
  *   scales_dev  fp32 [D, ceil(T / 128)].
- *   D a multiple of 16.
- * Errors: as nts_rmsnorm_blockcast.
+ *   D a multiple of 16; T at most 65535 * 128 = 8388480.
+ * Errors: as nts_rmsnorm_blockcast, but D only has to stay below 2^31;
+ * UNSUPPORTED also for more tokens.
  */
 NTS_API int nts_blockcast_t(const void *X_dev, uint8_t *codes_dev, float *scales_dev, int64_t T,
                             int64_t D, void *stream);

@@ -540,9 +540,6 @@ int launch(CastKernel kern, dim3 grid, const CastParams& p, cudaStream_t stream,
 
 int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const LaunchTuning& tune) {
   if (const int injected = take_injected_failure()) return injected;
-  const DeviceInfo& dev = device_info();
-  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
-  note_launch(kCastUnit);
   CastParams p = {};
   p.x = static_cast<const __nv_bfloat16*>(rq.X);
   p.gamma = rq.gamma;
@@ -556,16 +553,20 @@ int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const Laun
   p.eps = rq.eps;
   p.inv_d = 1.0f / (float)p.D;
   const int64_t tblocks = (p.T + 127) / 128;
+  if (rq.kind == kCastTiles && tblocks > 0x7fffffffll / p.blocks)
+    return fail(NTS_ERR_UNSUPPORTED, "too many 128 x 128 blocks in one call");
+  if (rq.kind == kCastTranspose && tblocks > 65535)
+    return fail(NTS_ERR_UNSUPPORTED, "more than 65535 blocks of tokens");
+  const DeviceInfo& dev = device_info();
+  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kCastUnit);
 
   if (rq.kind == kCastTiles) {
-    if (tblocks > 0x7fffffffll / p.blocks)
-      return fail(NTS_ERR_UNSUPPORTED, "too many 128 x 128 blocks in one call");
     log_launch("blockcast", "T=%lld D=%d 128x128", (long long)p.T, p.D);
     return launch(blockcast_tiles_kernel, dim3((unsigned)(tblocks * p.blocks)), p, stream,
                   tune.pdl != 0);
   }
   if (rq.kind == kCastTranspose) {
-    if (tblocks > 65535) return fail(NTS_ERR_UNSUPPORTED, "more than 65535 blocks of tokens");
     p.pitch = (p.T + 15) / 16 * 16;
     p.tblocks = (int)tblocks;
     log_launch("blockcast_t", "T=%lld D=%d", (long long)p.T, p.D);

@@ -909,13 +909,13 @@ int launch(void (*kern)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t 
 
 int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& tune) {
   if (const int injected = take_injected_failure()) return injected;
-  const DeviceInfo& dev = device_info();
-  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
-  note_launch(kRopeUnit);
   RopeParams p = common_params(rq, tune);
   uint64_t items[2];
   int rc = set_items(&p, 1, items);
   if (rc != NTS_OK) return rc;
+  const DeviceInfo& dev = device_info();
+  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kRopeUnit);
   const bool ring = tune.force_rows > 0 || items[0] + items[1] > (uint64_t)dev.sm_count * kDirectItems;
   size_t smem = 0;
   unsigned grid = (unsigned)((items[0] + items[1] + kRopeWarps - 1) / kRopeWarps);
@@ -942,13 +942,13 @@ int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& 
 int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k,
                          float* workspace, cudaStream_t stream, const LaunchTuning& tune) {
   if (const int injected = take_injected_failure()) return injected;
-  const DeviceInfo& dev = device_info();
-  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
-  note_launch(kRopeUnit);
   RopeParams p = common_params(rq, tune);
   uint64_t items[2];
   int rc = set_items(&p, 1, items);
   if (rc != NTS_OK) return rc;
+  const DeviceInfo& dev = device_info();
+  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  note_launch(kRopeUnit);
   const bool ring = tune.force_rows > 0 ||
                     items[0] + items[1] > (uint64_t)dev.sm_count * kBackwardDirectItems;
   size_t smem = (size_t)kRopeWarps * std::max(p.d, 128) * sizeof(float);

@@ -53,6 +53,11 @@ def test_rope_refusals(lib, fn):
     assert fn(lib, ldk=260) == UNSUPPORTED      # rows off 16-byte boundaries
     assert fn(lib, hq=65537, ldq=65537 * 128) == UNSUPPORTED
     assert fn(lib, T=1 << 31) == UNSUPPORTED
+    # 4 + 2 heads of 128 are one item each, of 512 are four and two: 2^31 - 1 items at most
+    assert fn(lib, T=1 << 30) == UNSUPPORTED
+    assert fn(lib, T=(1 << 31) // 6 + 1, d=512, ldq=2048, ldk=1024, **(
+        dict(ldyq=2048, ldyk=1024) if fn is rope else
+        dict(lddyq=2048, lddyk=1024, lddq=2048, lddk=1024))) == UNSUPPORTED
     for eps in (0.0, -1.0, math.nan, math.inf):
         assert fn(lib, eps=eps) == INVALID
     assert len(lib.nts_last_error()) > 0
@@ -116,6 +121,8 @@ def test_cast_refusals(lib):
     assert norm(eps=0.0) == INVALID and norm(D=32784) == UNSUPPORTED
     assert norm(g=MIS) == UNSUPPORTED and norm(r=MIS2) == UNSUPPORTED
     assert plain(rows=64) == INVALID and plain(rows=64, T=0) == INVALID
+    assert trans(T=65535 * 128 + 1) == UNSUPPORTED       # blocks of tokens
+    assert plain(T=1 << 30, D=256 * 128, rows=128) == UNSUPPORTED   # 2^31 blocks
 
 
 def test_gemm_refusals(lib):
