@@ -426,7 +426,7 @@ NTS_API int nts_qknorm_rope_backward_workspace(int64_t head_dim, int64_t *bytes_
  *   rinv_dev    fp32 [T] or NULL.
  *   T >= 0; D a multiple of 16 up to 32768; eps > 0 and finite.
  * Errors: INVALID_ARG (null X/codes/scales, T < 0, D <= 0, bad eps),
- *         UNSUPPORTED (D % 16, D too wide, unaligned pointer), CUDA.
+ *         UNSUPPORTED (D % 16, D too wide, T >= 2^31, unaligned pointer), CUDA.
  */
 NTS_API int nts_rmsnorm_blockcast(const void *X_dev, const float *gamma_dev, uint8_t *codes_dev,
                                   float *scales_dev, float *rinv_dev, int64_t T, int64_t D,

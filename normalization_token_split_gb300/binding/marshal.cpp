@@ -4,8 +4,8 @@
 // of the computation runs here.
 //
 // These calls serve single tokens, where the host's share of a call is the
-// larger one: in Python, checking and passing the fifteen arguments of a
-// rotation took 13 of a call's 17 us, against 4 in the library with the launch.
+// larger one: marshalled in Python, a rotation of one token that makes its
+// outputs took 26 us of host time, so it takes 5.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>

@@ -11,10 +11,11 @@
 // RMSNorm: rinv = 1 / sqrt((1/D) sum x^2 + eps), w = fp32(fp32(x gamma) rinv).
 //
 // All of these are bound by HBM, 2 bytes read and 1 + 4/128 written per value,
-// as far as their instructions allow.  Measured (us, back to back in a graph; of the copy's rate): with the
-// norm [16384, 4096] 37.5, 0.80, issue slots 65 % busy with 16 warps an SM;
-// [64, 4096] 2.4; without, [16384, 4096] 33.2, 0.91; weights [10240, 5120] 24.8,
-// 0.94; the transpose of [4099, 5120] 12.3, 0.77.
+// as far as their instructions allow.  Measured (us, back to back in a graph,
+// inputs and outputs rotated over more than L2; of the copy's rate): with the norm
+// [16384, 4096] 38.1, 0.79, issue slots 65 % busy with 16 warps an SM; [64, 4096]
+// 2.4; without, [16384, 4096] 35.3, 0.85; weights [10240, 5120] 24.8, 0.94; the
+// transpose of [4099, 5120] 13.2, 0.71.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -196,12 +197,12 @@ __global__ void __launch_bounds__(kCastThreads) blockcast_rows_kernel(const Cast
 // named barrier, and the part is read a second time from shared memory, not kept
 // in registers.  The barrier is what parts cost, so they are as large as the
 // gain's registers allow: 160 units (5 KB; [16384, 4096] by four warps a row in
-// place of two 50.3 us, 37.5 so); without the norm 128.  A thread reads the two
+// place of two 51.1 us, 38.1 so); without the norm 128.  A thread reads the two
 // vectors of its unit in the order that lets the 8 lanes of each shared-memory
 // phase hit distinct banks.  GAIN: a thread meets the same units of the gain on
 // every row and keeps the first four in registers (all from L1, where a warp's
-// 64-byte steps take 16 passes a load: [16384, 4096] 45.2 us); a fifth is read
-// from L1 ([8192, 5120] 26.8 us, 32.7 by four warps a row).
+// 64-byte steps take 16 passes a load: [16384, 4096] 45.3 us); a fifth is read
+// from L1 ([8192, 5120] 26.8 us, 33.7 by four warps a row).
 constexpr int kStages = 2;
 constexpr int kPartUnits = 160, kHeldUnits = 128;
 

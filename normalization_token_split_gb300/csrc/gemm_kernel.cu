@@ -28,14 +28,16 @@
 //    CTAs of a cluster, which add their sums in rank order through
 //    distributed shared memory.
 //
-// Measured (us in a graph): [8192, 5120] x [15360, 5120] 498, 2.6 PFLOP/s; the
-// tensor pipe is 56 % busy, as the sums of a K block of 256 x 256 x 128 are read
-// back and scaled in ~900 cycles, and its matrix instructions take 512 (without
-// the scaling fmas 415, without the matrix instructions 423, with half of the
-// operand bytes 489).  [4096, 4112] x [4096, 4112] with scales per row, fp32:
-// 105, one more multiply per sum.  [333, 5120] x [5120, 5120] 15.5, 510 cycles
-// per K block of 128 x 128 and 4 us to start and end.  One row by [12288, 4096]
-// 11.7: W at 0.97 of the copy's rate, and the same 4 us.
+// Measured (us in a graph): [8192, 5120] x [15360, 5120] 494 at 2070 MHz, 2.6
+// PFLOP/s; kept up for seconds, in a graph or by calls, 530 to 540, 2.4 PFLOP/s,
+// as the power limit takes the clock to 1910 to 1940 MHz.  The tensor pipe is 57 %
+// busy, as the sums of a K block of 256 x 256 x 128 are read back and scaled in
+// ~900 cycles, and its matrix instructions take 512 (without the scaling fmas 415,
+// without the matrix instructions 423, with half of the operand bytes 489).
+// [4096, 4112] x [4096, 4112] with scales per row, fp32: 107, one more multiply per
+// sum.  [333, 5120] x [5120, 5120] 15.8, 510 cycles per K block of 128 x 128 and 4
+// us to start and end.  One row by [12288, 4096] 11.7: W at 0.97 of the copy's
+// rate, and the same 4 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -452,8 +454,6 @@ wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
               a[i] = fmaf(__uint_as_float(x[i]),
                           r4[2 * (j & 1) + (i >> 1 & 1)] * w[(i >> 2) * 2 + (i & 1)], a[i]);
           } else {
-            // one fma per value: in pairs (f32x2) the loaded registers are no operands
-            // without two moves for each pair, 121 instructions for 64 values
 #pragma unroll
             for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(x[i]), s, a[i]);
           }
@@ -566,7 +566,7 @@ constexpr int kNarrowThreads = 256;   // TMA, MMA, 2 scale warps, 4 epilogue war
 // A stage holds two K blocks: a role's waits and arrivals cost several hundred
 // cycles whatever a stage holds, more than the copies and instructions of one
 // block.  Two CTAs share an SM: its 512 columns of tensor memory, and shared
-// memory for three stages each (TN = 16) or two.
+// memory for three stages each (TN = 16 with a scale per 128 rows of W) or two.
 template <int TN, bool ROWS>
 struct Narrow {
   static constexpr int kPer = 2;                          // K blocks per stage
@@ -960,20 +960,26 @@ int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& 
   int kind = tune.force_vpt <= kPair ? tune.force_vpt : kAuto;   // debug: one of these
   if (kind == kAuto) {
     // Few tiles of 128 x 128: their K loops leave SMs idle, and narrow_kernel
-    // splits K (us, narrow / one CTA: [200, 4096] x [1024, 4096] 8.2 / 12.2,
-    // [100, 4096] x [4096, 4096] 10.1 / 12.6; [128, 5120] x [5120, 5120], 40
-    // tiles, 15.1 both; [128, 5120] x [15360, 5120] 26.6 / 17.4).  Up to 64 rows
-    // of A it reads W with less waste and holds out longer ([64, 5120] x [5120,
-    // 5120] 10.9 / 14.5, [64, 5120] x [15360, 5120] 17.9 / 16.9), up to 32 always.
+    // splits K (us, narrow / one CTA, bf16 with 128-row scales, then fp32 with a
+    // scale per row of W: [200, 4096] x [1024, 4096] 7.8 / 12.1, 8.1 / 16.1; [100,
+    // 4096] x [4096, 4096] 9.7 / 12.5, 10.3 / 16.3; [128, 5120] x [5120, 5120], 40
+    // tiles, 14.8 / 15.1, 17.1 / 20.2; [128, 5120] x [15360, 5120] 27.2 / 18.7,
+    // 31.0 / 22.0).  Up to 64 rows of A it reads W with less waste and holds out
+    // longer ([64, 5120] x [5120, 5120] 10.7 / 14.5, 11.9 / 19.2; [64, 5120] x
+    // [15360, 5120] 18.8 / 17.8, 20.2 / 21.2), up to 32 always ([32, 5120] x [15360,
+    // 5120] 17.1 / 17.4, 17.6 / 20.6).
     const int64_t ones = (p.M + 127) / 128 * ((p.N + 127) / 128);
     const int64_t pairs = (p.M + 255) / 256 * ((p.N + 255) / 256);
     const int64_t sms = dev.sm_count;
     if (p.M <= 32 || 4 * ones <= sms || (p.M <= 64 && 2 * ones <= sms)) {
       kind = kNarrow;
     } else {
-      // A K block takes a pair ~1.5 times as long as one CTA: by the rounds of
-      // tiles ([333, 5120] x [5120, 5120] one CTA 15.6, pair 22.5; [512, 5120]
-      // 27.8 and 22.8, as 160 tiles take two rounds).
+      // A K block takes a pair ~1.5 times as long as one CTA, with either layout of
+      // W's scales: by the rounds of tiles (us, one CTA / pair, bf16 with 128-row
+      // scales, then fp32 with a scale per row, by [5120, 5120]: [333, 5120], one
+      // round of each, 15.4 / 22.3, 20.6 / 32.8; [512, 5120], two and one, 27.6 /
+      // 22.5, 38.1 / 32.7; [1024, 5120], three and two, 39.8 / 41.1, 55.7 / 61.9;
+      // [2048, 5120], five and three, 64.4 / 60.1, 90.9 / 90.4).
       const int64_t rounds = (ones + sms - 1) / sms, rounds2 = (pairs + sms / 2 - 1) / (sms / 2);
       kind = 2 * rounds <= 3 * rounds2 ? kWide : kPair;
     }

@@ -24,8 +24,8 @@
 // Measured (us, back to back in a graph; of the copy's rate): forward [8192, 40
 // + 40 heads of 128] 53.4, 0.94; [1237, 20 + 4 heads of 96, 64 turned] 5.8; one
 // token of 32 + 32 heads 1.9 (an empty launch 1.0 to 1.5).  Backward [8192, 40 +
-// 40] 89.6, 0.84: two values in for each out, and 127 registers leave 16 warps
-// an SM to cover the ring's latencies; [333, 32 + 8 heads of 64] 5.5.
+// 40] 90.2, 0.83: two values in for each out, and 127 registers leave 16 warps
+// an SM to cover the ring's latencies; [333, 32 + 8 heads of 64] 5.6.
 #include <cuda_runtime.h>
 
 #include <algorithm>
