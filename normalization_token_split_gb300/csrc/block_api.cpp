@@ -9,8 +9,8 @@
 #include <exception>
 #include <new>
 
+#include "block_internal.h"
 #include "nts.h"
-#include "nts_internal.h"
 
 using namespace nts;
 

@@ -20,8 +20,8 @@
 
 #include <algorithm>
 
+#include "block_internal.h"
 #include "nts_device.cuh"
-#include "nts_internal.h"
 
 namespace nts {
 

@@ -42,8 +42,8 @@
 
 #include <algorithm>
 
+#include "block_internal.h"
 #include "gemm_device.cuh"
-#include "nts_internal.h"
 
 namespace nts {
 

@@ -15,9 +15,9 @@
 #include <tuple>
 #include <vector>
 
+#include "block_internal.h"
 #include "nts.h"
 #include "nts_debug.h"
-#include "nts_internal.h"
 
 namespace nts {
 
@@ -690,7 +690,7 @@ int nts_check_status(void* stream) {
   }
   log_launch("check_status", "words of %d operators around a projection read", units);
   const unsigned cast = unit[kCastUnit], gemm = unit[kGemmUnit], rope = unit[kRopeUnit];
-  if ((qk | mx | cast | gemm | (rope & kStatusTimeout)) != 0)
+  if ((qk | mx | cast | gemm | (rope & ~kStatusPosition)) != 0)
     return fail(NTS_ERR_TIMEOUT,
                 "a kernel gave up on a bounded wait (qk=%u mx=%u cast=%u gemm=%u rotation=%u)", qk,
                 mx, cast, gemm, rope);

@@ -8,6 +8,9 @@
 
 namespace nts {
 
+// Status bits a kernel ORs into its device status word.
+constexpr unsigned kStatusTimeout = 1u;
+
 __host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 

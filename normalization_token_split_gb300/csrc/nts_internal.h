@@ -11,10 +11,6 @@
 
 namespace nts {
 
-// Status bits a kernel ORs into its device status word.
-constexpr unsigned kStatusTimeout = 1u;
-constexpr unsigned kStatusPosition = 2u;   // a token position outside the rotation table
-
 // A CTA has up to 480 consumer threads (the threads that own data) plus one
 // producer warp that only issues the TMA copies.  512 threads leave up to
 // 128 registers per thread.
@@ -67,8 +63,6 @@ LaunchTuning current_tuning();
 // launch returns the injected status (with last-error text saying so)
 // instead of touching the device; otherwise NTS_OK.
 int take_injected_failure();
-// Whether this call is to meet a C++ exception (nts_debug_inject_failure).
-bool take_injected_throw();
 
 // The zeroed counter pair of `stream` for a dynamically scheduled launch
 // (sched.cu), or nullptr: schedule round-robin.
@@ -95,8 +89,6 @@ RowShape choose_row_shape(int nvec, int force_vpt);
 int prepare_kernel(const void* kernel, size_t smem);
 // Registers per thread of a kernel (cached per device).
 int kernel_registers(const void* kernel, int* regs);
-// CTAs of this kernel that fit an SM (cached per device).
-int blocks_per_sm(const void* kernel, int threads, size_t smem, int* out);
 // Co-resident clusters of `cluster` CTAs for this launch configuration.
 int max_active_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster,
                         int64_t* out);
@@ -168,66 +160,6 @@ int mxnorm_cast_host_one_stream(const void* X_host, const float* gamma_dev, uint
                                 uint8_t* scales_dev, int64_t T, int64_t D, float eps, int B,
                                 int fmt, int p, void* stream);
 
-// Headwise QK-RMSNorm of Q (ten[0]) and K (ten[1]) with the rotary position
-// embedding, and its gradient (rope_kernel.cu).
-struct RopeOperand {
-  const void* x;
-  const void* dy;      // backward
-  void* out;           // y, or dx
-  const float* gamma;
-  float* rinv;         // forward, nullable
-  int64_t ldx, lddy, ldout;
-  int64_t nheads;
-};
-struct RopeRequest {
-  RopeOperand ten[2];
-  const int64_t* pos;
-  const float* table;
-  int64_t P, T, head_dim, rot_dim;
-  int interleaved;
-  float eps;
-};
-// Most CTAs (rows of partial sums in the workspace) of a gradient launch.
-constexpr int kRopePartials = 1024;
-int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
-int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k,
-                         float* workspace, cudaStream_t stream, const LaunchTuning& tune);
-
-// Casts to E4M3 codes with an fp32 scale per 128 values (blockcast_kernel.cu).
-enum CastKind { kCastNorm, kCastPlain, kCastTiles, kCastTranspose };
-struct BlockcastRequest {
-  CastKind kind;
-  const void* X;
-  const float* gamma;  // kCastNorm, nullable
-  uint8_t* codes;
-  float* scales;
-  float* rinv;         // kCastNorm, nullable
-  int64_t T, D;
-  float eps;
-};
-int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
-
-// Block-scaled product of E4M3 operands (gemm_kernel.cu).
-struct GemmRequest {
-  const void* A;
-  const float* a_scales;
-  const void* W;
-  const float* w_scales;
-  int w_rows;          // 128 or 1: rows of W per scale
-  void* Y;
-  int fp32_out;
-  int64_t M, N, K;
-};
-int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
-
-// The operators around a projection whose kernels this process has launched or
-// captured: nts_check_status reads the status words of those alone (a blocking
-// copy of ~13 us each), so the other operators' users do not pay for them.
-enum StatusUnit { kCastUnit, kGemmUnit, kRopeUnit, kStatusUnits };
-void note_launch(StatusUnit unit);
-int read_and_clear_cast_status(unsigned* out);
-int read_and_clear_gemm_status(unsigned* out);
-int read_and_clear_rope_status(unsigned* out);
 int read_and_clear_qk_status(unsigned* out);
 int read_and_clear_mx_status(unsigned* out);
 

@@ -73,3 +73,14 @@ def test_reference_arm_prints_one_json_line():
 
 def test_reference_arm_other_ranks_print_nothing():
     assert _run_reference({"RANK": "1", "WORLD_SIZE": "2", "LOCAL_RANK": "1"}) == ""
+
+
+def test_the_committed_traffic_belongs_to_the_current_kernels():
+    """An edit of the step's kernels, or of a header that they share, needs new
+    captures: the bench line would lose its traffic."""
+    sys.path.insert(0, ROOT)
+    import bench
+    traffic, least = bench.kernel_traffic(), bench.step_bytes()
+    assert set(traffic) == set(bench.KERNELS)
+    # reads and writes of one launch, less what is still dirty in L2 at its end
+    assert all(0.7 * least[k] < v < 1.1 * least[k] for k, v in traffic.items())
