@@ -53,11 +53,6 @@ def test_rope_refusals(lib, fn):
     assert fn(lib, ldk=260) == UNSUPPORTED      # rows off 16-byte boundaries
     assert fn(lib, hq=65537, ldq=65537 * 128) == UNSUPPORTED
     assert fn(lib, T=1 << 31) == UNSUPPORTED
-    # 4 + 2 heads of 128 are one item each, of 512 are four and two: 2^31 - 1 items at most
-    assert fn(lib, T=1 << 30) == UNSUPPORTED
-    assert fn(lib, T=(1 << 31) // 6 + 1, d=512, ldq=2048, ldk=1024, **(
-        dict(ldyq=2048, ldyk=1024) if fn is rope else
-        dict(lddyq=2048, lddyk=1024, lddq=2048, lddk=1024))) == UNSUPPORTED
     for eps in (0.0, -1.0, math.nan, math.inf):
         assert fn(lib, eps=eps) == INVALID
     assert len(lib.nts_last_error()) > 0
@@ -82,8 +77,6 @@ def test_rope_backward_refusals(lib):
     assert rope_bwd(lib, wsb=need.value - 1) == INVALID
     assert rope_bwd(lib, ws=None) == INVALID
     assert rope_bwd(lib, ws=MIS2) == UNSUPPORTED
-    assert rope_bwd(lib, eps=2.0 ** -127) == UNSUPPORTED     # rinv^2 beyond fp32
-    assert rope_bwd(lib, eps=2.0 ** -149, T=0) == UNSUPPORTED
     assert lib.nts_qknorm_rope_backward_workspace(0, ctypes.byref(need)) == INVALID
     assert lib.nts_qknorm_rope_backward_workspace(128, None) == INVALID
 
@@ -121,8 +114,6 @@ def test_cast_refusals(lib):
     assert norm(eps=0.0) == INVALID and norm(D=32784) == UNSUPPORTED
     assert norm(g=MIS) == UNSUPPORTED and norm(r=MIS2) == UNSUPPORTED
     assert plain(rows=64) == INVALID and plain(rows=64, T=0) == INVALID
-    assert trans(T=65535 * 128 + 1) == UNSUPPORTED       # blocks of tokens
-    assert plain(T=1 << 30, D=256 * 128, rows=128) == UNSUPPORTED   # 2^31 blocks
 
 
 def test_gemm_refusals(lib):
@@ -173,3 +164,22 @@ def test_a_cpp_exception_ends_as_a_status(lib):
             assert b"host failure in a launch" in lib.nts_last_error()
     finally:
         assert lib.nts_debug_inject_failure(0, 0) == OK
+
+
+@pytest.mark.parametrize("fn", [rope, rope_bwd])
+def test_rope_refuses_more_items_than_32_bits_count(lib, fn):
+    """4 + 2 heads of 128 are two items a token, of 512 six: 2^31 - 1 items at most."""
+    assert fn(lib, T=1 << 30) == UNSUPPORTED
+    assert fn(lib, T=(1 << 31) // 6 + 1, d=512, ldq=2048, ldk=1024, **(
+        dict(ldyq=2048, ldyk=1024) if fn is rope else
+        dict(lddyq=2048, lddyk=1024, lddq=2048, lddk=1024))) == UNSUPPORTED
+
+
+def test_rope_backward_refuses_an_eps_whose_rinv_squared_overflows(lib):
+    assert rope_bwd(lib, eps=2.0 ** -127) == UNSUPPORTED
+    assert rope_bwd(lib, eps=2.0 ** -149, T=0) == UNSUPPORTED
+
+
+def test_cast_refuses_more_blocks_than_a_launch_holds(lib):
+    assert lib.nts_blockcast_t(A, A, A, 65535 * 128 + 1, 256, None) == UNSUPPORTED
+    assert lib.nts_blockcast(A, A, A, 1 << 30, 256 * 128, 128, None) == UNSUPPORTED   # 2^31
