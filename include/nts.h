@@ -410,6 +410,54 @@ NTS_API int nts_qknorm_rope_backward(const void *dYq_dev, int64_t lddyq, const v
 NTS_API int nts_qknorm_rope_backward_workspace(int64_t head_dim, int64_t *bytes_out);
 
 /*
+ * nts_qknorm_rope_axes, nts_qknorm_rope_axes_backward -- nts_qknorm_rope and
+ * its gradient for tokens with a position on each of several axes (time,
+ * height and width of images and video): pair i turns by the position on its
+ * own axis,
+ *
+ *     c = table[pos_a][i],  s = table[pos_a][rot_dim/2 + i],
+ *     pos_a = positions[t][a],  a = pair_axis[i].
+ *
+ * The table is the caller's: nts_rope_table_host's, whose pair i has one
+ * frequency on every axis, or one whose columns start their frequencies anew
+ * on each axis.
+ *   positions_dev    int64, token t's on axis a at t*pos_stride_t +
+ *                    a*pos_stride_a elements (strides >= 0): [T, naxes] or
+ *                    [naxes, T].  A token with a negative position on any axis
+ *                    is a padding row; one with none and a position >= P on an
+ *                    axis gives the same zeros and is reported by
+ *                    nts_check_status.
+ *   naxes            1 to 4.
+ *   pair_axis_host   uint8 [rot_dim/2] on the host, each below naxes, read
+ *                    before the call returns.
+ * Other arguments, limits and errors as nts_qknorm_rope and
+ * nts_qknorm_rope_backward (its workspace too); INVALID_ARG also for another
+ * naxes, an axis out of range or a negative stride, UNSUPPORTED for a table of
+ * 2^31 values or more or a stride whose last position lies beyond 64-bit
+ * addresses.
+ */
+NTS_API int nts_qknorm_rope_axes(const void *Q_dev, int64_t ldq, const float *gamma_q_dev,
+                                 void *Yq_dev, int64_t ldyq, float *rinv_q_dev,
+                                 const void *K_dev, int64_t ldk, const float *gamma_k_dev,
+                                 void *Yk_dev, int64_t ldyk, float *rinv_k_dev,
+                                 const int64_t *positions_dev, int64_t pos_stride_t,
+                                 int64_t pos_stride_a, int naxes,
+                                 const uint8_t *pair_axis_host, const float *table_dev,
+                                 int64_t P, int64_t T, int64_t nheads_q, int64_t nheads_k,
+                                 int64_t head_dim, int64_t rot_dim, int interleaved, float eps,
+                                 void *stream);
+
+NTS_API int nts_qknorm_rope_axes_backward(
+    const void *dYq_dev, int64_t lddyq, const void *dYk_dev, int64_t lddyk, const void *Q_dev,
+    int64_t ldq, const float *gamma_q_dev, const void *K_dev, int64_t ldk,
+    const float *gamma_k_dev, const int64_t *positions_dev, int64_t pos_stride_t,
+    int64_t pos_stride_a, int naxes, const uint8_t *pair_axis_host, const float *table_dev,
+    int64_t P, void *dQ_dev, int64_t lddq, void *dK_dev, int64_t lddk, float *dgamma_q_dev,
+    float *dgamma_k_dev, void *workspace_dev, int64_t workspace_bytes, int64_t T,
+    int64_t nheads_q, int64_t nheads_k, int64_t head_dim, int64_t rot_dim, int interleaved,
+    float eps, void *stream);
+
+/*
  * nts_rmsnorm_blockcast -- RMSNorm fused with the cast to E4M3 codes that
  * carry one fp32 scale per block of 128 contiguous values (the last block of
  * a row may be shorter), the operand of nts_gemm_blockscaled:

@@ -17,7 +17,9 @@ Around the QKV projection between the two:
 * ``gemm_blockscaled``  the matrix product of such operands on the tensor
                       cores, from single tokens to training batches;
 * ``qknorm_rope``, ``qknorm_rope_backward``  headwise QK-RMSNorm of Q and K
-                      with the rotary position embedding, and its gradient.
+                      with the rotary position embedding, and its gradient;
+* ``qknorm_rope_axes``, ``qknorm_rope_axes_backward``  the same with a position
+                      on each of several axes (images, video).
 
 Build the library with ``python -m normalization_token_split_gb300.build``.
 """
@@ -30,7 +32,8 @@ from .ops import (FMT_E2M1, FMT_E4M3, FMT_NVFP4, MxOut, check_status, codes_row_
                   set_wait_limit_ns, check_nvfp4_scale, set_pdl, set_host_chunks,
                   check_e8m0, inject_failure,
                   BlockOut, blockcast, blockcast_t, gemm_blockscaled, qknorm_rope,
-                  qknorm_rope_backward, rmsnorm_blockcast, rope_backward_workspace, rope_table)
+                  qknorm_rope_axes, qknorm_rope_axes_backward, qknorm_rope_backward,
+                  rmsnorm_blockcast, rope_axes, rope_backward_workspace, rope_table)
 
 __all__ = [
     "NtsError", "FMT_E4M3", "FMT_E2M1", "FMT_NVFP4", "MxOut", "qknorm_rms", "qknorm_rms_fp8", "qknorm_rms_heads", "qknorm_rms_qk", "layernorm_split", "qknorm_rms_mxcast", "qknorm_rms_qk_mxcast", "rmsnorm_mxcast", "mxnorm_cast", "mxnorm_postround_cast",
@@ -38,5 +41,6 @@ __all__ = [
     "rmsnorm_mxcast_host", "mxnorm_cast_host", "mxnorm_cast_host_noalloc", "set_tuning", "set_wait_limit_ns",
     "set_missing_tx", "set_schedule", "set_direct", "check_nvfp4_scale", "set_pdl", "set_host_chunks", "check_e8m0", "inject_failure",
     "BlockOut", "rmsnorm_blockcast", "blockcast", "blockcast_t", "gemm_blockscaled", "qknorm_rope",
-    "qknorm_rope_backward", "rope_backward_workspace", "rope_table",
+    "qknorm_rope_backward", "rope_backward_workspace", "rope_table", "rope_axes", "qknorm_rope_axes",
+    "qknorm_rope_axes_backward",
 ]

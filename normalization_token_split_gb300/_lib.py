@@ -52,6 +52,11 @@ def _declare(lib):
         "nts_qknorm_rope_backward": ([P, i64, P, i64, P, i64, P, P, i64, P, P, P, i64, P, i64, P,
                                       i64, P, P, P, i64, i64, i64, i64, i64, i64, i32, f32, P],
                                      i32),
+        "nts_qknorm_rope_axes": ([P, i64, P, P, i64, P, P, i64, P, P, i64, P, P, i64, i64, i32, P, P,
+                                  i64, i64, i64, i64, i64, i64, i32, f32, P], i32),
+        "nts_qknorm_rope_axes_backward": ([P, i64, P, i64, P, i64, P, P, i64, P, P, i64, i64, i32, P,
+                                           P, i64, P, i64, P, i64, P, P, P, i64, i64, i64, i64, i64,
+                                           i64, i32, f32, P], i32),
         "nts_qknorm_rope_backward_workspace": ([i64, ctypes.POINTER(i64)], i32),
         "nts_rmsnorm_blockcast": ([P, P, P, P, P, i64, i64, f32, P], i32),
         "nts_blockcast": ([P, P, P, i64, i64, i32, P], i32),

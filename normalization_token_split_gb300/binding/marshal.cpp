@@ -227,16 +227,19 @@ float* fptr(const at::Tensor& t) { return static_cast<float*>(ptr(t)); }
 
 // ------------------------------------------------------------- rotation
 
-// What a rotation and its gradient share.
+// What a rotation and its gradient share; opair: each pair's axis (bytes), or nullptr
+// for one axis.
 struct RopeArgs {
-  int dev;
+  int dev, naxes = 0;
+  int64_t pos_st = 1, pos_sa = 0;
+  const uint8_t* pair_axis = nullptr;
   Rows q, k;
   float *gq, *gk, *table;
   int64_t* pos;
   int64_t P, T, nq, nk, d, rot;
 
   RopeArgs(PyObject* oq, PyObject* ogq, PyObject* ok, PyObject* ogk, PyObject* opos,
-           PyObject* otable, PyObject* od) {
+           PyObject* otable, PyObject* od, PyObject* opair = nullptr) {
     dev = device_of("q", tensor("q", oq));
     q = rows("q", oq, dev);
     k = rows("k", ok, dev);
@@ -249,8 +252,18 @@ struct RopeArgs {
     const at::Tensor& tk = flat("gamma_k", ogk, at::kFloat, dev);
     if (tg.numel() != d) refuse("%s must hold head_dim values", "gamma_q");
     if (tk.numel() != d) refuse("%s must hold head_dim values", "gamma_k");
-    const at::Tensor& tp = flat("positions", opos, at::kLong, dev);
-    if (tp.numel() != T) refuse("%s must hold one position per token", "positions");
+    const at::Tensor& tp =
+        opair == nullptr ? flat("positions", opos, at::kLong, dev) : tensor("positions", opos);
+    if (opair == nullptr) {
+      if (tp.numel() != T) refuse("%s must hold one position per token", "positions");
+    } else {
+      check_place("positions", tp, at::kLong, dev);
+      if (matrix("positions", tp).size(0) != T || tp.size(1) < 1 || tp.size(1) > 4)
+        refuse("%s must hold 1 to 4 positions for each token", "positions");
+      naxes = (int)tp.size(1);
+      pos_st = tp.stride(0);
+      pos_sa = tp.stride(1);
+    }
     const at::Tensor& tt = matrix("table", flat("table", otable, at::kFloat, dev));
     gq = fptr(tg);
     gk = fptr(tk);
@@ -258,15 +271,17 @@ struct RopeArgs {
     pos = static_cast<int64_t*>(tp.data_ptr());
     P = tt.size(0);
     rot = tt.size(1);
+    if (opair != nullptr) {
+      if (!PyBytes_Check(opair)) refuse("%s must be bytes", "axes");
+      if (PyBytes_GET_SIZE(opair) != rot / 2) refuse("%s must hold an axis for each pair", "axes");
+      pair_axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(opair));
+    }
     nq = q.t.size(1) / d;
     nk = k.t.size(1) / d;
   }
 };
 
-// q, gamma_q, k, gamma_k, positions, table, head_dim, eps, interleaved, out_q,
-// out_k, rinv_q, rinv_k, want_rinv, stream
-PyObject* qknorm_rope(PyObject* const* a) {
-  const RopeArgs r(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+PyObject* rope(const RopeArgs& r, PyObject* const* a) {
   const float eps = real(a[7]);
   const int il = truth(a[8]);
   const On on(a[14], r.dev);
@@ -276,6 +291,11 @@ PyObject* qknorm_rope(PyObject* const* a) {
   if (want || given(a[11])) rq = output("rinv_q", a[11], {r.T, r.nq}, at::kFloat, on);
   if (want || given(a[12])) rk = output("rinv_k", a[12], {r.T, r.nk}, at::kFloat, on);
   call([&] {
+    if (r.pair_axis != nullptr)
+      return nts_qknorm_rope_axes(ptr(r.q.t), r.q.ld, r.gq, ptr(yq.t), yq.ld, fptr(rq), ptr(r.k.t),
+                                  r.k.ld, r.gk, ptr(yk.t), yk.ld, fptr(rk), r.pos, r.pos_st,
+                                  r.pos_sa, r.naxes, r.pair_axis, r.table, r.P, r.T, r.nq, r.nk,
+                                  r.d, r.rot, il, eps, on.handle);
     return nts_qknorm_rope(ptr(r.q.t), r.q.ld, r.gq, ptr(yq.t), yq.ld, fptr(rq), ptr(r.k.t),
                            r.k.ld, r.gk, ptr(yk.t), yk.ld, fptr(rk), r.pos, r.table, r.P, r.T, r.nq,
                            r.nk, r.d, r.rot, il, eps, on.handle);
@@ -283,10 +303,16 @@ PyObject* qknorm_rope(PyObject* const* a) {
   return tuple_of(yq.t, yk.t, rq, rk);
 }
 
-// dyq, dyk, q, gamma_q, k, gamma_k, positions, table, head_dim, eps,
-// interleaved, out_dq, out_dk, dgamma_q, dgamma_k, workspace, stream
-PyObject* qknorm_rope_backward(PyObject* const* a) {
-  const RopeArgs r(a[2], a[3], a[4], a[5], a[6], a[7], a[8]);
+// q, gamma_q, k, gamma_k, positions, table, head_dim, eps, interleaved, out_q,
+// out_k, rinv_q, rinv_k, want_rinv, stream, and axes
+PyObject* qknorm_rope(PyObject* const* a) {
+  return rope(RopeArgs(a[0], a[1], a[2], a[3], a[4], a[5], a[6]), a);
+}
+PyObject* qknorm_rope_axes(PyObject* const* a) {
+  return rope(RopeArgs(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[15]), a);
+}
+
+PyObject* rope_backward(const RopeArgs& r, PyObject* const* a) {
   const float eps = real(a[9]);
   const int il = truth(a[10]);
   const Rows dyq = rows("dyq", a[0], r.dev, &r.q.t), dyk = rows("dyk", a[1], r.dev, &r.k.t);
@@ -305,12 +331,27 @@ PyObject* qknorm_rope_backward(PyObject* const* a) {
     ws = scratch({bytes}, at::kByte, on);
   }
   call([&] {
+    if (r.pair_axis != nullptr)
+      return nts_qknorm_rope_axes_backward(
+          ptr(dyq.t), dyq.ld, ptr(dyk.t), dyk.ld, ptr(r.q.t), r.q.ld, r.gq, ptr(r.k.t), r.k.ld,
+          r.gk, r.pos, r.pos_st, r.pos_sa, r.naxes, r.pair_axis, r.table, r.P, ptr(dq.t), dq.ld,
+          ptr(dk.t), dk.ld, fptr(dgq), fptr(dgk), ptr(ws), ws.numel(), r.T, r.nq, r.nk, r.d, r.rot,
+          il, eps, on.handle);
     return nts_qknorm_rope_backward(ptr(dyq.t), dyq.ld, ptr(dyk.t), dyk.ld, ptr(r.q.t), r.q.ld,
                                     r.gq, ptr(r.k.t), r.k.ld, r.gk, r.pos, r.table, r.P, ptr(dq.t),
                                     dq.ld, ptr(dk.t), dk.ld, fptr(dgq), fptr(dgk), ptr(ws),
                                     ws.numel(), r.T, r.nq, r.nk, r.d, r.rot, il, eps, on.handle);
   });
   return tuple_of(dq.t, dk.t, dgq, dgk);
+}
+
+// dyq, dyk, q, gamma_q, k, gamma_k, positions, table, head_dim, eps,
+// interleaved, out_dq, out_dk, dgamma_q, dgamma_k, workspace, stream, and axes
+PyObject* qknorm_rope_backward(PyObject* const* a) {
+  return rope_backward(RopeArgs(a[2], a[3], a[4], a[5], a[6], a[7], a[8]), a);
+}
+PyObject* qknorm_rope_axes_backward(PyObject* const* a) {
+  return rope_backward(RopeArgs(a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[17]), a);
 }
 
 // ---------------------------------------------------------------- casts
@@ -440,6 +481,8 @@ PyObject* set_check(PyObject*, PyObject* f) {
 
 PyMethodDef g_methods[] = {ENTRY(qknorm_rope, 15),
                            ENTRY(qknorm_rope_backward, 17),
+                           ENTRY(qknorm_rope_axes, 16),
+                           ENTRY(qknorm_rope_axes_backward, 18),
                            ENTRY(rmsnorm_blockcast, 8),
                            ENTRY(blockcast, 5),
                            ENTRY(blockcast_t, 4),

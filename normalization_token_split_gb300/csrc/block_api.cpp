@@ -75,6 +75,35 @@ int check_table(const int64_t* positions, const float* table, int64_t T) {
   return check_vec("table", table, T, 16);
 }
 
+// The positions of a rotation call: [T], or of several axes, token t's on axis a at
+// t * st + a * sa, with the axis of each pair.
+struct RopePositions {
+  const int64_t* dev;
+  int64_t st = 1, sa = 0;
+  int naxes = 0;
+  const uint8_t* pair_axis = nullptr;
+  bool several = false;
+};
+
+int check_axes(const RopePositions& pos, int64_t P, int64_t T, int64_t rot_dim) {
+  if (!pos.several) return NTS_OK;
+  if (pos.naxes < 1 || pos.naxes > 4)
+    return fail(NTS_ERR_INVALID_ARG, "a token has 1 to 4 positions, got %d", pos.naxes);
+  if (pos.pair_axis == nullptr) return fail(NTS_ERR_INVALID_ARG, "pair_axis must be non-NULL");
+  for (int64_t i = 0; i < rot_dim / 2; ++i)
+    if (pos.pair_axis[i] >= pos.naxes)
+      return fail(NTS_ERR_INVALID_ARG, "pair %lld turns by axis %d of %d", (long long)i,
+                  (int)pos.pair_axis[i], pos.naxes);
+  if (pos.st < 0 || pos.sa < 0)
+    return fail(NTS_ERR_INVALID_ARG, "strides of the positions must be >= 0");
+  const int64_t far = INT64_MAX / 32;   // the last position's byte offset fits 64 bits
+  if ((T > 1 && pos.st > far / T) || pos.sa > far / 4)
+    return fail(NTS_ERR_UNSUPPORTED, "strides of the positions are too large");
+  if (P > (kMaxIndex - 1) / rot_dim)
+    return fail(NTS_ERR_UNSUPPORTED, "the table must stay below 2^31 values");
+  return NTS_OK;
+}
+
 int check_cast(const void* X, const uint8_t* codes, const float* scales, int64_t T, int64_t D) {
   if (T < 0) return fail(NTS_ERR_INVALID_ARG, "T must be >= 0, got %lld", (long long)T);
   if (D <= 0) return fail(NTS_ERR_INVALID_ARG, "D must be > 0, got %lld", (long long)D);
@@ -108,6 +137,81 @@ int cast(const BlockcastRequest& rq, void* stream) {
       [&] { return launch_blockcast(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
 }
 
+int run_rope(const void* Q_dev, int64_t ldq, const float* gamma_q_dev, void* Yq_dev, int64_t ldyq,
+             float* rinv_q_dev, const void* K_dev, int64_t ldk, const float* gamma_k_dev,
+             void* Yk_dev, int64_t ldyk, float* rinv_k_dev, const RopePositions& pos,
+             const float* table_dev, int64_t P, int64_t T, int64_t nheads_q, int64_t nheads_k,
+             int64_t head_dim, int64_t rot_dim, int interleaved, float eps, void* stream) {
+  int rc = check_rope_shape(P, T, nheads_q, nheads_k, head_dim, rot_dim, eps);
+  const int64_t wq = nheads_q * head_dim, wk = nheads_k * head_dim;
+  if (rc == NTS_OK) rc = check_rows("Q", Q_dev, ldq, wq, T);
+  if (rc == NTS_OK) rc = check_rows("K", K_dev, ldk, wk, T);
+  if (rc == NTS_OK) rc = check_rows("Yq", Yq_dev, ldyq, wq, T);
+  if (rc == NTS_OK) rc = check_rows("Yk", Yk_dev, ldyk, wk, T);
+  if (rc == NTS_OK) rc = check_vec("gamma_q", gamma_q_dev, T, 16);
+  if (rc == NTS_OK) rc = check_vec("gamma_k", gamma_k_dev, T, 16);
+  if (rc == NTS_OK) rc = check_table(pos.dev, table_dev, T);
+  if (rc == NTS_OK) rc = check_axes(pos, P, T, rot_dim);
+  if (rc != NTS_OK) return rc;
+  if (!aligned(rinv_q_dev, 4) || !aligned(rinv_k_dev, 4))
+    return fail(NTS_ERR_UNSUPPORTED, "rinv must be 4-byte aligned");
+  if (T == 0) return NTS_OK;
+  const RopeRequest rq{{{Q_dev, nullptr, Yq_dev, gamma_q_dev, rinv_q_dev, ldq, 0, ldyq, nheads_q},
+                        {K_dev, nullptr, Yk_dev, gamma_k_dev, rinv_k_dev, ldk, 0, ldyk, nheads_k}},
+                       pos.dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps,
+                       pos.naxes, pos.st, pos.sa, pos.pair_axis};
+  return guarded(
+      [&] { return launch_rope(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
+}
+
+int run_rope_backward(const void* dYq_dev, int64_t lddyq, const void* dYk_dev, int64_t lddyk,
+                      const void* Q_dev, int64_t ldq, const float* gamma_q_dev, const void* K_dev,
+                      int64_t ldk, const float* gamma_k_dev, const RopePositions& pos,
+                      const float* table_dev, int64_t P, void* dQ_dev, int64_t lddq, void* dK_dev,
+                      int64_t lddk, float* dgamma_q_dev, float* dgamma_k_dev, void* workspace_dev,
+                      int64_t workspace_bytes, int64_t T, int64_t nheads_q, int64_t nheads_k,
+                      int64_t head_dim, int64_t rot_dim, int interleaved, float eps,
+                      void* stream) {
+  int rc = check_rope_shape(P, T, nheads_q, nheads_k, head_dim, rot_dim, eps);
+  const int64_t wq = nheads_q * head_dim, wk = nheads_k * head_dim;
+  if (rc == NTS_OK) rc = check_rows("dYq", dYq_dev, lddyq, wq, T);
+  if (rc == NTS_OK) rc = check_rows("dYk", dYk_dev, lddyk, wk, T);
+  if (rc == NTS_OK) rc = check_rows("Q", Q_dev, ldq, wq, T);
+  if (rc == NTS_OK) rc = check_rows("K", K_dev, ldk, wk, T);
+  if (rc == NTS_OK) rc = check_rows("dQ", dQ_dev, lddq, wq, T);
+  if (rc == NTS_OK) rc = check_rows("dK", dK_dev, lddk, wk, T);
+  if (rc == NTS_OK) rc = check_vec("gamma_q", gamma_q_dev, T, 16);
+  if (rc == NTS_OK) rc = check_vec("gamma_k", gamma_k_dev, T, 16);
+  if (rc == NTS_OK) rc = check_table(pos.dev, table_dev, T);
+  if (rc == NTS_OK) rc = check_axes(pos, P, T, rot_dim);
+  if (rc == NTS_OK && eps < FLT_MIN)   // rinv^2 of a row of zeros would overflow
+    rc = fail(NTS_ERR_UNSUPPORTED, "eps must be at least 2^-126 for the gradient");
+  // the gains' gradients are written for an empty batch too
+  if (rc == NTS_OK) rc = check_vec("dgamma_q", dgamma_q_dev, 1, 4);
+  if (rc == NTS_OK) rc = check_vec("dgamma_k", dgamma_k_dev, 1, 4);
+  if (rc != NTS_OK) return rc;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    cudaError_t e = cudaMemsetAsync(dgamma_q_dev, 0, head_dim * sizeof(float), s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dgamma_k_dev, 0, head_dim * sizeof(float), s);
+    return e == cudaSuccess ? NTS_OK : fail_cuda(e, "clearing the gains' gradients");
+  }
+  const int64_t need = (int64_t)kRopePartials * head_dim * (int64_t)sizeof(float);
+  if (workspace_dev == nullptr || workspace_bytes < need)
+    return fail(NTS_ERR_INVALID_ARG, "the workspace needs %lld bytes, got %lld", (long long)need,
+                (long long)(workspace_dev == nullptr ? 0 : workspace_bytes));
+  if (!aligned(workspace_dev, 4))
+    return fail(NTS_ERR_UNSUPPORTED, "the workspace must be 4-byte aligned");
+  const RopeRequest rq{{{Q_dev, dYq_dev, dQ_dev, gamma_q_dev, nullptr, ldq, lddyq, lddq, nheads_q},
+                        {K_dev, dYk_dev, dK_dev, gamma_k_dev, nullptr, ldk, lddyk, lddk, nheads_k}},
+                       pos.dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps,
+                       pos.naxes, pos.st, pos.sa, pos.pair_axis};
+  return guarded([&] {
+    return launch_rope_backward(rq, dgamma_q_dev, dgamma_k_dev, static_cast<float*>(workspace_dev),
+                                s, current_tuning());
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -138,24 +242,24 @@ int nts_qknorm_rope(const void* Q_dev, int64_t ldq, const float* gamma_q_dev, vo
                     const int64_t* positions_dev, const float* table_dev, int64_t P, int64_t T,
                     int64_t nheads_q, int64_t nheads_k, int64_t head_dim, int64_t rot_dim,
                     int interleaved, float eps, void* stream) {
-  int rc = check_rope_shape(P, T, nheads_q, nheads_k, head_dim, rot_dim, eps);
-  const int64_t wq = nheads_q * head_dim, wk = nheads_k * head_dim;
-  if (rc == NTS_OK) rc = check_rows("Q", Q_dev, ldq, wq, T);
-  if (rc == NTS_OK) rc = check_rows("K", K_dev, ldk, wk, T);
-  if (rc == NTS_OK) rc = check_rows("Yq", Yq_dev, ldyq, wq, T);
-  if (rc == NTS_OK) rc = check_rows("Yk", Yk_dev, ldyk, wk, T);
-  if (rc == NTS_OK) rc = check_vec("gamma_q", gamma_q_dev, T, 16);
-  if (rc == NTS_OK) rc = check_vec("gamma_k", gamma_k_dev, T, 16);
-  if (rc == NTS_OK) rc = check_table(positions_dev, table_dev, T);
-  if (rc != NTS_OK) return rc;
-  if (!aligned(rinv_q_dev, 4) || !aligned(rinv_k_dev, 4))
-    return fail(NTS_ERR_UNSUPPORTED, "rinv must be 4-byte aligned");
-  if (T == 0) return NTS_OK;
-  const RopeRequest rq{{{Q_dev, nullptr, Yq_dev, gamma_q_dev, rinv_q_dev, ldq, 0, ldyq, nheads_q},
-                        {K_dev, nullptr, Yk_dev, gamma_k_dev, rinv_k_dev, ldk, 0, ldyk, nheads_k}},
-                       positions_dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps};
-  return guarded(
-      [&] { return launch_rope(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
+  return run_rope(Q_dev, ldq, gamma_q_dev, Yq_dev, ldyq, rinv_q_dev, K_dev, ldk, gamma_k_dev,
+                  Yk_dev, ldyk, rinv_k_dev, RopePositions{positions_dev}, table_dev, P, T,
+                  nheads_q, nheads_k, head_dim, rot_dim, interleaved, eps, stream);
+}
+
+int nts_qknorm_rope_axes(const void* Q_dev, int64_t ldq, const float* gamma_q_dev, void* Yq_dev,
+                         int64_t ldyq, float* rinv_q_dev, const void* K_dev, int64_t ldk,
+                         const float* gamma_k_dev, void* Yk_dev, int64_t ldyk, float* rinv_k_dev,
+                         const int64_t* positions_dev, int64_t pos_stride_t, int64_t pos_stride_a,
+                         int naxes, const uint8_t* pair_axis_host, const float* table_dev,
+                         int64_t P, int64_t T, int64_t nheads_q, int64_t nheads_k,
+                         int64_t head_dim, int64_t rot_dim, int interleaved, float eps,
+                         void* stream) {
+  return run_rope(Q_dev, ldq, gamma_q_dev, Yq_dev, ldyq, rinv_q_dev, K_dev, ldk, gamma_k_dev,
+                  Yk_dev, ldyk, rinv_k_dev,
+                  RopePositions{positions_dev, pos_stride_t, pos_stride_a, naxes, pair_axis_host, true},
+                  table_dev, P, T, nheads_q, nheads_k, head_dim, rot_dim, interleaved, eps,
+                  stream);
 }
 
 int nts_qknorm_rope_backward_workspace(int64_t head_dim, int64_t* bytes_out) {
@@ -174,43 +278,30 @@ int nts_qknorm_rope_backward(const void* dYq_dev, int64_t lddyq, const void* dYk
                              void* workspace_dev, int64_t workspace_bytes, int64_t T,
                              int64_t nheads_q, int64_t nheads_k, int64_t head_dim,
                              int64_t rot_dim, int interleaved, float eps, void* stream) {
-  int rc = check_rope_shape(P, T, nheads_q, nheads_k, head_dim, rot_dim, eps);
-  const int64_t wq = nheads_q * head_dim, wk = nheads_k * head_dim;
-  if (rc == NTS_OK) rc = check_rows("dYq", dYq_dev, lddyq, wq, T);
-  if (rc == NTS_OK) rc = check_rows("dYk", dYk_dev, lddyk, wk, T);
-  if (rc == NTS_OK) rc = check_rows("Q", Q_dev, ldq, wq, T);
-  if (rc == NTS_OK) rc = check_rows("K", K_dev, ldk, wk, T);
-  if (rc == NTS_OK) rc = check_rows("dQ", dQ_dev, lddq, wq, T);
-  if (rc == NTS_OK) rc = check_rows("dK", dK_dev, lddk, wk, T);
-  if (rc == NTS_OK) rc = check_vec("gamma_q", gamma_q_dev, T, 16);
-  if (rc == NTS_OK) rc = check_vec("gamma_k", gamma_k_dev, T, 16);
-  if (rc == NTS_OK) rc = check_table(positions_dev, table_dev, T);
-  if (rc == NTS_OK && eps < FLT_MIN)   // rinv^2 of a row of zeros would overflow
-    rc = fail(NTS_ERR_UNSUPPORTED, "eps must be at least 2^-126 for the gradient");
-  // the gains' gradients are written for an empty batch too
-  if (rc == NTS_OK) rc = check_vec("dgamma_q", dgamma_q_dev, 1, 4);
-  if (rc == NTS_OK) rc = check_vec("dgamma_k", dgamma_k_dev, 1, 4);
-  if (rc != NTS_OK) return rc;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0) {
-    cudaError_t e = cudaMemsetAsync(dgamma_q_dev, 0, head_dim * sizeof(float), s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dgamma_k_dev, 0, head_dim * sizeof(float), s);
-    return e == cudaSuccess ? NTS_OK : fail_cuda(e, "clearing the gains' gradients");
-  }
-  int64_t need = 0;
-  nts_qknorm_rope_backward_workspace(head_dim, &need);
-  if (workspace_dev == nullptr || workspace_bytes < need)
-    return fail(NTS_ERR_INVALID_ARG, "the workspace needs %lld bytes, got %lld", (long long)need,
-                (long long)(workspace_dev == nullptr ? 0 : workspace_bytes));
-  if (!aligned(workspace_dev, 4))
-    return fail(NTS_ERR_UNSUPPORTED, "the workspace must be 4-byte aligned");
-  const RopeRequest rq{{{Q_dev, dYq_dev, dQ_dev, gamma_q_dev, nullptr, ldq, lddyq, lddq, nheads_q},
-                        {K_dev, dYk_dev, dK_dev, gamma_k_dev, nullptr, ldk, lddyk, lddk, nheads_k}},
-                       positions_dev, table_dev, P, T, head_dim, rot_dim, interleaved != 0, eps};
-  return guarded([&] {
-    return launch_rope_backward(rq, dgamma_q_dev, dgamma_k_dev, static_cast<float*>(workspace_dev),
-                                s, current_tuning());
-  });
+  return run_rope_backward(dYq_dev, lddyq, dYk_dev, lddyk, Q_dev, ldq, gamma_q_dev, K_dev, ldk,
+                           gamma_k_dev, RopePositions{positions_dev}, table_dev, P, dQ_dev, lddq,
+                           dK_dev, lddk, dgamma_q_dev, dgamma_k_dev, workspace_dev,
+                           workspace_bytes, T, nheads_q, nheads_k, head_dim, rot_dim, interleaved,
+                           eps, stream);
+}
+
+int nts_qknorm_rope_axes_backward(const void* dYq_dev, int64_t lddyq, const void* dYk_dev,
+                                  int64_t lddyk, const void* Q_dev, int64_t ldq,
+                                  const float* gamma_q_dev, const void* K_dev, int64_t ldk,
+                                  const float* gamma_k_dev, const int64_t* positions_dev,
+                                  int64_t pos_stride_t, int64_t pos_stride_a, int naxes,
+                                  const uint8_t* pair_axis_host, const float* table_dev,
+                                  int64_t P, void* dQ_dev, int64_t lddq, void* dK_dev,
+                                  int64_t lddk, float* dgamma_q_dev, float* dgamma_k_dev,
+                                  void* workspace_dev, int64_t workspace_bytes, int64_t T,
+                                  int64_t nheads_q, int64_t nheads_k, int64_t head_dim,
+                                  int64_t rot_dim, int interleaved, float eps, void* stream) {
+  return run_rope_backward(dYq_dev, lddyq, dYk_dev, lddyk, Q_dev, ldq, gamma_q_dev, K_dev, ldk,
+                           gamma_k_dev,
+                           RopePositions{positions_dev, pos_stride_t, pos_stride_a, naxes, pair_axis_host, true},
+                           table_dev, P, dQ_dev, lddq, dK_dev, lddk, dgamma_q_dev, dgamma_k_dev,
+                           workspace_dev, workspace_bytes, T, nheads_q, nheads_k, head_dim,
+                           rot_dim, interleaved, eps, stream);
 }
 
 int nts_rmsnorm_blockcast(const void* X_dev, const float* gamma_dev, uint8_t* codes_dev,

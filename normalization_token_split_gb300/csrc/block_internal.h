@@ -34,6 +34,10 @@ struct RopeRequest {
   int64_t P, T, head_dim, rot_dim;
   int interleaved;
   float eps;
+  // several axes: positions per token, their strides, and each pair's axis (host)
+  int naxes = 0;
+  int64_t pos_st = 0, pos_sa = 0;
+  const uint8_t* pair_axis = nullptr;
 };
 // Most CTAs (rows of partial sums in the workspace) of a gradient launch.
 constexpr int kRopePartials = 1024;

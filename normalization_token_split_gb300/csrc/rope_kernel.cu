@@ -90,6 +90,9 @@ struct RopeParams {
   float* dgamma[2];          // backward
   unsigned int* sched;       // backward: zeroed counter pair of the launch (its second
                              // word counts CTAs), or nullptr: a launch of its own sums
+  int naxes;                 // several axes: positions per token, their strides and the
+  int64_t pos_st, pos_sa;    // axis of each pair, two bits each
+  uint32_t pair_axis[16];
 };
 
 // A lane's place: the element offsets of its two vectors, whether it rotates
@@ -240,6 +243,91 @@ __device__ __forceinline__ bool table_row(const RopeParams& p, unsigned t, int l
   if (pos >= p.P && lane == 0) atomicOr(&g_rope_status, kStatusPosition);
   *row = p.table + (ok ? pos : 0) * p.rot;
   return ok;
+}
+
+// Where a token's angles stand in the table.  With one axis: a row.  With several,
+// each pair's come from the row of the position on its axis: lane a of every four
+// holds the offset of axis a's row, and a shuffle in fours hands each pair its own
+// (the pair's two bits are the source lane), so a lane reads one position whatever
+// the number of axes.
+template <bool AX>
+struct RopeRows {
+  const float* row;   // one axis
+  int at;             // several: offset of this lane's axis's row
+  bool ok;
+};
+
+// Several axes: the axes of the lane's two groups of four pairs, two bits each, and
+// whether each group has one axis (its four cosines are then one load).
+struct RopeLaneAxes {
+  uint32_t bits = 0;
+  bool same0 = true, same1 = true;
+};
+
+template <bool AX>
+__device__ __forceinline__ RopeLaneAxes lane_axes(const RopeParams& p, const RopeLane& l) {
+  RopeLaneAxes x;
+  if (AX && l.turns) {
+    const uint32_t a = p.pair_axis[l.c0 >> 4] >> (2 * (l.c0 & 15)) & 0xffu;
+    const uint32_t b = p.pair_axis[l.c1 >> 4] >> (2 * (l.c1 & 15)) & 0xffu;
+    x.bits = a | b << 8;
+    x.same0 = a == (a & 3u) * 0x55u;
+    x.same1 = b == (b & 3u) * 0x55u;
+  }
+  return x;
+}
+
+template <bool AX>
+__device__ __forceinline__ RopeRows<AX> find_rows(const RopeParams& p, unsigned t, int lane) {
+  RopeRows<AX> r;
+  if (!AX) {
+    r.ok = table_row(p, t, lane, &r.row);
+    return r;
+  }
+  const int a = lane & 3;
+  int64_t pos = 0;
+  if (a < p.naxes) pos = __ldg(p.pos + t * p.pos_st + a * p.pos_sa);
+  const bool low = __any_sync(0xFFFFFFFFu, pos < 0);
+  const bool high = __any_sync(0xFFFFFFFFu, pos >= p.P);
+  r.ok = !low && !high;
+  if (high && !low && lane == 0) atomicOr(&g_rope_status, kStatusPosition);
+  r.at = r.ok ? (int)pos * p.rot : 0;
+  return r;
+}
+
+// The eight cosines and sines of a lane that turns.
+template <bool AX>
+__device__ __forceinline__ void load_angles(const RopeParams& p, const RopeRows<AX>& r,
+                                            const RopeLane& l, const RopeLaneAxes& x,
+                                            float (&c)[8], float (&s)[8]) {
+  if (!AX) {
+    if (l.turns) {
+      load8(c, r.row + l.c0, r.row + l.c1);
+      load8(s, r.row + p.rot / 2 + l.c0, r.row + p.rot / 2 + l.c1);
+    }
+    return;
+  }
+  int at[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)   // the source lane counts modulo the width
+    at[i] = __shfl_sync(0xFFFFFFFFu, r.at, x.bits >> (2 * i), 4);
+  if (!l.turns) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* col = p.table + (h ? l.c1 : l.c0);
+    if (h ? x.same1 : x.same0) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(col + at[4 * h]));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(col + at[4 * h] + p.rot / 2));
+      c[4 * h] = u.x, c[4 * h + 1] = u.y, c[4 * h + 2] = u.z, c[4 * h + 3] = u.w;
+      s[4 * h] = v.x, s[4 * h + 1] = v.y, s[4 * h + 2] = v.z, s[4 * h + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[4 * h + i] = __ldg(col + at[4 * h + i] + i);
+        s[4 * h + i] = __ldg(col + at[4 * h + i] + p.rot / 2 + i);
+      }
+    }
+  }
 }
 
 // Walks a warp's items, `step` apart, without a division per item: item =
@@ -447,11 +535,12 @@ __device__ __forceinline__ void reduce_gain_grad(const RopeParams& p, const Rope
 // A warp takes one round of heads of one token straight from global memory.
 // Every load of an item is issued at once; nothing is staged.
 
-template <bool IL>
+template <bool IL, bool AX>
 __global__ void __launch_bounds__(kRopeThreads) rope_forward_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << p.lshift;
   const RopeLane l = rope_lane<IL>(p, lane & (lanes - 1));
+  const RopeLaneAxes ax = lane_axes<AX>(p, l);
   const unsigned per_token = p.ten[0].chunks + p.ten[1].chunks;
   const unsigned item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
   grid_dependency_wait();
@@ -475,14 +564,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_forward_kernel(const RopePa
     load8(g0, tn.gamma + l.e0, tn.gamma + l.e0 + 4);
     load8(g1, tn.gamma + l.e1, tn.gamma + l.e1 + 4);
   }
-  const float* row;
-  const bool ok = table_row(p, t, lane, &row);
-  if (l.turns) {
-    load8(c, row + l.c0, row + l.c1);
-    load8(s, row + p.rot / 2 + l.c0, row + p.rot / 2 + l.c1);
-  }
+  const RopeRows<AX> rows = find_rows<AX>(p, t, lane);
+  load_angles<AX>(p, rows, l, ax, c, s);
   float rinv;
-  forward_head<IL>(p, l, lanes, x0, x1, gain_factors<IL>(l, g0, g1, c, s), ok, &rinv);
+  forward_head<IL>(p, l, lanes, x0, x1, gain_factors<IL>(l, g0, g1, c, s), rows.ok, &rinv);
   if (in) {
     __nv_bfloat16* y = tn.out + (int64_t)t * tn.ldout + at;
     st_global_v4_stream(y + l.e0, x0);
@@ -493,12 +578,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_forward_kernel(const RopePa
 
 // The first ctas_q CTAs take the items of Q, the others those of K, in a
 // fixed order, so the result does not depend on timing.
-template <bool IL>
+template <bool IL, bool AX>
 __global__ void __launch_bounds__(kRopeThreads) rope_backward_kernel(const RopeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << p.lshift;
   const RopeLane l = rope_lane<IL>(p, lane & (lanes - 1));
+  const RopeLaneAxes ax = lane_axes<AX>(p, l);
   const int ti = blockIdx.x >= p.ctas_q;
   const RopeTensor& tn = p.ten[ti];
   const unsigned ctas = ti ? gridDim.x - p.ctas_q : p.ctas_q;
@@ -524,14 +610,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_backward_kernel(const RopeP
       y0 = ldg_stream(y + l.e0);
       y1 = ldg_stream(y + l.e1);
     }
-    const float* row;
-    const bool ok = table_row(p, t, lane, &row);
+    const RopeRows<AX> rows = find_rows<AX>(p, t, lane);
     float c[8] = {}, s[8] = {};
-    if (l.turns) {
-      load8(c, row + l.c0, row + l.c1);
-      load8(s, row + p.rot / 2 + l.c0, row + p.rot / 2 + l.c1);
-    }
-    if (ok)   // of the whole warp
+    load_angles<AX>(p, rows, l, ax, c, s);
+    if (rows.ok)   // of the whole warp
       backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, s, sum);
     else
       x0 = x1 = make_uint4(0, 0, 0, 0);
@@ -597,12 +679,13 @@ __device__ __forceinline__ void ring_drain(const RopeParams& p, const RopeRing& 
   }
 }
 
-template <bool IL>
+template <bool IL, bool AX>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_forward_ring_kernel(const RopeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << p.lshift;
   const RopeLane l = rope_lane<IL>(p, lane & (lanes - 1));
+  const RopeLaneAxes ax = lane_axes<AX>(p, l);
   const int hps = 32 >> p.lshift;
   const unsigned per_token = p.ten[0].chunks + p.ten[1].chunks;
   const unsigned items = p.T * per_token;
@@ -640,17 +723,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_forward_ring_kernel(cons
     int ti;
     const RopeItem it = place(cur, &ti);
     const RopeTensor& tn = p.ten[ti];
-    const float* row;
-    const bool ok = table_row(p, it.t, lane, &row);
+    const RopeRows<AX> rows = find_rows<AX>(p, it.t, lane);
     float c[8] = {}, sn[8] = {}, g0[8] = {}, g1[8] = {};
     if (l.active) {
       load8(g0, tn.gamma + l.e0, tn.gamma + l.e0 + 4);
       load8(g1, tn.gamma + l.e1, tn.gamma + l.e1 + 4);
     }
-    if (l.turns) {
-      load8(c, row + l.c0, row + l.c1);
-      load8(sn, row + p.rot / 2 + l.c0, row + p.rot / 2 + l.c1);
-    }
+    load_angles<AX>(p, rows, l, ax, c, sn);
     const RopeFactors f = gain_factors<IL>(l, g0, g1, c, sn);
     if (!ring_wait(p, ring, s, parity)) {
       ring_drain(p, ring, s, parity, min(mine - n, (unsigned)ring.S));
@@ -669,7 +748,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_forward_ring_kernel(cons
         x1 = lds128(stage + (h * p.d + l.e1) * 2);
       }
       float rinv;
-      forward_head<IL>(p, l, lanes, x0, x1, f, ok, &rinv);
+      forward_head<IL>(p, l, lanes, x0, x1, f, rows.ok, &rinv);
       if (in) {
         st_global_v4_stream(y + (int64_t)h * p.d + l.e0, x0);
         st_global_v4_stream(y + (int64_t)h * p.d + l.e1, x1);
@@ -689,12 +768,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_forward_ring_kernel(cons
   }
 }
 
-template <bool IL>
+template <bool IL, bool AX>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(const RopeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << p.lshift;
   const RopeLane l = rope_lane<IL>(p, lane & (lanes - 1));
+  const RopeLaneAxes ax = lane_axes<AX>(p, l);
   const int hps = 32 >> p.lshift;
   const int ti = blockIdx.x >= p.ctas_q;
   const RopeTensor& tn = p.ten[ti];
@@ -732,13 +812,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(con
   uint32_t parity = 0;
   for (unsigned n = 0; n < mine; ++n, cur.advance()) {
     const RopeItem it = rope_item(tn, cur.t, cur.chunk, p.heads);
-    const float* row;
-    const bool ok = table_row(p, it.t, lane, &row);
+    const RopeRows<AX> rows = find_rows<AX>(p, it.t, lane);
     float c[8] = {}, sn[8] = {};
-    if (l.turns) {
-      load8(c, row + l.c0, row + l.c1);
-      load8(sn, row + p.rot / 2 + l.c0, row + p.rot / 2 + l.c1);
-    }
+    load_angles<AX>(p, rows, l, ax, c, sn);
     if (!ring_wait(p, ring, s, parity)) {
       ring_drain(p, ring, s, parity, min(mine - n, (unsigned)ring.S));
       break;
@@ -756,7 +832,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_ring_kernel(con
         y0 = lds128(at + half + l.e0 * 2);
         y1 = lds128(at + half + l.e1 * 2);
       }
-      if (ok)
+      if (rows.ok)
         backward_head<IL>(p, l, lanes, x0, x1, y0, y1, gain, c, sn, sum);
       else
         x0 = x1 = make_uint4(0, 0, 0, 0);
@@ -830,6 +906,11 @@ GainGradKernel pick_gain_grad(int rows) {
 
 using RopeKernel = void (*)(RopeParams);
 
+// The instantiation for a call's pairs and axes.
+#define NTS_PICK_ROPE(kernel, rq)                                            \
+  ((rq).naxes > 0 ? ((rq).interleaved ? kernel<true, true> : kernel<false, true>) \
+                  : ((rq).interleaved ? kernel<true, false> : kernel<false, false>))
+
 RopeParams common_params(const RopeRequest& rq, const LaunchTuning& tune) {
   RopeParams p = {};
   for (int i = 0; i < 2; ++i) {
@@ -856,6 +937,11 @@ RopeParams common_params(const RopeRequest& rq, const LaunchTuning& tune) {
   p.inv_d = 1.0f / (float)p.d;
   p.wait_limit_ns = tune.wait_limit_ns;
   p.missing_tx = tune.missing_tx;
+  p.naxes = rq.naxes;
+  p.pos_st = rq.pos_st;
+  p.pos_sa = rq.pos_sa;
+  for (int i = 0; rq.naxes > 0 && i < p.rot / 2; ++i)
+    p.pair_axis[i >> 4] |= (uint32_t)rq.pair_axis[i] << (2 * (i & 15));
   return p;
 }
 
@@ -919,9 +1005,9 @@ int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& 
   const bool ring = tune.force_rows > 0 || items[0] + items[1] > (uint64_t)dev.sm_count * kDirectItems;
   size_t smem = 0;
   unsigned grid = (unsigned)((items[0] + items[1] + kRopeWarps - 1) / kRopeWarps);
-  RopeKernel kern = rq.interleaved ? rope_forward_kernel<true> : rope_forward_kernel<false>;
+  RopeKernel kern = NTS_PICK_ROPE(rope_forward_kernel, rq);
   if (ring) {
-    kern = rq.interleaved ? rope_forward_ring_kernel<true> : rope_forward_ring_kernel<false>;
+    kern = NTS_PICK_ROPE(rope_forward_ring_kernel, rq);
     rc = set_items(&p, tune.force_rows > 0 ? tune.force_rows : even_rounds(p, kForwardRounds), items);
     if (rc != NTS_OK) return rc;
     smem = set_ring(&p, 1, tune.force_stages > 0 ? tune.force_stages : kForwardStages);
@@ -934,8 +1020,8 @@ int launch_rope(const RopeRequest& rq, cudaStream_t stream, const LaunchTuning& 
     grid = (unsigned)std::min<uint64_t>((items[0] + items[1] + kRopeWarps - 1) / kRopeWarps,
                                         (uint64_t)per_sm * dev.sm_count);
   }
-  log_launch("qknorm_rope", "T=%u heads=%d+%d d=%d rot=%d ring=%d per item=%d S=%d smem=%zu grid=%u",
-             p.T, p.ten[0].nheads, p.ten[1].nheads, p.d, p.rot, ring, p.heads, p.stages, smem, grid);
+  log_launch("qknorm_rope", "T=%u heads=%d+%d d=%d rot=%d axes=%d ring=%d per item=%d S=%d smem=%zu grid=%u",
+             p.T, p.ten[0].nheads, p.ten[1].nheads, p.d, p.rot, p.naxes, ring, p.heads, p.stages, smem, grid);
   return launch(kern, dim3(grid), dim3(kRopeThreads), smem, stream, tune.pdl != 0, p);
 }
 
@@ -952,9 +1038,9 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
   const bool ring = tune.force_rows > 0 ||
                     items[0] + items[1] > (uint64_t)dev.sm_count * kBackwardDirectItems;
   size_t smem = (size_t)kRopeWarps * std::max(p.d, 128) * sizeof(float);
-  RopeKernel kern = rq.interleaved ? rope_backward_kernel<true> : rope_backward_kernel<false>;
+  RopeKernel kern = NTS_PICK_ROPE(rope_backward_kernel, rq);
   if (ring) {
-    kern = rq.interleaved ? rope_backward_ring_kernel<true> : rope_backward_ring_kernel<false>;
+    kern = NTS_PICK_ROPE(rope_backward_ring_kernel, rq);
     rc = set_items(&p, tune.force_rows > 0 ? tune.force_rows : even_rounds(p, kBackwardRounds), items);
     if (rc != NTS_OK) return rc;
     smem = set_ring(&p, 2, tune.force_stages > 0 ? tune.force_stages : kBackwardStages);
@@ -994,8 +1080,8 @@ int launch_rope_backward(const RopeRequest& rq, float* dgamma_q, float* dgamma_k
                 ? sched_counters(stream)
                 : nullptr;
   log_launch("qknorm_rope_backward",
-             "T=%u heads=%d+%d d=%d rot=%d ring=%d per item=%d S=%d smem=%zu grid=%u (%u for Q)",
-             p.T, p.ten[0].nheads, p.ten[1].nheads, p.d, p.rot, ring, p.heads, p.stages, smem, grid,
+             "T=%u heads=%d+%d d=%d rot=%d axes=%d ring=%d per item=%d S=%d smem=%zu grid=%u (%u for Q)",
+             p.T, p.ten[0].nheads, p.ten[1].nheads, p.d, p.rot, p.naxes, ring, p.heads, p.stages, smem, grid,
              p.ctas_q);
   rc = launch(kern, dim3(grid), dim3(kRopeThreads), smem, stream, tune.pdl != 0, p);
   if (rc != NTS_OK || p.sched != nullptr) return rc;

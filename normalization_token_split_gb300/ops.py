@@ -354,6 +354,57 @@ def rope_backward_workspace(head_dim: int) -> int:
     return n.value
 
 
+def rope_axes(sections, cyclic: bool = False) -> bytes:
+    """The axis of each pair for qknorm_rope_axes: sections[a] pairs turn by axis
+    a, in runs one axis after another, or (cyclic) the axes taking the pairs in
+    turn, for as long as the shorter ones last."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError("sections must be 1 to 4 counts of pairs")
+    if not cyclic:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    order = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n > 0:
+                order.append(a)
+                left[a] -= 1
+    return bytes(order)
+
+
+def qknorm_rope_axes(q: torch.Tensor, gamma_q: torch.Tensor, k: torch.Tensor,
+                     gamma_k: torch.Tensor, positions: torch.Tensor, table: torch.Tensor,
+                     axes: bytes, head_dim: int, eps: float = 1e-6, interleaved: bool = False,
+                     out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None,
+                     rinv_q: Optional[torch.Tensor] = None, rinv_k: Optional[torch.Tensor] = None,
+                     want_rinv: bool = False, stream=None):
+    """qknorm_rope for tokens with a position on each of 1 to 4 axes: positions
+    is int64 [T, A] with any strides (a transposed [A, T] too), axes the axis of
+    each of the rot_dim / 2 pairs (rope_axes).  A token with a negative position on
+    any axis is a padding row.  Pair i's angle is column i of the table, so a
+    table's columns may hold any frequencies: rope_table's, or those of one
+    rope_table per axis side by side (their cosines, then their sines)."""
+    return marshal().qknorm_rope_axes(q, gamma_q, k, gamma_k, positions, table, head_dim, eps,
+                                      interleaved, out_q, out_k, rinv_q, rinv_k, want_rinv, stream,
+                                      axes)
+
+
+def qknorm_rope_axes_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor,
+                              gamma_q: torch.Tensor, k: torch.Tensor, gamma_k: torch.Tensor,
+                              positions: torch.Tensor, table: torch.Tensor, axes: bytes,
+                              head_dim: int, eps: float = 1e-6, interleaved: bool = False,
+                              out_dq: Optional[torch.Tensor] = None,
+                              out_dk: Optional[torch.Tensor] = None,
+                              dgamma_q: Optional[torch.Tensor] = None,
+                              dgamma_k: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of qknorm_rope_axes; everything else as qknorm_rope_backward
+    (its workspace too)."""
+    return marshal().qknorm_rope_axes_backward(dyq, dyk, q, gamma_q, k, gamma_k, positions, table,
+                                               head_dim, eps, interleaved, out_dq, out_dk, dgamma_q,
+                                               dgamma_k, workspace, stream, axes)
+
+
 def rmsnorm_blockcast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
                       codes=None, scales=None, rinv=None, want_rinv: bool = False,
                       stream=None) -> BlockOut:
