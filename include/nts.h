@@ -481,6 +481,66 @@ NTS_API int nts_rmsnorm_blockcast(const void *X_dev, const float *gamma_dev, uin
                                   float eps, void *stream);
 
 /*
+ * nts_add_rmsnorm_blockcast -- nts_rmsnorm_blockcast of the sum of a layer's
+ * output and the residual stream, which is written too:
+ *
+ *     h_j  = round(x_j + r_j) to the stream's type
+ *     rinv = 1 / sqrt((1/D) sum_j h_j^2 + eps)                   (fp32)
+ *
+ * and w, scales and codes of h as there (the order of the sum may differ by
+ * fp32 roundings).  A row whose sum of squares is beyond fp32 gets rinv = 0.
+ *   X_dev          bf16 [T, D].      residual_dev  [T, D], bf16 or fp32
+ *                                    (residual_type, an nts_out_type).
+ *   gamma_dev      fp32 [D] or NULL.
+ *   H_dev          [T, D] in the stream's type; may be residual_dev, or X_dev
+ *                  when that is its type too; any other overlap is undefined.
+ *   codes_dev      uint8 [T, D].     scales_dev    fp32 [T, ceil(D/128)].
+ *   rinv_dev       fp32 [T] or NULL.
+ *   T >= 0; D a multiple of 16 up to 32768; eps > 0 and finite.
+ * Errors: as nts_rmsnorm_blockcast; INVALID_ARG also for another type.
+ */
+NTS_API int nts_add_rmsnorm_blockcast(const void *X_dev, const void *residual_dev,
+                                      const float *gamma_dev, void *H_dev, uint8_t *codes_dev,
+                                      float *scales_dev, float *rinv_dev, int residual_type,
+                                      int64_t T, int64_t D, float eps, void *stream);
+
+/*
+ * nts_add_rmsnorm_backward -- the gradient of nts_add_rmsnorm_blockcast, the
+ * cast taken as exact.  With dy the gradient of w, u_j = dy_j gamma_j and e the
+ * gradient of h from the layers behind:
+ *
+ *     dres_j   = rinv u_j - h_j rinv^3 (1/D) sum u h + e_j
+ *     dgamma_j = sum over the rows of dy_j h_j rinv              (fp32)
+ *
+ * dres is the gradient of x and of the residual alike.  The sums have a fixed
+ * order: equal calls give equal bits.
+ *   dY_dev         bf16 [T, D].      rinv_dev      fp32 [T], the forward pass's.
+ *   H_dev, dH_dev  [T, D] in the stream's type (residual_type); dH (e) or NULL.
+ *   gamma_dev      fp32 [D] or NULL.
+ *   dres_dev       [T, D] in the stream's type; may be dH_dev or H_dev, or
+ *                  dY_dev when that is its type too.
+ *   dX_dev         bf16 [T, D] or NULL: dres of an fp32 stream rounded once
+ *                  more, for the product behind; may be dY_dev.
+ *   dgamma_dev     fp32 [D], overwritten (zeros when T == 0), or NULL.
+ *   workspace_dev  with dgamma: scratch of at least
+ *                  nts_add_rmsnorm_backward_workspace() bytes, 16-byte aligned,
+ *                  contents arbitrary before and after; calls that overlap in
+ *                  time need one each.
+ *   T, D as above.
+ * Errors: INVALID_ARG (null required pointer, bad sizes or type, dX of a bf16
+ *         stream, dgamma without gamma, a missing or short workspace),
+ *         UNSUPPORTED (D % 16, D too wide, T >= 2^31, unaligned pointer), CUDA.
+ */
+NTS_API int nts_add_rmsnorm_backward(const void *dY_dev, const void *H_dev, const float *rinv_dev,
+                                     const float *gamma_dev, const void *dH_dev, void *dres_dev,
+                                     void *dX_dev, float *dgamma_dev, void *workspace_dev,
+                                     int64_t workspace_bytes, int residual_type, int64_t T,
+                                     int64_t D, void *stream);
+
+/* Workspace bytes of nts_add_rmsnorm_backward.  Errors: INVALID_ARG. */
+NTS_API int nts_add_rmsnorm_backward_workspace(int64_t D, int64_t *bytes_out);
+
+/*
  * nts_blockcast -- the cast of nts_rmsnorm_blockcast without the norm
  * (w = x), in blocks of block_rows x 128 values: 1 for activations and
  * gradients, 128 for weights.

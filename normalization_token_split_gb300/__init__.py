@@ -14,6 +14,8 @@ Around the QKV projection between the two:
 
 * ``rmsnorm_blockcast``, ``blockcast``, ``blockcast_t``  E4M3 casts with one
                       fp32 scale per 128 values;
+* ``add_rmsnorm_blockcast``, ``add_rmsnorm_backward``  the first of them with the
+                      residual's addition in front, and its gradient;
 * ``gemm_blockscaled``  the matrix product of such operands on the tensor
                       cores, from single tokens to training batches;
 * ``qknorm_rope``, ``qknorm_rope_backward``  headwise QK-RMSNorm of Q and K
@@ -31,7 +33,8 @@ from .ops import (FMT_E2M1, FMT_E4M3, FMT_NVFP4, MxOut, check_status, codes_row_
                   rmsnorm_mxcast, rmsnorm_mxcast_host, set_missing_tx, set_schedule, set_direct, set_tuning,
                   set_wait_limit_ns, check_nvfp4_scale, set_pdl, set_host_chunks,
                   check_e8m0, inject_failure,
-                  BlockOut, blockcast, blockcast_t, gemm_blockscaled, qknorm_rope,
+                  AddNormOut, BlockOut, add_rmsnorm_backward, add_rmsnorm_backward_workspace,
+                  add_rmsnorm_blockcast, blockcast, blockcast_t, gemm_blockscaled, qknorm_rope,
                   qknorm_rope_axes, qknorm_rope_axes_backward, qknorm_rope_backward,
                   rmsnorm_blockcast, rope_axes, rope_backward_workspace, rope_table)
 
@@ -42,5 +45,6 @@ __all__ = [
     "set_missing_tx", "set_schedule", "set_direct", "check_nvfp4_scale", "set_pdl", "set_host_chunks", "check_e8m0", "inject_failure",
     "BlockOut", "rmsnorm_blockcast", "blockcast", "blockcast_t", "gemm_blockscaled", "qknorm_rope",
     "qknorm_rope_backward", "rope_backward_workspace", "rope_table", "rope_axes", "qknorm_rope_axes",
-    "qknorm_rope_axes_backward",
+    "qknorm_rope_axes_backward", "AddNormOut", "add_rmsnorm_blockcast", "add_rmsnorm_backward",
+    "add_rmsnorm_backward_workspace",
 ]

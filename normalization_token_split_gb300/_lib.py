@@ -59,6 +59,9 @@ def _declare(lib):
                                            i64, i32, f32, P], i32),
         "nts_qknorm_rope_backward_workspace": ([i64, ctypes.POINTER(i64)], i32),
         "nts_rmsnorm_blockcast": ([P, P, P, P, P, i64, i64, f32, P], i32),
+        "nts_add_rmsnorm_blockcast": ([P, P, P, P, P, P, P, i32, i64, i64, f32, P], i32),
+        "nts_add_rmsnorm_backward": ([P, P, P, P, P, P, P, P, P, i64, i32, i64, i64, P], i32),
+        "nts_add_rmsnorm_backward_workspace": ([i64, ctypes.POINTER(i64)], i32),
         "nts_blockcast": ([P, P, P, i64, i64, i32, P], i32),
         "nts_blockcast_t": ([P, P, P, i64, i64, P], i32),
         "nts_gemm_blockscaled": ([P, P, P, P, i32, P, i32, i64, i64, i64, P], i32),

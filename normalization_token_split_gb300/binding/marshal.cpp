@@ -382,6 +382,93 @@ PyObject* rmsnorm_blockcast(PyObject* const* a) {
   return tuple_of(codes, scales, rinv);
 }
 
+// A residual stream's tensor: bf16 or fp32.
+const at::Tensor& stream_rows(const char* name, PyObject* o, int dev) {
+  const at::Tensor& t = tensor(name, o);
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+    refuse("%s must be torch.bfloat16 or torch.float32", name);
+  return matrix(name, flat(name, o, t.scalar_type(), dev));
+}
+
+const at::Tensor& same_shape(const char* name, const at::Tensor& t, const at::Tensor& like) {
+  if (t.sizes() != like.sizes()) refuse("%s has the wrong shape", name);
+  return t;
+}
+
+int stream_type(const at::Tensor& t) {
+  return t.scalar_type() == at::kFloat ? NTS_OUT_FP32 : NTS_OUT_BF16;
+}
+
+float* gain(PyObject* o, int64_t D, int dev) {
+  if (!given(o)) return nullptr;
+  const at::Tensor& g = flat("gamma", o, at::kFloat, dev);
+  if (g.numel() != D) refuse("%s must hold D values", "gamma");
+  return fptr(g);
+}
+
+// x, residual, gamma, eps, out, codes, scales, rinv, want_rinv, stream
+PyObject* add_rmsnorm_blockcast(PyObject* const* a) {
+  const int dev = device_of("x", tensor("x", a[0]));
+  const at::Tensor& x = matrix("x", flat("x", a[0], at::kBFloat16, dev));
+  const at::Tensor& r = same_shape("residual", stream_rows("residual", a[1], dev), x);
+  const int64_t T = x.size(0), D = x.size(1);
+  float* gamma = gain(a[2], D, dev);
+  const float eps = real(a[3]);
+  const On on(a[9], dev);
+  const at::Tensor h = output("out", a[4], {T, D}, r.scalar_type(), on);
+  const at::Tensor codes = output("codes", a[5], {T, D}, at::kByte, on);
+  const at::Tensor scales = output("scales", a[6], {T, blocks(D)}, at::kFloat, on);
+  at::Tensor rinv;
+  if (truth(a[8]) || given(a[7])) rinv = output("rinv", a[7], {T}, at::kFloat, on);
+  call([&] {
+    return nts_add_rmsnorm_blockcast(ptr(x), ptr(r), gamma, ptr(h),
+                                     static_cast<uint8_t*>(ptr(codes)), fptr(scales), fptr(rinv),
+                                     stream_type(r), T, D, eps, on.handle);
+  });
+  return tuple_of(h, codes, scales, rinv);
+}
+
+// dy, h, rinv, gamma, dres, out, out_x, dgamma, workspace, stream
+PyObject* add_rmsnorm_backward(PyObject* const* a) {
+  const int dev = device_of("dy", tensor("dy", a[0]));
+  const at::Tensor& dy = matrix("dy", flat("dy", a[0], at::kBFloat16, dev));
+  const at::Tensor& h = same_shape("h", stream_rows("h", a[1], dev), dy);
+  const int64_t T = dy.size(0), D = dy.size(1);
+  const at::Tensor& rinv = flat("rinv", a[2], at::kFloat, dev);
+  if (rinv.numel() != T) refuse("%s must hold a factor per row", "rinv");
+  float* gamma = gain(a[3], D, dev);
+  const at::ScalarType type = h.scalar_type();
+  const bool fp32 = type == at::kFloat;
+  void* behind = nullptr;
+  if (given(a[4])) behind = ptr(same_shape("dres", flat("dres", a[4], type, dev), dy));
+  const On on(a[9], dev);
+  const at::Tensor out = output("out", a[5], {T, D}, type, on);
+  at::Tensor dx, dgamma, ws;
+  if (fp32)
+    dx = output("out_x", a[6], {T, D}, at::kBFloat16, on);
+  else if (given(a[6]))
+    refuse("%s is the bf16 copy of an fp32 gradient; out is bfloat16 already", "out_x");
+  int64_t bytes = 0;
+  if (gamma != nullptr) {
+    dgamma = output("dgamma", a[7], {D}, at::kFloat, on);
+    if (given(a[8])) {
+      ws = flat("workspace", a[8], at::kByte, dev);
+      bytes = ws.numel();
+    } else {
+      call([&] { return nts_add_rmsnorm_backward_workspace(D, &bytes); });
+      if (on.foreign) refuse("a %s is needed on the per-thread stream", "workspace");
+      ws = scratch({bytes}, at::kByte, on);
+    }
+  } else if (given(a[7])) {
+    refuse("there is no gamma to form %s of", "dgamma");
+  }
+  call([&] {
+    return nts_add_rmsnorm_backward(ptr(dy), ptr(h), fptr(rinv), gamma, behind, ptr(out), ptr(dx),
+                                    fptr(dgamma), ptr(ws), bytes, stream_type(h), T, D, on.handle);
+  });
+  return tuple_of(out, dx, dgamma);
+}
+
 // x, block_rows, codes, scales, stream
 PyObject* blockcast(PyObject* const* a) {
   const int dev = device_of("x", tensor("x", a[0]));
@@ -484,6 +571,8 @@ PyMethodDef g_methods[] = {ENTRY(qknorm_rope, 15),
                            ENTRY(qknorm_rope_axes, 16),
                            ENTRY(qknorm_rope_axes_backward, 18),
                            ENTRY(rmsnorm_blockcast, 8),
+                           ENTRY(add_rmsnorm_blockcast, 10),
+                           ENTRY(add_rmsnorm_backward, 10),
                            ENTRY(blockcast, 5),
                            ENTRY(blockcast_t, 4),
                            ENTRY(gemm_blockscaled, 7),

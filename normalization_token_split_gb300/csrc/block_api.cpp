@@ -3,6 +3,7 @@
 // headwise QK-RMSNorm with rotation, and the rotation table on the host.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -115,6 +116,26 @@ int check_cast(const void* X, const uint8_t* codes, const float* scales, int64_t
     return fail(NTS_ERR_UNSUPPORTED, "T and D must stay below 2^31");
   if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4))
     return fail(NTS_ERR_UNSUPPORTED, "X and codes must be 16-byte aligned, scales 4-byte");
+  return NTS_OK;
+}
+
+int64_t norm_workspace(int64_t D) { return (int64_t)kNormPartials * D * (int64_t)sizeof(float); }
+
+// What the residual's addition and its gradient share: sizes, the stream's type and
+// two of its rows' operands.
+int check_addnorm(const char* name, const void* a, const void* r, const void* h, int type, int64_t T,
+                  int64_t D, const float* gamma) {
+  if (type != NTS_OUT_BF16 && type != NTS_OUT_FP32)
+    return fail(NTS_ERR_INVALID_ARG, "unknown type of the residual stream %d", type);
+  if (T < 0) return fail(NTS_ERR_INVALID_ARG, "T must be >= 0, got %lld", (long long)T);
+  if (D <= 0) return fail(NTS_ERR_INVALID_ARG, "D must be > 0, got %lld", (long long)D);
+  if (T > 0 && (a == nullptr || r == nullptr || h == nullptr))
+    return fail(NTS_ERR_INVALID_ARG, "%s must be non-NULL", name);
+  if (D % 16 != 0 || D > 32768)
+    return fail(NTS_ERR_UNSUPPORTED, "D (%lld) must be a multiple of 16 up to 32768", (long long)D);
+  if (T >= kMaxIndex) return fail(NTS_ERR_UNSUPPORTED, "T must stay below 2^31");
+  if (!aligned(a, 16) || !aligned(r, 16) || !aligned(h, 16) || !aligned(gamma, 16))
+    return fail(NTS_ERR_UNSUPPORTED, "%s and gamma must be 16-byte aligned", name);
   return NTS_OK;
 }
 
@@ -316,6 +337,83 @@ int nts_rmsnorm_blockcast(const void* X_dev, const float* gamma_dev, uint8_t* co
   if (T == 0) return NTS_OK;
   const BlockcastRequest rq{kCastNorm, X_dev, gamma_dev, codes_dev, scales_dev, rinv_dev, T, D, eps};
   return cast(rq, stream);
+}
+
+int nts_add_rmsnorm_blockcast(const void* X_dev, const void* residual_dev, const float* gamma_dev,
+                              void* H_dev, uint8_t* codes_dev, float* scales_dev, float* rinv_dev,
+                              int residual_type, int64_t T, int64_t D, float eps, void* stream) {
+  int rc = check_addnorm("X, residual and H", X_dev, residual_dev, H_dev, residual_type, T, D, gamma_dev);
+  if (rc == NTS_OK) rc = check_cast(H_dev, codes_dev, scales_dev, T, D);
+  if (rc == NTS_OK) rc = check_eps(eps);
+  if (rc != NTS_OK) return rc;
+  if (!aligned(rinv_dev, 4)) return fail(NTS_ERR_UNSUPPORTED, "rinv must be 4-byte aligned");
+  if (T == 0) return NTS_OK;
+  AddNormRequest rq = {};
+  rq.a = X_dev;
+  rq.r = residual_dev;
+  rq.gamma = gamma_dev;
+  rq.h = H_dev;
+  rq.codes = codes_dev;
+  rq.scales = scales_dev;
+  rq.rinv = rinv_dev;
+  rq.fp32 = residual_type == NTS_OUT_FP32;
+  rq.T = T;
+  rq.D = D;
+  rq.eps = eps;
+  return guarded(
+      [&] { return launch_addnorm(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
+}
+
+int nts_add_rmsnorm_backward_workspace(int64_t D, int64_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(NTS_ERR_INVALID_ARG, "bytes_out is NULL");
+  if (D <= 0) return fail(NTS_ERR_INVALID_ARG, "D must be > 0, got %lld", (long long)D);
+  *bytes_out = norm_workspace(std::min<int64_t>(D, 32768));
+  return NTS_OK;
+}
+
+int nts_add_rmsnorm_backward(const void* dY_dev, const void* H_dev, const float* rinv_dev,
+                             const float* gamma_dev, const void* dH_dev, void* dres_dev,
+                             void* dX_dev, float* dgamma_dev, void* workspace_dev,
+                             int64_t workspace_bytes, int residual_type, int64_t T, int64_t D,
+                             void* stream) {
+  int rc = check_addnorm("dY, H and dres", dY_dev, H_dev, dres_dev, residual_type, T, D, gamma_dev);
+  if (rc == NTS_OK) rc = check_vec("rinv", rinv_dev, T, 4);
+  if (rc != NTS_OK) return rc;
+  if (!aligned(dH_dev, 16) || !aligned(dX_dev, 16))
+    return fail(NTS_ERR_UNSUPPORTED, "dH and dX must be 16-byte aligned");
+  if (dX_dev != nullptr && residual_type != NTS_OUT_FP32)
+    return fail(NTS_ERR_INVALID_ARG, "dX is the bf16 copy of an fp32 dres; dres is bf16 already");
+  if (dgamma_dev != nullptr && gamma_dev == nullptr)
+    return fail(NTS_ERR_INVALID_ARG, "there is no gain to form dgamma of");
+  if (!aligned(dgamma_dev, 4)) return fail(NTS_ERR_UNSUPPORTED, "dgamma must be 4-byte aligned");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (dgamma_dev == nullptr) return NTS_OK;
+    const cudaError_t e = cudaMemsetAsync(dgamma_dev, 0, D * sizeof(float), s);
+    return e == cudaSuccess ? NTS_OK : fail_cuda(e, "clearing the gain's gradient");
+  }
+  if (dgamma_dev != nullptr) {
+    if (workspace_dev == nullptr || workspace_bytes < norm_workspace(D))
+      return fail(NTS_ERR_INVALID_ARG, "the workspace needs %lld bytes, got %lld",
+                  (long long)norm_workspace(D),
+                  (long long)(workspace_dev == nullptr ? 0 : workspace_bytes));
+    if (!aligned(workspace_dev, 16))
+      return fail(NTS_ERR_UNSUPPORTED, "the workspace must be 16-byte aligned");
+  }
+  AddNormRequest rq = {};
+  rq.a = dY_dev;
+  rq.r = H_dev;
+  rq.e = dH_dev;
+  rq.gamma = gamma_dev;
+  rq.h = dres_dev;
+  rq.dx = dX_dev;
+  rq.rinv_in = rinv_dev;
+  rq.dgamma = dgamma_dev;
+  rq.partial = static_cast<float*>(workspace_dev);
+  rq.fp32 = residual_type == NTS_OUT_FP32;
+  rq.T = T;
+  rq.D = D;
+  return guarded([&] { return launch_addnorm(rq, s, current_tuning()); });
 }
 
 int nts_blockcast(const void* X_dev, uint8_t* codes_dev, float* scales_dev, int64_t T, int64_t D,

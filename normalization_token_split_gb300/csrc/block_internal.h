@@ -59,6 +59,29 @@ struct BlockcastRequest {
 };
 int launch_blockcast(const BlockcastRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
 
+// The residual's addition with RMSNorm and the cast of kCastNorm, and its gradient
+// (rinv_in given), for a stream in bf16 or fp32 (addnorm_kernel.cu).
+struct AddNormRequest {
+  const void* a;          // x, or dy
+  const void* r;          // the residual, or h
+  const void* e;          // backward: the gradient from behind, nullable
+  const float* gamma;     // nullable
+  void* h;                // the sum, or dh
+  void* dx;               // backward, fp32 stream: dh in bf16, nullable
+  uint8_t* codes;
+  float* scales;
+  float* rinv;            // forward, nullable
+  const float* rinv_in;   // backward
+  float* dgamma;          // backward, with gamma
+  float* partial;         // backward, with gamma: the workspace
+  int fp32;
+  int64_t T, D;
+  float eps;
+};
+// Most rows of partial sums in the workspace of the gradient.
+constexpr int kNormPartials = 512;
+int launch_addnorm(const AddNormRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
+
 // Block-scaled product of E4M3 operands (gemm_kernel.cu).
 struct GemmRequest {
   const void* A;

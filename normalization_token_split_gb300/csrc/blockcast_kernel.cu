@@ -20,8 +20,8 @@
 
 #include <algorithm>
 
+#include "block_device.cuh"
 #include "block_internal.h"
-#include "nts_device.cuh"
 
 namespace nts {
 
@@ -38,49 +38,6 @@ constexpr int64_t kRingValues = 4 << 20, kNormRingValues = 3 << 20;
 
 // kStatusTimeout bits of these kernels.
 __device__ unsigned int g_cast_status;
-
-// fp32(max(a, 2^-100) / 448) by one multiply and two fmas (Brisebarre, Muller
-// and Raina, as div6_rn; the quotient is normal, and equal to the IEEE one for
-// every such a).  An infinite a stays infinite.
-__device__ __forceinline__ float block_scale(float a) {
-  a = fmaxf(a, 0x1p-100f);
-  const float z = 0x1.24924ap-9f;   // fl(1 / 448)
-  const float q = __fmul_rn(a, z);
-  const float s = __fmaf_rn(__fmaf_rn(-q, 448.0f, a), z, q);
-  return a <= 3.402823466e38f ? s : a;
-}
-
-// 16 bf16 (two 16-byte loads; p is 16-byte aligned).
-__device__ __forceinline__ void load16(uint4 (&v)[2], const __nv_bfloat16* p) {
-  v[0] = __ldcs(reinterpret_cast<const uint4*>(p));
-  v[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
-}
-
-__device__ __forceinline__ void unpack16(const uint4 (&v)[2], float (&f)[16]) {
-  float a[8], b[8];
-  bf16x8_to_f32(v[0], a);
-  bf16x8_to_f32(v[1], b);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    f[j] = a[j];
-    f[8 + j] = b[j];
-  }
-}
-
-__device__ __forceinline__ float absmax16(const float (&f)[16]) {
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; j += 2) m = fmax3(m, fabsf(f[j]), fabsf(f[j + 1]));
-  return m;
-}
-
-__device__ __forceinline__ uint4 codes16(const float (&f)[16], float inv) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = cvt_e4m3x4(f[4 * j] * inv, f[4 * j + 1] * inv, f[4 * j + 2] * inv, f[4 * j + 3] * inv);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 struct CastParams {
   const __nv_bfloat16* x;
@@ -205,10 +162,6 @@ __global__ void __launch_bounds__(kCastThreads) blockcast_rows_kernel(const Cast
 // from L1 ([8192, 5120] 26.8 us, 33.7 by four warps a row).
 constexpr int kStages = 2;
 constexpr int kPartUnits = 160, kHeldUnits = 128;
-
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 template <bool NORM, bool GAIN>
 __global__ void __launch_bounds__(kCastThreads, GAIN ? 2 : 3)

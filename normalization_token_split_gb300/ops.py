@@ -297,6 +297,13 @@ class BlockOut(NamedTuple):
     rinv: Optional[torch.Tensor]   # fp32 [T]
 
 
+class AddNormOut(NamedTuple):
+    h: torch.Tensor         # [T, D], the residual's type
+    codes: torch.Tensor     # uint8 [T, D]
+    scales: torch.Tensor    # fp32 [T, ceil(D/128)]
+    rinv: Optional[torch.Tensor]   # fp32 [T]
+
+
 # The checks, missing outputs and the call itself are in binding/marshal.cpp:
 # these operators serve single tokens, where Python's share of a call would be
 # the larger part of it.
@@ -413,6 +420,43 @@ def rmsnorm_blockcast(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps
     rinv or None)."""
     return BlockOut(*marshal().rmsnorm_blockcast(x, gamma, eps, codes, scales, rinv, want_rinv,
                                                  stream))
+
+
+def add_rmsnorm_blockcast(x: torch.Tensor, residual: torch.Tensor,
+                          gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          out: Optional[torch.Tensor] = None, codes=None, scales=None, rinv=None,
+                          want_rinv: bool = False, stream=None) -> AddNormOut:
+    """rmsnorm_blockcast of h = x + residual, both [T, D], x in bf16 and the
+    residual in bf16 or fp32, h in the residual's type and written too:
+    AddNormOut(h, codes [T, D], scales [T, ceil(D/128)], rinv or None).  out (h)
+    may be the residual, or x when that has its type."""
+    return AddNormOut(*marshal().add_rmsnorm_blockcast(x, residual, gamma, eps, out, codes, scales,
+                                                       rinv, want_rinv, stream))
+
+
+def add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rinv: torch.Tensor,
+                         gamma: Optional[torch.Tensor] = None,
+                         dres: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         out_x: Optional[torch.Tensor] = None,
+                         dgamma: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of add_rmsnorm_blockcast, the cast taken as exact: dy (bf16) is
+    the gradient of the normalized rows, h and rinv the forward pass's, dres the
+    gradient of h from the layers behind (h's type).  Returns (the gradient of
+    the residual and of x in h's type, the same in bf16 when h is fp32 or None,
+    gamma's gradient in fp32 [D] or None).  out may be dres or h, or dy when that
+    has its type; out_x may be dy.  Without a workspace (uint8,
+    add_rmsnorm_backward_workspace bytes) one is taken from torch's allocator for
+    the call."""
+    return marshal().add_rmsnorm_backward(dy, h, rinv, gamma, dres, out, out_x, dgamma, workspace,
+                                          stream)
+
+
+def add_rmsnorm_backward_workspace(D: int) -> int:
+    """Workspace bytes of add_rmsnorm_backward."""
+    n = ctypes.c_int64()
+    check(lib().nts_add_rmsnorm_backward_workspace(int(D), ctypes.byref(n)))
+    return n.value
 
 
 def blockcast(x: torch.Tensor, block_rows: int = 1, codes=None, scales=None,
