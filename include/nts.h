@@ -75,6 +75,13 @@ typedef enum {
     NTS_OUT_FP32 = 1
 } nts_out_type;
 
+/* Codes of 4-bit weights, two to a byte, the even one's in bits 0 to 3: E2M1, or
+   two's complement. */
+typedef enum {
+    NTS_W4_E2M1 = 0,
+    NTS_W4_INT4 = 1
+} nts_w4_fmt;
+
 /* Library version, major*10000 + minor*100 + patch. */
 NTS_API int nts_version(void);
 
@@ -598,6 +605,56 @@ NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scal
                                  const uint8_t *W_codes_dev, const float *w_scales_dev,
                                  int w_block_rows, void *Y_dev, int out_type, int64_t M,
                                  int64_t N, int64_t K, void *stream);
+
+/*
+ * nts_gemv_groupscaled -- product of few rows with weights of 4 bits, which
+ * carry a bf16 scale per group of 32, 64 or 128 values along K (the last group
+ * of a row may be shorter):
+ *
+ *     Y[m][n] = sum_g w_scales[n][g] sum_{k in group g} A[m][k] W[n][k]
+ *
+ * Sums in fp32, one rounding to the output type.  Up to 32 rows are one pass
+ * over the weights (16 with a K above 16384); more rows are passes of up to as
+ * many, and from about 64 on nts_gemm_blockscaled is the faster product.
+ *   A_dev         with a_scales NULL: bf16, row m at m*lda elements, a value that
+ *                 is below 2^-31 of the largest of its 128 neighbours along K
+ *                 off by up to 2^-39 of that one; otherwise E4M3 codes (uint8)
+ *                 with one fp32 scale per 128 values, as nts_gemm_blockscaled
+ *                 takes them.
+ *   a_scales_dev  fp32 [M, ceil(K/128)] or NULL.
+ *   W_codes_dev   uint8 [N, K/2] (fmt, an nts_w4_fmt).
+ *   w_scales_dev  bf16 [N, ceil(K/group)].
+ *   Y_dev         bf16 or fp32 [M, N] (out_type, an nts_out_type), written;
+ *                 overlaps no operand.
+ *   M >= 0; N > 0; K a positive multiple of 32 up to 32768; lda >= K, a multiple
+ *   of 16 bytes.
+ * The order of the sums depends on the shape alone: equal calls give equal
+ * bits.
+ * Errors: INVALID_ARG (null pointer, bad sizes, group, fmt or out_type, a stride
+ *         below the row), UNSUPPORTED (K % 32, K too long, unaligned rows,
+ *         codes, scales or Y, M above 65535 * 16, N from 2^31 - 256), CUDA.
+ */
+NTS_API int nts_gemv_groupscaled(const void *A_dev, int64_t lda, const float *a_scales_dev,
+                                 const uint8_t *W_codes_dev, const void *w_scales_dev, int group,
+                                 int fmt, void *Y_dev, int out_type, int64_t M, int64_t N,
+                                 int64_t K, void *stream);
+
+/*
+ * nts_groupcast_host -- weights [N, K] to the operand of nts_gemv_groupscaled,
+ * on the host:
+ *
+ *     scale = bf16(fp32(max(absmax of the group, 2^-100) / top)),
+ *             top = 6 (E2M1) or 7 (int4)
+ *     code  = the value nearest to fp32(w / scale), ties to the even code,
+ *             saturating (int4: -7 to 7)
+ *
+ *   W_host       bf16 [N, K], finite.   codes_host   uint8 [N, K/2], written.
+ *   scales_host  bf16 [N, ceil(K/group)], written.
+ * Errors: INVALID_ARG (null pointer, bad sizes, group or fmt, a weight that is
+ *         not finite), UNSUPPORTED (K % 32).
+ */
+NTS_API int nts_groupcast_host(const void *W_host, uint8_t *codes_host, void *scales_host,
+                               int64_t N, int64_t K, int group, int fmt);
 
 /*
  * nts_check_status -- synchronizes `stream`, then reads and clears the

@@ -18,6 +18,8 @@ Around the QKV projection between the two:
                       residual's addition in front, and its gradient;
 * ``gemm_blockscaled``  the matrix product of such operands on the tensor
                       cores, from single tokens to training batches;
+* ``gemv_groupscaled``, ``groupcast``  products of few rows with weights of 4 bits
+                      and a scale per group, and the cast of the weights;
 * ``qknorm_rope``, ``qknorm_rope_backward``  headwise QK-RMSNorm of Q and K
                       with the rotary position embedding, and its gradient;
 * ``qknorm_rope_axes``, ``qknorm_rope_axes_backward``  the same with a position
@@ -33,8 +35,8 @@ from .ops import (FMT_E2M1, FMT_E4M3, FMT_NVFP4, MxOut, check_status, codes_row_
                   rmsnorm_mxcast, rmsnorm_mxcast_host, set_missing_tx, set_schedule, set_direct, set_tuning,
                   set_wait_limit_ns, check_nvfp4_scale, set_pdl, set_host_chunks,
                   check_e8m0, inject_failure,
-                  AddNormOut, BlockOut, add_rmsnorm_backward, add_rmsnorm_backward_workspace,
-                  add_rmsnorm_blockcast, blockcast, blockcast_t, gemm_blockscaled, qknorm_rope,
+                  AddNormOut, BlockOut, GroupOut, add_rmsnorm_backward, add_rmsnorm_backward_workspace,
+                  add_rmsnorm_blockcast, blockcast, blockcast_t, gemm_blockscaled, gemv_groupscaled, groupcast, qknorm_rope,
                   qknorm_rope_axes, qknorm_rope_axes_backward, qknorm_rope_backward,
                   rmsnorm_blockcast, rope_axes, rope_backward_workspace, rope_table)
 
@@ -46,5 +48,5 @@ __all__ = [
     "BlockOut", "rmsnorm_blockcast", "blockcast", "blockcast_t", "gemm_blockscaled", "qknorm_rope",
     "qknorm_rope_backward", "rope_backward_workspace", "rope_table", "rope_axes", "qknorm_rope_axes",
     "qknorm_rope_axes_backward", "AddNormOut", "add_rmsnorm_blockcast", "add_rmsnorm_backward",
-    "add_rmsnorm_backward_workspace",
+    "add_rmsnorm_backward_workspace", "GroupOut", "groupcast", "gemv_groupscaled",
 ]

@@ -65,6 +65,8 @@ def _declare(lib):
         "nts_blockcast": ([P, P, P, i64, i64, i32, P], i32),
         "nts_blockcast_t": ([P, P, P, i64, i64, P], i32),
         "nts_gemm_blockscaled": ([P, P, P, P, i32, P, i32, i64, i64, i64, P], i32),
+        "nts_gemv_groupscaled": ([P, i64, P, P, P, i32, i32, P, i32, i64, i64, i64, P], i32),
+        "nts_groupcast_host": ([P, P, P, i64, i64, i32, i32], i32),
         "nts_mxnorm_correction": ([i32, i32, ctypes.POINTER(ctypes.c_double)], i32),
         "nts_check_status": ([P], i32),
         "nts_qknorm_rms_host": ([P, P, P, P, P, P, P, i64, i64, f32, i32, P], i32),

@@ -540,6 +540,49 @@ PyObject* gemm_blockscaled(PyObject* const* a) {
   return wrap(y);
 }
 
+// a, w_codes, w_scales, a_scales, group, int4, out, fp32 (when there is no out), stream
+PyObject* gemv_groupscaled(PyObject* const* a) {
+  const int dev = device_of("a", tensor("a", a[0]));
+  const bool coded = given(a[3]);
+  Rows x;
+  float* sx = nullptr;
+  if (coded) {
+    const at::Tensor& t = operand("a", a[0], dev);
+    x = {t, t.size(1)};
+  } else {
+    x = rows("a", a[0], dev);
+  }
+  const int64_t M = x.t.size(0), K = x.t.size(1), group = integer(a[4]);
+  if (group != 32 && group != 64 && group != 128) refuse("%s must be 32, 64 or 128", "group");
+  if (coded) {
+    const at::Tensor& s = flat("a_scales", a[3], at::kFloat, dev);
+    if (s.sizes() != at::IntArrayRef({M, blocks(K)}))
+      refuse("%s must have shape [M, ceil(K/128)]", "a_scales");
+    sx = fptr(s);
+  }
+  const at::Tensor& w = matrix("w_codes", flat("w_codes", a[1], at::kByte, dev));
+  const int64_t N = w.size(0);
+  if (2 * w.size(1) != K) refuse("%s must hold K/2 bytes a row", "w_codes");
+  const at::Tensor& sw = flat("w_scales", a[2], at::kBFloat16, dev);
+  if (sw.sizes() != at::IntArrayRef({N, blocks(K, group)}))
+    refuse("%s must have shape [N, ceil(K/group)]", "w_scales");
+  const int fmt = truth(a[5]) ? NTS_W4_INT4 : NTS_W4_E2M1;
+  bool fp32 = truth(a[7]);
+  if (given(a[6])) {
+    const at::ScalarType t = tensor("out", a[6]).scalar_type();
+    if (t != at::kFloat && t != at::kBFloat16) refuse("%s must be bfloat16 or float32", "out");
+    fp32 = t == at::kFloat;
+  }
+  const On on(a[8], dev);
+  const at::Tensor y = output("out", a[6], {M, N}, fp32 ? at::kFloat : at::kBFloat16, on);
+  call([&] {
+    return nts_gemv_groupscaled(ptr(x.t), x.ld, sx, static_cast<uint8_t*>(ptr(w)), ptr(sw),
+                                (int)group, fmt, ptr(y), fp32 ? NTS_OUT_FP32 : NTS_OUT_BF16, M, N, K,
+                                on.handle);
+  });
+  return wrap(y);
+}
+
 // ------------------------------------------------------------- the module
 
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -576,6 +619,7 @@ PyMethodDef g_methods[] = {ENTRY(qknorm_rope, 15),
                            ENTRY(blockcast, 5),
                            ENTRY(blockcast_t, 4),
                            ENTRY(gemm_blockscaled, 7),
+                           ENTRY(gemv_groupscaled, 9),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 

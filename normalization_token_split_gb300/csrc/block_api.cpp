@@ -7,6 +7,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <exception>
 #include <new>
 
@@ -137,6 +138,30 @@ int check_addnorm(const char* name, const void* a, const void* r, const void* h,
   if (!aligned(a, 16) || !aligned(r, 16) || !aligned(h, 16) || !aligned(gamma, 16))
     return fail(NTS_ERR_UNSUPPORTED, "%s and gamma must be 16-byte aligned", name);
   return NTS_OK;
+}
+
+// Sizes and format of 4-bit weights.
+int check_group(int64_t N, int64_t K, int group, int fmt) {
+  if (fmt != NTS_W4_E2M1 && fmt != NTS_W4_INT4)
+    return fail(NTS_ERR_INVALID_ARG, "unknown format of 4-bit weights %d", fmt);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(NTS_ERR_INVALID_ARG, "a group has 32, 64 or 128 weights, got %d", group);
+  if (N <= 0 || K <= 0)
+    return fail(NTS_ERR_INVALID_ARG, "N and K must be > 0, got %lld and %lld", (long long)N,
+                (long long)K);
+  if (K % 32 != 0)
+    return fail(NTS_ERR_UNSUPPORTED, "K (%lld) must be a multiple of 32", (long long)K);
+  return NTS_OK;
+}
+
+// The 4-bit code nearest to v, ties to the even code, saturating.
+unsigned code4(float v, int fmt) {
+  if (fmt == NTS_W4_INT4) return (unsigned)(int)std::nearbyint(std::max(-7.f, std::min(7.f, v))) & 15u;
+  static const float middle[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
+  const float a = std::fabs(v);
+  unsigned code = 0;
+  while (code < 7 && (a > middle[code] || (a == middle[code] && code % 2 == 1))) ++code;
+  return code | (v < 0 && code != 0 ? 8u : 0u);
 }
 
 // Runs a launch; what it throws (the host out of memory, a lock that fails) ends
@@ -465,6 +490,69 @@ int nts_gemm_blockscaled(const uint8_t* A_codes_dev, const float* a_scales_dev,
                        out_type == NTS_OUT_FP32, M, N, K};
   return guarded(
       [&] { return launch_gemm(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
+}
+
+int nts_groupcast_host(const void* W_host, uint8_t* codes_host, void* scales_host, int64_t N,
+                       int64_t K, int group, int fmt) {
+  int rc = check_group(N, K, group, fmt);
+  if (rc != NTS_OK) return rc;
+  if (W_host == nullptr || codes_host == nullptr || scales_host == nullptr)
+    return fail(NTS_ERR_INVALID_ARG, "W, codes and scales must be non-NULL");
+  const uint16_t* w = static_cast<const uint16_t*>(W_host);
+  uint16_t* scales = static_cast<uint16_t*>(scales_host);
+  const int64_t groups = (K + group - 1) / group;
+  const auto value = [](uint16_t bits) {
+    const uint32_t u = (uint32_t)bits << 16;
+    float f;
+    std::memcpy(&f, &u, sizeof(f));
+    return f;
+  };
+  for (int64_t i = 0; i < N * K; ++i)
+    if ((w[i] & 0x7F80) == 0x7F80)
+      return fail(NTS_ERR_INVALID_ARG, "weight %lld is not finite", (long long)i);
+  const float top = fmt == NTS_W4_E2M1 ? 6.f : 7.f;
+  for (int64_t n = 0; n < N; ++n)
+    for (int64_t g = 0; g < groups; ++g) {
+      const int64_t begin = n * K + g * group, end = std::min(begin + group, (n + 1) * K);
+      float most = 0x1p-100f;
+      for (int64_t i = begin; i < end; ++i) most = std::max(most, std::fabs(value(w[i])));
+      const float scale = most / top;
+      uint32_t bits;
+      std::memcpy(&bits, &scale, sizeof(bits));
+      scales[n * groups + g] = (uint16_t)((bits + 0x7FFF + (bits >> 16 & 1)) >> 16);
+      const float s = value(scales[n * groups + g]);
+      for (int64_t i = begin; i < end; i += 2)
+        codes_host[i / 2] = (uint8_t)(code4(value(w[i]) / s, fmt) | code4(value(w[i + 1]) / s, fmt) << 4);
+    }
+  return NTS_OK;
+}
+
+int nts_gemv_groupscaled(const void* A_dev, int64_t lda, const float* a_scales_dev,
+                         const uint8_t* W_codes_dev, const void* w_scales_dev, int group, int fmt,
+                         void* Y_dev, int out_type, int64_t M, int64_t N, int64_t K, void* stream) {
+  if (out_type != NTS_OUT_BF16 && out_type != NTS_OUT_FP32)
+    return fail(NTS_ERR_INVALID_ARG, "unknown output type %d", out_type);
+  if (M < 0) return fail(NTS_ERR_INVALID_ARG, "M must be >= 0, got %lld", (long long)M);
+  int rc = check_group(N, K, group, fmt);
+  if (rc != NTS_OK) return rc;
+  if (lda < K)
+    return fail(NTS_ERR_INVALID_ARG, "A: row stride %lld below the row's %lld values", (long long)lda,
+                (long long)K);
+  if (M > 0 && (A_dev == nullptr || W_codes_dev == nullptr || w_scales_dev == nullptr ||
+                Y_dev == nullptr))
+    return fail(NTS_ERR_INVALID_ARG, "operands, scales and Y must be non-NULL");
+  if (M > 65535 * 16ll || N >= kMaxIndex - 256)
+    return fail(NTS_ERR_UNSUPPORTED, "M must be at most 65535 * 16, N below 2^31 - 256");
+  if (K > 32768) return fail(NTS_ERR_UNSUPPORTED, "K (%lld) exceeds 32768", (long long)K);
+  if (!aligned(A_dev, 16) || !aligned(W_codes_dev, 16) || !aligned(w_scales_dev, 16) ||
+      !aligned(Y_dev, 16) || !aligned(a_scales_dev, 4) || lda % (a_scales_dev != nullptr ? 16 : 8) != 0)
+    return fail(NTS_ERR_UNSUPPORTED,
+                "A's rows, codes, group scales and Y must be 16-byte aligned, a_scales 4-byte");
+  if (M == 0) return NTS_OK;
+  const GemvRequest rq{A_dev, a_scales_dev, lda, W_codes_dev, w_scales_dev, fmt == NTS_W4_INT4, group,
+                       Y_dev, out_type == NTS_OUT_FP32, M, N, K};
+  return guarded(
+      [&] { return launch_gemv(rq, static_cast<cudaStream_t>(stream), current_tuning()); });
 }
 
 }  // extern "C"

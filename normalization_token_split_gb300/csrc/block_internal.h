@@ -95,6 +95,21 @@ struct GemmRequest {
 };
 int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
 
+// Product of few rows with 4-bit weights (gemv_kernel.cu).
+struct GemvRequest {
+  const void* A;          // bf16, or E4M3 codes where a_scales is given
+  const float* a_scales;
+  int64_t lda;
+  const void* W;
+  const void* w_scales;
+  int int4;               // codes are int4, not E2M1
+  int group;
+  void* Y;
+  int fp32_out;
+  int64_t M, N, K;
+};
+int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
+
 // The operators around a projection whose kernels this process has launched or
 // captured: nts_check_status reads the status words of those alone (a blocking
 // copy of ~13 us each), so the other operators' users do not pay for them.

@@ -297,6 +297,11 @@ class BlockOut(NamedTuple):
     rinv: Optional[torch.Tensor]   # fp32 [T]
 
 
+class GroupOut(NamedTuple):
+    codes: torch.Tensor     # uint8 [N, K/2], the even value's code in bits 0 to 3
+    scales: torch.Tensor    # bf16 [N, ceil(K/group)]
+
+
 class AddNormOut(NamedTuple):
     h: torch.Tensor         # [T, D], the residual's type
     codes: torch.Tensor     # uint8 [T, D]
@@ -484,6 +489,46 @@ def gemm_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: tor
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
     return marshal().gemm_blockscaled(a_codes, a_scales, w_codes, w_scales, out,
+                                      out_dtype is torch.float32, stream)
+
+
+_W4_NAMES = {"e2m1": 0, "int4": 1}
+
+
+def _w4(fmt) -> int:
+    try:
+        return _W4_NAMES[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"4-bit weights are 'e2m1' or 'int4', got {fmt!r}") from None
+
+
+def groupcast(w: torch.Tensor, group: int = 32, fmt="e2m1", device="cuda") -> GroupOut:
+    """Weights w [N, K] (bf16, finite) as 4-bit codes with a bf16 scale per group
+    of 32, 64 or 128 values along K, formed on the host:
+    GroupOut(codes uint8 [N, K/2], scales [N, ceil(K/group)])."""
+    if w.dtype != torch.bfloat16 or w.dim() != 2:
+        raise ValueError("w must be a matrix of torch.bfloat16")
+    N, K = w.shape
+    w = w.detach().to("cpu").contiguous()
+    f, g = _w4(fmt), int(group)
+    codes = torch.empty(N, K // 2, dtype=torch.uint8)
+    scales = torch.empty(N, -(-K // g) if g > 0 else 0, dtype=torch.bfloat16)
+    check(lib().nts_groupcast_host(_ptr(w), _ptr(codes), _ptr(scales), N, K, g, f))
+    return GroupOut(codes.to(device), scales.to(device))
+
+
+def gemv_groupscaled(a: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                     a_scales: Optional[torch.Tensor] = None, group: int = 32, fmt="e2m1",
+                     out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                     stream=None) -> torch.Tensor:
+    """Y = A W^T of few rows with 4-bit weights (groupcast): w_codes uint8
+    [N, K/2] with w_scales bf16 [N, ceil(K/group)], fmt "e2m1" or "int4".  a [M, K]
+    is bf16 (contiguous rows, any row stride), or E4M3 codes (uint8 or
+    float8_e4m3fn) with a_scales fp32 [M, ceil(K/128)] (a BlockOut's).  Returns
+    Y [M, N], bf16 or fp32 (out_dtype, or out's)."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
+    return marshal().gemv_groupscaled(a, w_codes, w_scales, a_scales, group, _w4(fmt), out,
                                       out_dtype is torch.float32, stream)
 
 
