@@ -95,7 +95,7 @@ struct GemmRequest {
 };
 int launch_gemm(const GemmRequest& rq, cudaStream_t stream, const LaunchTuning& tune);
 
-// Product of few rows with 4-bit weights (gemv_kernel.cu).
+// Product of few rows with 4-bit weights (gemv_launch.cu).
 struct GemvRequest {
   const void* A;          // bf16, or E4M3 codes where a_scales is given
   const float* a_scales;

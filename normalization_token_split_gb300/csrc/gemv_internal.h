@@ -1,0 +1,58 @@
+// gemv_internal.h -- what the launcher of the products with 4-bit weights and its kernels
+// share.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace nts {
+
+constexpr int kMaxGemvWarps = 16;
+constexpr int kGemvRows = 16;      // weight rows of a tile
+constexpr int kRedPitch = 20;      // floats per row of A in a tile's sums: distinct banks
+
+#ifdef __CUDACC__
+#define NTS_GEMV_RULE __host__ __device__ constexpr
+#else
+#define NTS_GEMV_RULE constexpr
+#endif
+// k values of a warp's chunk (its part of A fills 64 registers at most), and the ring's
+// stages, for rows of A in E4M3 or bf16 and NT tiles of 8 of them.
+NTS_GEMV_RULE int chunk_of(bool e4m3, int nt) { return e4m3 || nt <= 2 ? 256 : 128; }
+NTS_GEMV_RULE int stages_of(bool e4m3, int nt) {
+  return chunk_of(e4m3, nt) == 128 ? 6 : nt == 4 ? 3 : 4;
+}
+
+struct GemvParams {
+  const void* a;
+  const float* a_scales;     // E4M3 rows
+  int64_t lda;
+  const uint8_t* w;
+  const __nv_bfloat16* s;
+  void* y;
+  int M, N, K;
+  int groups;                // scales of a weight row
+  int kb;                    // a_scales per row
+  int chunks;                // chunks of K
+  int warps;                 // per CTA
+  int cluster;               // CTAs along K
+  int slices;                // row slices (clusters along N)
+  int per;                   // rows of A per slice of M (blockIdx.y)
+  int vector;                // a chunk's scales of a row are one aligned copy
+  int scale_pitch;           // bytes of a row's scales in a stage
+  int stage_bytes;           // a multiple of 128
+  int fp32;
+};
+
+using GemvKernel = void (*)(GemvParams);
+
+// The kernel for a group size and a number of tiles of 8 rows (gemv_*.cu).
+template <bool E4M3, bool INT4>
+GemvKernel pick_gemv(int group, int nt);
+extern template GemvKernel pick_gemv<false, false>(int, int);
+extern template GemvKernel pick_gemv<false, true>(int, int);
+extern template GemvKernel pick_gemv<true, false>(int, int);
+extern template GemvKernel pick_gemv<true, true>(int, int);
+
+}  // namespace nts

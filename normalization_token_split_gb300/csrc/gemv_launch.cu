@@ -1,0 +1,132 @@
+// gemv_launch.cu -- products of few rows with weights of 4 bits that carry a bf16 scale
+// per group of 32, 64 or 128 values along K, on one GB300.
+//
+//     Y[m][n] = sum_g s[n][g] sum_{k in g} A[m][k] c[n][k],
+//
+// c the E2M1 or int4 value of a code, A in bf16, or E4M3 codes with an fp32 scale per 128
+// values (the operand of nts_gemm_blockscaled).
+//
+// GB300 mapping: with few rows the weights' bytes are the whole cost (0.5 a weight, and
+// 2 per group), so they go through once, at HBM's rate, and everything else has to fit
+// beside them: about six issue slots for the two weights of a lane.  The products run on
+// mma.sync (m16n8k16, fp16 in, fp32 sums), 16 weight rows against 8 rows of A at a time:
+// a fifth of the tensor instructions' rate is enough, and their operands come from
+// registers, where the codes are turned into fp16 (exactly).  A's rows are the narrow
+// operand, so 1 to 8 of them cost the same.
+// A warp owns a chunk of K: its part of A stays in registers as B fragments for the
+// whole call, and it streams its chunk of one tile of 16 weight rows after the other
+// through its own ring of shared memory (cp.async, no barrier and no other warp's copies
+// to wait for).  The codes of a group lie in the four lanes of a quad, four bytes each,
+// so a group's products end in one fragment, which the group's scale multiplies in fp32.
+// A tile's sums over the warps' chunks meet in shared memory, in a fixed order; a longer
+// K is split over the CTAs of a cluster, whose sums meet once at the end.
+// A's values become fp16 without loss where it matters: E4M3 codes exactly; bf16 rows by
+// a power of two per 128 values that puts the largest near 2^14, so a value is exact
+// unless it is below 2^-31 of the largest beside it, and then off by at most 2^-39 of it,
+// under the fp32 sums' own roundings.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "block_internal.h"
+#include "gemv_internal.h"
+
+namespace nts {
+
+int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& tune) {
+  if (const int injected = take_injected_failure()) return injected;
+  const DeviceInfo& dev = device_info();
+  if (!dev.ok) return fail(NTS_ERR_CUDA, "could not query the current device");
+  GemvParams p = {};
+  p.a = rq.A;
+  p.a_scales = rq.a_scales;
+  p.lda = rq.lda;
+  p.w = static_cast<const uint8_t*>(rq.W);
+  p.s = static_cast<const __nv_bfloat16*>(rq.w_scales);
+  p.y = rq.Y;
+  p.M = (int)rq.M;
+  p.N = (int)rq.N;
+  p.K = (int)rq.K;
+  p.groups = (p.K + rq.group - 1) / rq.group;
+  p.kb = (p.K + 127) / 128;
+  p.fp32 = rq.fp32_out;
+  const bool e4m3 = rq.a_scales != nullptr;
+  // slices of A's rows, in even parts; a chunk is half as long from 17 rows on, and a
+  // cluster holds 128 chunks
+  const int slices_m = (p.M + 31) / 32 * (!e4m3 && p.M > 16 && p.K > 16384 ? 2 : 1);
+  p.per = ((p.M + slices_m - 1) / slices_m + 7) / 8 * 8;
+  const int nt = p.per <= 8 ? 1 : p.per <= 16 ? 2 : 4;
+  p.per = 8 * nt;
+  const int chunk = chunk_of(e4m3, nt), stages = stages_of(e4m3, nt);
+  p.chunks = (p.K + chunk - 1) / chunk;
+  p.cluster = (p.chunks + kMaxGemvWarps - 1) / kMaxGemvWarps;
+  p.warps = (p.chunks + p.cluster - 1) / p.cluster;
+  const int per_row = chunk / rq.group;
+  p.vector = per_row >= 2 && p.groups % per_row == 0;
+  p.scale_pitch = p.vector ? 2 * per_row : (2 * per_row + 2 + 3) / 4 * 4;
+  p.stage_bytes = (kGemvRows * (chunk / 2 + p.scale_pitch) + 127) / 128 * 128;
+  const GemvKernel kern = e4m3 ? (rq.int4 ? pick_gemv<true, true> : pick_gemv<true, false>)(rq.group, nt)
+                               : (rq.int4 ? pick_gemv<false, true> : pick_gemv<false, false>)(rq.group, nt);
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3((unsigned)(32 * p.warps));
+  const size_t base =
+      (size_t)p.warps * (stages * p.stage_bytes +
+                         (2 * kRedPitch + (e4m3 && rq.int4 ? per_row : 0)) * 8 * nt * sizeof(float));
+  // slices: what the GPU holds at once; the sums of a slice across a cluster take
+  // shared memory, so a long N takes more slices than that
+  const size_t limit = (size_t)dev.max_smem_optin;
+  int64_t fit = 0;
+  cfg.dynamicSmemBytes = base;
+  int rc = prepare_kernel((const void*)kern, p.cluster > 1 ? limit : base);
+  if (rc != NTS_OK) return rc;
+  if (p.cluster == 1) {
+    int per_sm = 0;
+    rc = blocks_per_sm((const void*)kern, cfg.blockDim.x, base, &per_sm);
+    fit = (int64_t)dev.sm_count * per_sm;
+  } else {
+    // asked with a size of shared memory that names the cluster too: the answers are
+    // kept by kernel, threads and size
+    cudaLaunchAttribute size;
+    size.id = cudaLaunchAttributeClusterDimension;
+    size.val.clusterDim.x = p.cluster;
+    size.val.clusterDim.y = size.val.clusterDim.z = 1;
+    cfg.attrs = &size;
+    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = limit - 16 * p.cluster;
+    rc = max_active_clusters((const void*)kern, cfg, p.cluster, &fit);
+    cfg.dynamicSmemBytes = base;
+  }
+  if (rc != NTS_OK) return rc;
+  p.slices = (int)std::min<int64_t>(std::max<int64_t>(1, fit / slices_m), p.N);
+  if (p.cluster > 1) {
+    const int row = 8 * nt * (int)sizeof(float);
+    const int most = (int)((limit - base) / row) / kGemvRows * kGemvRows;   // rows of a slice
+    p.slices = std::max(p.slices, (p.N + most - 1) / most);
+    while ((p.N + p.slices - 1) / p.slices > most) ++p.slices;
+    const int rows = (p.N + p.slices - 1) / p.slices;
+    cfg.dynamicSmemBytes = base + (size_t)((rows + kGemvRows - 1) / kGemvRows * kGemvRows) * row;
+  }
+  cfg.gridDim = dim3((unsigned)(p.slices * p.cluster), (unsigned)slices_m);
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (p.cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = p.cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (tune.pdl) attr[n++] = pdl_attribute();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  log_launch("gemv_groupscaled",
+             "M=%d N=%d K=%d group=%d int4=%d tiles of 8=%d warps=%d cluster=%d slices=%d smem=%zu",
+             p.M, p.N, p.K, rq.group, rq.int4, nt, p.warps, p.cluster, p.slices,
+             cfg.dynamicSmemBytes);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return fail_cuda(e, "launching the product with 4-bit weights");
+  return NTS_OK;
+}
+
+}  // namespace nts
