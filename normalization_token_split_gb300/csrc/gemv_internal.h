@@ -10,7 +10,6 @@ namespace nts {
 
 constexpr int kMaxGemvWarps = 16;
 constexpr int kGemvRows = 16;      // weight rows of a tile
-constexpr int kRedPitch = 20;      // floats per row of A in a tile's sums: distinct banks
 
 #ifdef __CUDACC__
 #define NTS_GEMV_RULE __host__ __device__ constexpr
@@ -43,6 +42,7 @@ struct GemvParams {
   int scale_pitch;           // bytes of a row's scales in a stage
   int stage_bytes;           // a multiple of 128
   int fp32;
+  int batch;                 // tiles whose sums the warps keep between two barriers
 };
 
 using GemvKernel = void (*)(GemvParams);

@@ -56,6 +56,15 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&p)[E4M3 ? 2 : 4])
   }
 }
 
+// Four 8 x 16-byte matrices, one 4-byte word of row g of each per lane (g, t); lanes
+// 8 i .. 8 i + 7 give the rows' addresses of matrix i.
+__device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // d = A B + c: rows g and g + 8 of A by lanes (g, t), column g of B.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
@@ -96,25 +105,26 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
                                           float (&factor)[chunk_of(false, NT) / 128][NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int end = min(p.M, m0 + p.per);
+  // every load is issued before the first is used
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int m = m0 + 8 * j + g;
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < chunk_of(false, NT) / 32; ++i) {
+      const int m = m0 + 8 * j + g, k = k0 + 32 * i;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (m < end && k < p.K)
+        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a) +
+                                                 m * p.lda + k + 8 * t));
+      frag[i][j][0] = x.x, frag[i][j][1] = x.y, frag[i][j][2] = x.z, frag[i][j][3] = x.w;
+    }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int b = 0; b < chunk_of(false, NT) / 128; ++b) {
-      uint4 x[4];
-      float most = 0.f;
+      uint32_t most2 = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + 128 * b + 32 * i;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (m < end && k < p.K)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a) +
-                                                      m * p.lda + k + 8 * t));
-        float v[8];
-        bf16x8_to_f32(x[i], v);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) most = fmax3(most, fabsf(v[e]), fabsf(v[e + 1]));
-      }
+      for (int i = 0; i < 16; ++i) most2 = bf16x2_absmax(most2, frag[4 * b + i / 4][j][i % 4]);
+      float most = bf16x2_hmax_abs(most2);
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
       // 2^f: the largest comes to [2^14, 2^15), as far as 2^f and 2^-f are normal
@@ -123,9 +133,9 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
       const float down = __uint_as_float((uint32_t)(127 - f) << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v[8];
-        bf16x8_to_f32(x[i], v);
         uint32_t(&q)[4] = frag[4 * b + i][j];
+        float v[8];
+        bf16x8_to_f32(make_uint4(q[0], q[1], q[2], q[3]), v);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           q[e] = INT4 ? pack_f16x2(v[e] * up, v[e + 4] * up)
@@ -135,7 +145,6 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
       for (int i = 0; i < 2; ++i)   // column 2t + i is row 2t + i of A, of lanes (2t + i, .)
         factor[b][j][i] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * i);
     }
-  }
 }
 
 // int4: also eight times the sums of A over each group, times the 2^-9 of the codes, into
@@ -148,16 +157,22 @@ __device__ __forceinline__ void load_e4m3(const GemvParams& p, int m0, int k0,
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int end = min(p.M, m0 + p.per);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int m = m0 + 8 * j + g;
-    uint64_t sum = 0;
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < chunk_of(true, NT) / 32; ++i) {
-      const int k = k0 + 32 * i;
+      const int m = m0 + 8 * j + g, k = k0 + 32 * i;
       uint2 x = make_uint2(0, 0);
       if (m < end && k < p.K)
         x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.a) + m * p.lda + k +
                                                  8 * t));
+      frag[i][j][0] = x.x, frag[i][j][1] = x.y;
+    }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < chunk_of(true, NT) / 32; ++i) {
+      const uint2 x = make_uint2(frag[i][j][0], frag[i][j][1]);
       frag[i][j][0] = __byte_perm(x.x, x.y, 0x6420);
       frag[i][j][1] = __byte_perm(x.x, x.y, 0x7531);
       if constexpr (INT4) {
@@ -194,12 +209,12 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   constexpr int kFrag = frag_of(E4M3);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   unsigned char* ring = smem + warp * kStages * p.stage_bytes;
-  // sums over the warps [2][warps][8 NT][kRedPitch]; int4 by E4M3: the groups' sums of A;
-  // across the cluster [8 NT][16 tiles]
+  // the warps' sums of a batch of tiles [batch][warps][NT][16 rows][8]; int4 by E4M3: the
+  // groups' sums of A; across the cluster [8 NT][16 tiles]
   float* red = reinterpret_cast<float*>(smem + p.warps * kStages * p.stage_bytes);
-  constexpr int kRed = 8 * NT * kRedPitch, kOuts = 8 * NT * kGemvRows;
-  float* sums = red + 2 * p.warps * kRed + warp * (E4M3 && INT4 ? kPer * 8 * NT : 0);
-  float* total = red + 2 * p.warps * kRed + p.warps * (E4M3 && INT4 ? kPer * 8 * NT : 0);
+  constexpr int kOuts = 8 * NT * kGemvRows;
+  float* sums = red + p.batch * p.warps * kOuts + warp * (E4M3 && INT4 ? kPer * 8 * NT : 0);
+  float* total = red + p.batch * p.warps * kOuts + p.warps * (E4M3 && INT4 ? kPer * 8 * NT : 0);
 
   const int slice = blockIdx.x / p.cluster;
   const int rank = blockIdx.x - slice * p.cluster;
@@ -271,14 +286,19 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
     load_bf16<INT4, NT>(p, m0, k0, frag, factor);
 
   const int summed = min(p.warps, p.chunks - rank * p.warps);   // warps with a chunk
-  int turned = threadIdx.x;   // the sums' threads move on by a tile's outputs each time
+  // Row and piece of the matrix rows whose addresses this lane gives: matrices 0 and 1
+  // are rows 0 to 7 and 8 to 15 of an even sub-block, 2 and 3 of the odd one behind it.
+  const int mrow = lane & 15, mturn = kSubs == 8 ? lane & 7 : lane >> 1 & 3;
+  const uint32_t matrices =
+      smem_addr(ring) + mrow * kSubs * 16 + ((lane >> 4) ^ mturn) * 16;
   uint32_t at = 0;
+  int slot = 0;   // of the batch
   for (int tile = 0; tile < tiles; ++tile) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
-    float* mine = red + ((tile & 1) * p.warps + warp) * kRed;
+    float* mine = red + (slot * p.warps + warp) * kOuts;
     if (live) {
-      const unsigned char* st = ring + at;
+      const unsigned char* st = ring + at;   // the tile's stage
       // the scales of rows g and g + 8
       float sc[2][kPer];
 #pragma unroll
@@ -308,9 +328,7 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
           for (int i = 0; i < kPer; ++i) sc[h][i] = __uint_as_float((uint32_t)v[i] << 16);
         }
       }
-      // a row's pieces are 16 bytes each, in the order of their numbers xor its turn
-      const uint32_t word =
-          (uint32_t)(g * kSubs * 16 + (kSubs == 8 ? g : g >> 1 & 3) * 16 + 4 * t);
+      uint32_t w[4];
       float acc[NT][4];
 #pragma unroll
       for (int b = 0; b < kChunk / 128; ++b) {
@@ -318,10 +336,10 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int sub = 4 * b + i;
-          const unsigned char* from = st + (word ^ (16u * sub));
+          if (i % 2 == 0) load_matrices((matrices + at) ^ (16u * sub), w);
           uint32_t lo[kFrag], hi[kFrag];
-          decode8<E4M3, INT4>(*reinterpret_cast<const uint32_t*>(from), lo);
-          decode8<E4M3, INT4>(*reinterpret_cast<const uint32_t*>(from + 8 * kSubs * 16), hi);
+          decode8<E4M3, INT4>(w[i % 2 * 2], lo);
+          decode8<E4M3, INT4>(w[i % 2 * 2 + 1], hi);
           const bool opens = 32 * i % G == 0, ends = 32 * (i + 1) % G == 0;
           const int grp = 32 * sub / G;
 #pragma unroll
@@ -360,36 +378,45 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mine[(8 * j + 2 * t + (e & 1)) * kRedPitch + g + 8 * (e >> 1)] = acc[j][e];
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(mine + (16 * j + g + 8 * h) * 8 + 2 * t) =
+              make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
     }
     __syncwarp();   // the stage is read by all before the next copy into it
     stage(tile + kStages, at);
     at += p.stage_bytes;
     if (at == (uint32_t)(kStages * p.stage_bytes)) at = 0;
-    __syncthreads();   // the other buffer's readers are past this barrier
-    const int first = kGemvRows * tile;
-    for (int o = turned; o < kOuts; o += blockDim.x) {
-      const int m = o / kGemvRows, r = o % kGemvRows;
-      const float* from = red + (tile & 1) * p.warps * kRed + m * kRedPitch + r;
-      float v = 0.f;
-#pragma unroll 8
-      for (int w = 0; w < summed; ++w) v += from[w * kRed];
-      if (E4M3) v *= INT4 ? 512.f : 64.f;   // of the codes' bits
-      if (p.cluster > 1) {
-        total[m * kGemvRows * tiles + first + r] = v;
-      } else if (m0 + m < p.M && first + r < rows) {
-        const int64_t out = (int64_t)(m0 + m) * p.N + n0 + first + r;
-        if (p.fp32)
-          static_cast<float*>(p.y)[out] = v;
-        else
-          static_cast<__nv_bfloat16*>(p.y)[out] = __float2bfloat16_rn(v);
+    if (++slot < p.batch && tile + 1 < tiles) continue;
+
+    // the batch's sums over the warps, four columns of a row of W at a time
+    __syncthreads();
+    for (int o = threadIdx.x; o < slot * (kOuts / 4); o += blockDim.x) {
+      const int b = o / (kOuts / 4), q = o % (kOuts / 4);
+      const int m = q / 32 * 8 + q % 2 * 4, r = kGemvRows * (tile + 1 - slot + b) + q % 32 / 2;
+      if (m0 + m >= p.M) continue;
+      const float4* from = reinterpret_cast<const float4*>(red + b * p.warps * kOuts) + q;
+      float v[4] = {};
+#pragma unroll 4
+      for (int w = 0; w < summed; ++w) {
+        const float4 x = from[w * (kOuts / 4)];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (E4M3) v[e] *= INT4 ? 512.f : 64.f;   // of the codes' bits
+        if (p.cluster > 1) {
+          total[(m + e) * kGemvRows * tiles + r] = v[e];
+        } else if (m0 + m + e < p.M && r < rows) {
+          const int64_t out = (int64_t)(m0 + m + e) * p.N + n0 + r;
+          if (p.fp32)
+            static_cast<float*>(p.y)[out] = v[e];
+          else
+            static_cast<__nv_bfloat16*>(p.y)[out] = __float2bfloat16_rn(v[e]);
+        }
       }
     }
-    if (kOuts < (int)blockDim.x) {
-      turned -= kOuts;
-      if (turned < 0) turned += blockDim.x;
-    }
+    slot = 0;
+    if (tile + 1 < tiles) __syncthreads();   // read by all before the next batch
   }
   if (p.cluster == 1) return;
 

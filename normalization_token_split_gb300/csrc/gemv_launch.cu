@@ -33,6 +33,13 @@
 
 namespace nts {
 
+namespace {
+
+// Tiles of a batch, by tiles of 8 rows of A: 4 KB of sums per warp.
+constexpr int kBatch = 8;
+
+}  // namespace
+
 int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& tune) {
   if (const int injected = take_injected_failure()) return injected;
   const DeviceInfo& dev = device_info();
@@ -70,9 +77,10 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
 
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((unsigned)(32 * p.warps));
+  p.batch = kBatch / nt;
   const size_t base =
-      (size_t)p.warps * (stages * p.stage_bytes +
-                         (2 * kRedPitch + (e4m3 && rq.int4 ? per_row : 0)) * 8 * nt * sizeof(float));
+      (size_t)p.warps * (stages * p.stage_bytes + (kGemvRows * p.batch + (e4m3 && rq.int4 ? per_row : 0)) *
+                                                      8 * nt * sizeof(float));
   // slices: what the GPU holds at once; the sums of a slice across a cluster take
   // shared memory, so a long N takes more slices than that
   const size_t limit = (size_t)dev.max_smem_optin;
