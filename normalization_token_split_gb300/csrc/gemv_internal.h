@@ -6,10 +6,12 @@
 
 #include <cstdint>
 
+#include "block_internal.h"
+
 namespace nts {
 
 constexpr int kMaxGemvWarps = 16;
-constexpr int kGemvRows = 16;      // weight rows of a tile
+constexpr int kGemvRows = 32;      // weight rows of a tile
 
 #ifdef __CUDACC__
 #define NTS_GEMV_RULE __host__ __device__ constexpr
@@ -17,11 +19,9 @@ constexpr int kGemvRows = 16;      // weight rows of a tile
 #define NTS_GEMV_RULE constexpr
 #endif
 // k values of a warp's chunk (its part of A fills 64 registers at most), and the ring's
-// stages, for rows of A in E4M3 or bf16 and NT tiles of 8 of them.
-NTS_GEMV_RULE int chunk_of(bool e4m3, int nt) { return e4m3 || nt <= 2 ? 256 : 128; }
-NTS_GEMV_RULE int stages_of(bool e4m3, int nt) {
-  return chunk_of(e4m3, nt) == 128 ? 6 : nt == 4 ? 3 : 4;
-}
+// stages, for NT tiles of 8 rows of A.
+NTS_GEMV_RULE int chunk_of(int nt) { return nt <= 2 ? 256 : 128; }
+NTS_GEMV_RULE int stages_of(int nt) { return nt <= 2 ? 2 : 3; }
 
 struct GemvParams {
   const void* a;
@@ -47,12 +47,10 @@ struct GemvParams {
 
 using GemvKernel = void (*)(GemvParams);
 
-// The kernel for a group size and a number of tiles of 8 rows (gemv_*.cu).
-template <bool E4M3, bool INT4>
+// The kernel for a group size and a number of tiles of 8 rows (gemv_e2m1.cu, gemv_int4.cu).
+template <bool INT4>
 GemvKernel pick_gemv(int group, int nt);
-extern template GemvKernel pick_gemv<false, false>(int, int);
-extern template GemvKernel pick_gemv<false, true>(int, int);
-extern template GemvKernel pick_gemv<true, false>(int, int);
-extern template GemvKernel pick_gemv<true, true>(int, int);
+extern template GemvKernel pick_gemv<false>(int, int);
+extern template GemvKernel pick_gemv<true>(int, int);
 
 }  // namespace nts

@@ -1,5 +1,5 @@
 // gemv_kernel.cuh -- the kernel of the products with 4-bit weights (gemv_launch.cu
-// describes it); instantiated in gemv_{bf16,e4m3}_{e2m1,int4}.cu.
+// describes it); instantiated in gemv_e2m1.cu and gemv_int4.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,21 +22,12 @@ __device__ __forceinline__ void copy_async_small(uint32_t dst, const void* src, 
                : "memory");
 }
 
-// Eight codes in the operand type of the products.  fp16 (four pairs): E2M1's pair j
-// holds values 2j and 2j + 1, by the hardware's conversion; int4's values j and j + 4, a
-// code's four bits put under the exponent of 1024 (or 64, where they stand four bits
-// higher) and the offset taken off.  E4M3 (two fours): the even values, then the odd
-// ones.  E2M1's bits under E4M3's bias are the values times 2^-6, subnormal ones too;
-// int4's plus eight, 0 to 15, are as bits of E4M3 themselves times 2^-9.
-template <bool E4M3, bool INT4>
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&p)[E4M3 ? 2 : 4]) {
-  if constexpr (E4M3 && INT4) {
-    p[0] = (w & 0x0F0F0F0Fu) ^ 0x08080808u;
-    p[1] = (w >> 4 & 0x0F0F0F0Fu) ^ 0x08080808u;
-  } else if constexpr (E4M3) {
-    p[0] = (w << 2 & 0x1C1C1C1Cu) | (w << 4 & 0x80808080u);
-    p[1] = (w >> 2 & 0x1C1C1C1Cu) | (w & 0x80808080u);
-  } else if constexpr (INT4) {
+// Eight codes as four pairs of fp16.  E2M1: pair j holds values 2j and 2j + 1, by the
+// hardware's conversion.  int4: values j and j + 4, a code's four bits put under the
+// exponent of 1024 (or 64, where they stand four bits higher) and the offset taken off.
+template <bool INT4>
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&p)[4]) {
+  if constexpr (INT4) {
     const uint32_t v = w >> 8;
     const uint32_t a = (w & 0x000F000Fu) ^ 0x64086408u, b = (w & 0x00F000F0u) ^ 0x54805480u;
     const uint32_t c = (v & 0x000F000Fu) ^ 0x64086408u, d = (v & 0x00F000F0u) ^ 0x54805480u;
@@ -74,42 +65,38 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
-                                         float c2, float c3) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-__device__ __forceinline__ uint64_t e4m3x4_sum(uint32_t v, uint64_t s) {
-  s = f2_add(s, e4m3x2_to_f2((uint16_t)v));
-  return f2_add(s, e4m3x2_to_f2((uint16_t)(v >> 16)));
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
 }
 
-// Registers of a lane's part of 32 values of one row of A.
-__host__ __device__ constexpr int frag_of(bool e4m3) { return e4m3 ? 2 : 4; }
+// Eight values in pairs (0, 1), (2, 3), .. as (0, 4), (1, 5), ..
+__device__ __forceinline__ void by_fours(uint32_t (&p)[4]) {
+  const uint32_t a = __byte_perm(p[0], p[2], 0x5410), b = __byte_perm(p[0], p[2], 0x7632);
+  const uint32_t c = __byte_perm(p[1], p[3], 0x5410), d = __byte_perm(p[1], p[3], 0x7632);
+  p[0] = a, p[1] = b, p[2] = c, p[3] = d;
+}
 
 // A warp's chunk of A as B fragments: frag[sub-block of 32][tile of 8 rows], and per
 // block of 128 and tile the factors of the lane's two columns of a product.
 template <bool INT4, int NT>
 __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
-                                          uint32_t (&frag)[chunk_of(false, NT) / 32][NT][4],
-                                          float (&factor)[chunk_of(false, NT) / 128][NT][2]) {
+                                          uint32_t (&frag)[chunk_of(NT) / 32][NT][4],
+                                          float (&factor)[chunk_of(NT) / 128][NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int end = min(p.M, m0 + p.per);
   // every load is issued before the first is used
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < chunk_of(false, NT) / 32; ++i) {
+    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
       const int m = m0 + 8 * j + g, k = k0 + 32 * i;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (m < end && k < p.K)
@@ -120,7 +107,7 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int b = 0; b < chunk_of(false, NT) / 128; ++b) {
+    for (int b = 0; b < chunk_of(NT) / 128; ++b) {
       uint32_t most2 = 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) most2 = bf16x2_absmax(most2, frag[4 * b + i / 4][j][i % 4]);
@@ -147,74 +134,61 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
     }
 }
 
-// int4: also eight times the sums of A over each group, times the 2^-9 of the codes, into
-// sums[group of the chunk][8 NT]: what the products are too large by.
-template <bool INT4, int G, int NT>
+template <bool INT4, int NT>
 __device__ __forceinline__ void load_e4m3(const GemvParams& p, int m0, int k0,
-                                          uint32_t (&frag)[chunk_of(true, NT) / 32][NT][2],
-                                          float (&factor)[chunk_of(true, NT) / 128][NT][2],
-                                          float* sums) {
+                                          uint32_t (&frag)[chunk_of(NT) / 32][NT][4],
+                                          float (&factor)[chunk_of(NT) / 128][NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int end = min(p.M, m0 + p.per);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < chunk_of(true, NT) / 32; ++i) {
+    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
       const int m = m0 + 8 * j + g, k = k0 + 32 * i;
       uint2 x = make_uint2(0, 0);
       if (m < end && k < p.K)
         x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.a) + m * p.lda + k +
                                                  8 * t));
-      frag[i][j][0] = x.x, frag[i][j][1] = x.y;
+      frag[i][j][0] = x.x, frag[i][j][2] = x.y;
     }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    uint64_t sum = 0;
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < chunk_of(true, NT) / 32; ++i) {
-      const uint2 x = make_uint2(frag[i][j][0], frag[i][j][1]);
-      frag[i][j][0] = __byte_perm(x.x, x.y, 0x6420);
-      frag[i][j][1] = __byte_perm(x.x, x.y, 0x7531);
-      if constexpr (INT4) {
-        sum = e4m3x4_sum(x.y, e4m3x4_sum(x.x, sum));
-        if (32 * (i + 1) % G == 0) {
-          float v = f2_lo(sum) + f2_hi(sum);
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-          if (t == 0) sums[32 * i / G * 8 * NT + 8 * j + g] = v * -0x1p-6f;
-          sum = 0;
-        }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < chunk_of(true, NT) / 128; ++b)
+    for (int b = 0; b < chunk_of(NT) / 128; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = m0 + 8 * j + 2 * t + i, block = k0 / 128 + b;
         factor[b][j][i] =
             col < end && block < p.kb ? __ldg(p.a_scales + (int64_t)col * p.kb + block) : 0.f;
       }
-  }
-  if (INT4) __syncwarp();
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
+      uint32_t(&f)[4] = frag[i][j];
+      f[1] = e4m3x2_to_f16x2(f[0] >> 16), f[3] = e4m3x2_to_f16x2(f[2] >> 16);
+      f[0] = e4m3x2_to_f16x2(f[0]), f[2] = e4m3x2_to_f16x2(f[2]);
+      if (INT4) by_fours(f);
+    }
 }
 
-template <bool E4M3, bool INT4, int G, int NT>
+template <bool INT4, int G, int NT>
 __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kChunk = chunk_of(E4M3, NT), kStages = stages_of(E4M3, NT);
+  constexpr int kChunk = chunk_of(NT), kStages = stages_of(NT);
   constexpr int kSubs = kChunk / 32;             // 16-byte pieces of a row's chunk of codes
   constexpr int kPer = kChunk / G;               // scales of a row's chunk
   constexpr int kCodes = kGemvRows * kChunk / 2;
   constexpr int kCopies = kGemvRows * kSubs / 32;   // of 16 bytes, per lane and tile
-  constexpr int kFrag = frag_of(E4M3);
+  constexpr int kStep = 32 / kSubs;              // rows of one copy of the warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  unsigned char* ring = smem + warp * kStages * p.stage_bytes;
-  // the warps' sums of a batch of tiles [batch][warps][NT][16 rows][8]; int4 by E4M3: the
-  // groups' sums of A; across the cluster [8 NT][16 tiles]
-  float* red = reinterpret_cast<float*>(smem + p.warps * kStages * p.stage_bytes);
+  // Shared memory: stages [warps][stages] of codes and scales of 32 rows, the warps' sums
+  // of a batch of tiles [batch][warps][2 halves][NT][16 rows][8], and across the cluster
+  // the sums of the slice [8 NT][32 tiles]
   constexpr int kOuts = 8 * NT * kGemvRows;
-  float* sums = red + p.batch * p.warps * kOuts + warp * (E4M3 && INT4 ? kPer * 8 * NT : 0);
-  float* total = red + p.batch * p.warps * kOuts + p.warps * (E4M3 && INT4 ? kPer * 8 * NT : 0);
+  unsigned char* ring = smem + warp * kStages * p.stage_bytes;
+  float* red = reinterpret_cast<float*>(smem + p.warps * kStages * p.stage_bytes);
+  float* total = red + p.batch * p.warps * kOuts;
 
   const int slice = blockIdx.x / p.cluster;
   const int rank = blockIdx.x - slice * p.cluster;
@@ -229,7 +203,6 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   // One tile's codes and scales into a stage.  A row's pieces change places with the
   // row's number, so that the eight rows that a warp reads at once meet distinct banks.
   const int row0 = lane / kSubs, piece = lane % kSubs;
-  constexpr int kStep = 32 / kSubs;              // rows of one copy of the warp
   const int turn = kSubs == 8 ? row0 : row0 >> 1 & 3;
   const int64_t pitch = p.K / 2;
   const unsigned char* codes = p.w + (n0 + row0) * pitch + k0 / 2 + 16 * piece;
@@ -239,22 +212,22 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   auto stage = [&](int tile, uint32_t at) {
     if (live && tile < tiles) {
       const int left = rows - kGemvRows * tile;
+      const unsigned char* from = codes;
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
         // with eight pieces a row, rows four apart differ in the turn's third bit
         const uint32_t dst = (kSubs == 8 && i % 2 ? to ^ 64u : to) + 512 * i;
-        copy_async16(dst + at, codes + i * kStep * pitch, row0 + i * kStep < left ? bytes : 0);
+        copy_async16(dst + at, from, row0 + i * kStep < left ? bytes : 0);
+        from += kStep * pitch;
       }
-      codes += kGemvRows * pitch;
-      if (p.vector) {
-        if (lane < kGemvRows) {
-          const uint32_t dst = smem_addr(ring) + at + kCodes + lane * p.scale_pitch;
-          const int n = lane < left ? 2 * kPer : 0;
-          if constexpr (kPer == 8)
-            copy_async16(dst, scales, n);
-          else if constexpr (kPer >= 2)
-            copy_async_small<2 * kPer>(dst, scales, n);
-        }
+      codes = from;
+      const uint32_t into = smem_addr(ring) + at + kCodes;
+      if (kPer >= 2 && p.vector) {
+        const int n = lane < left ? 2 * kPer : 0;
+        if constexpr (kPer == 8)
+          copy_async16(into + lane * p.scale_pitch, scales, n);
+        else if constexpr (kPer >= 2)
+          copy_async_small<2 * kPer>(into + lane * p.scale_pitch, scales, n);
         scales += (int64_t)kGemvRows * p.groups;
       } else {
         // words that hold them, from the word of the first; nothing beyond the last
@@ -267,7 +240,7 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
           const int n = row < left
                             ? (int)max64(0, min64(4, 2 * (first + have) - (4 * (first / 2) + 4 * word)))
                             : 0;
-          copy_async_small<4>(smem_addr(ring) + at + kCodes + row * p.scale_pitch + 4 * word,
+          copy_async_small<4>(into + row * p.scale_pitch + 4 * word,
                               n > 0 ? p.s + 2 * (first / 2) + 2 * word : p.s, n);
         }
       }
@@ -278,10 +251,10 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   allow_dependent_launch();
   for (int s = 0; s < kStages; ++s) stage(s, s * p.stage_bytes);
 
-  uint32_t frag[kSubs][NT][kFrag];
+  uint32_t frag[kSubs][NT][4];
   float factor[kChunk / 128][NT][2];
-  if constexpr (E4M3)
-    load_e4m3<INT4, G, NT>(p, m0, k0, frag, factor, sums);
+  if (p.a_scales != nullptr)
+    load_e4m3<INT4, NT>(p, m0, k0, frag, factor);
   else
     load_bf16<INT4, NT>(p, m0, k0, frag, factor);
 
@@ -291,96 +264,134 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   const int mrow = lane & 15, mturn = kSubs == 8 ? lane & 7 : lane >> 1 & 3;
   const uint32_t matrices =
       smem_addr(ring) + mrow * kSubs * 16 + ((lane >> 4) ^ mturn) * 16;
+  // Halves of a tile and sub-blocks whose products are formed side by side: independent
+  // sums for the tensor pipe, as far as registers go.
+  constexpr int kHalves = NT == 1 ? 2 : 1, kSide = NT == 4 ? 1 : 2;
   uint32_t at = 0;
   int slot = 0;   // of the batch
   for (int tile = 0; tile < tiles; ++tile) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
-    float* mine = red + (slot * p.warps + warp) * kOuts;
     if (live) {
-      const unsigned char* st = ring + at;   // the tile's stage
-      // the scales of rows g and g + 8
-      float sc[2][kPer];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const unsigned char* from = st + kCodes + (g + 8 * h) * p.scale_pitch;
-        if (kPer >= 2 && p.vector) {
-          uint32_t w[kPer >= 2 ? kPer / 2 : 1];
-          if constexpr (kPer == 8) {
-            const uint4 v = lds128(from);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-          } else if constexpr (kPer == 4) {
-            const uint2 v = lds64(from);
-            w[0] = v.x, w[1] = v.y;
-          } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(from);
-          }
+      for (int half = 0; half < 2; half += kHalves) {
+        if (kHalves == 1 && rows <= kGemvRows * tile + 16 * half) break;
+        float acc[kHalves][NT][4];
 #pragma unroll
-          for (int i = 0; i < kPer / 2; ++i) {
-            sc[h][2 * i] = __uint_as_float(w[i] << 16);
-            sc[h][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-          }
-        } else {
-          const int odd = (int)(((int64_t)(n0 + kGemvRows * tile + g + 8 * h) * p.groups +
-                                 chunk * kPer) & 1);
-          const uint16_t* v = reinterpret_cast<const uint16_t*>(from) + odd;
+        for (int b = 0; b < kChunk / 128; ++b) {
+          constexpr int kGroups = 128 / G;
+          // the block's scales of rows g and g + 8
+          float sc[kHalves][2][kGroups];
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) sc[h][i] = __uint_as_float((uint32_t)v[i] << 16);
-        }
-      }
-      uint32_t w[4];
-      float acc[NT][4];
-#pragma unroll
-      for (int b = 0; b < kChunk / 128; ++b) {
-        float d[NT][4], c[NT][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int sub = 4 * b + i;
-          if (i % 2 == 0) load_matrices((matrices + at) ^ (16u * sub), w);
-          uint32_t lo[kFrag], hi[kFrag];
-          decode8<E4M3, INT4>(w[i % 2 * 2], lo);
-          decode8<E4M3, INT4>(w[i % 2 * 2 + 1], hi);
-          const bool opens = 32 * i % G == 0, ends = 32 * (i + 1) % G == 0;
-          const int grp = 32 * sub / G;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint32_t(&f)[kFrag] = frag[sub][j];
-            float(&cj)[4] = c[j];
-            if constexpr (E4M3) {
-              float2 x = make_float2(0.f, 0.f);
-              if (INT4 && opens) x = *reinterpret_cast<const float2*>(sums + grp * 8 * NT + 8 * j + 2 * t);
-              if (opens)
-                mma_e4m3(cj, lo[0], hi[0], lo[1], hi[1], f[0], f[1], x.x, x.y, x.x, x.y);
-              else
-                mma_e4m3(cj, lo[0], hi[0], lo[1], hi[1], f[0], f[1], cj[0], cj[1], cj[2], cj[3]);
+          for (int h = 0; h < 2 * kHalves; ++h) {
+            const int row = 16 * half + g + 8 * h;
+            const unsigned char* from = ring + at + kCodes + row * p.scale_pitch;
+            float(&v)[kGroups] = sc[h / 2][h % 2];
+            if (kPer >= 2 && p.vector) {
+              if constexpr (kGroups == 4) {
+                const uint2 w = lds64(from + 8 * b);
+                v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+                v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+              } else if constexpr (kGroups == 2) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(from + 4 * b);
+                v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xFFFF0000u);
+              } else {
+                v[0] = __uint_as_float(
+                    (uint32_t)*reinterpret_cast<const uint16_t*>(from + 2 * b) << 16);
+              }
             } else {
-              if (opens)
-                mma_f16(cj, lo[0], hi[0], lo[1], hi[1], f[0], f[1], 0.f, 0.f, 0.f, 0.f);
-              else
-                mma_f16(cj, lo[0], hi[0], lo[1], hi[1], f[0], f[1], cj[0], cj[1], cj[2], cj[3]);
-              mma_f16(cj, lo[2], hi[2], lo[3], hi[3], f[2], f[3], cj[0], cj[1], cj[2], cj[3]);
+              const int odd = (int)(((int64_t)(n0 + kGemvRows * tile + row) * p.groups +
+                                     chunk * kPer) & 1);
+#pragma unroll
+              for (int i = 0; i < kGroups; ++i)
+                v[i] = __uint_as_float(
+                    (uint32_t)reinterpret_cast<const uint16_t*>(from)[odd + kGroups * b + i] << 16);
             }
-            if (ends) {
-              const bool begins = 32 * (i + 1) == G;   // the block's first group
+          }
+          float d[kHalves][NT][4], c[kHalves][kSide][NT][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {   // pairs of sub-blocks
+            uint32_t w[kHalves][4];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              load_matrices(((matrices + at) ^ (16u * (4 * b + 2 * i))) +
+                                (half + h) * (16 * kSubs * 16), w[h]);
+#pragma unroll
+            for (int s0 = 0; s0 < 2; s0 += kSide) {
+              uint32_t lo[kHalves][kSide][4], hi[kHalves][kSide][4];
+#pragma unroll
+              for (int s = 0; s < kSide; ++s)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                  decode8<INT4>(w[h][2 * (s0 + s)], lo[h][s]);
+                  decode8<INT4>(w[h][2 * (s0 + s) + 1], hi[h][s]);
+                }
+              // whether a sum of this pair (or sub-block) opens its group
+              const bool opens = kSide == 2 ? G <= 64 || i == 0 : 32 * (2 * i + s0) % G == 0;
+#pragma unroll
+              for (int s = 0; s < kSide; ++s)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                  for (int j = 0; j < NT; ++j) {
+                    const uint32_t(&f)[4] = frag[4 * b + 2 * i + s0 + s][j];
+                    float(&x)[4] = c[h][s][j];
+                    const uint32_t(&l)[4] = lo[h][s], (&u)[4] = hi[h][s];
+                    if (opens)
+                      mma_f16(x, l[0], u[0], l[1], u[1], f[0], f[1], 0.f, 0.f, 0.f, 0.f);
+                    else
+                      mma_f16(x, l[0], u[0], l[1], u[1], f[0], f[1], x[0], x[1], x[2], x[3]);
+                  }
+#pragma unroll
+              for (int s = 0; s < kSide; ++s)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                  for (int j = 0; j < NT; ++j) {
+                    const uint32_t(&f)[4] = frag[4 * b + 2 * i + s0 + s][j];
+                    float(&x)[4] = c[h][s][j];
+                    const uint32_t(&l)[4] = lo[h][s], (&u)[4] = hi[h][s];
+                    mma_f16(x, l[2], u[2], l[3], u[3], f[2], f[3], x[0], x[1], x[2], x[3]);
+                  }
+              // groups that end here, into the block's sums
+#pragma unroll
+              for (int s = 0; s < kSide; ++s) {
+                const int sub = 2 * i + s0 + s;
+                if (32 * (sub + 1) % G != 0) continue;
+                const int grp = 32 * sub / G;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                  for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const float v = G > 32 && kSide == 2 ? c[h][0][j][e] + c[h][1][j][e]
+                                                           : c[h][s][j][e];
+                      d[h][j][e] = grp == 0 ? v * sc[h][e >> 1][grp]
+                                            : fmaf(v, sc[h][e >> 1][grp], d[h][j][e]);
+                    }
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                d[j][e] = begins ? cj[e] * sc[e >> 1][grp] : fmaf(cj[e], sc[e >> 1][grp], d[j][e]);
-            }
-          }
+                acc[h][j][e] = b == 0 ? d[h][j][e] * factor[b][j][e & 1]
+                                      : fmaf(d[h][j][e], factor[b][j][e & 1], acc[h][j][e]);
         }
+        float* mine = red + (slot * p.warps + warp) * kOuts + half * (kOuts / 2);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[j][e] = b == 0 ? d[j][e] * factor[b][j][e & 1]
-                               : fmaf(d[j][e], factor[b][j][e & 1], acc[j][e]);
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              *reinterpret_cast<float2*>(mine + h * (kOuts / 2) + (16 * j + g + 4 * e) * 8 + 2 * t) =
+                  make_float2(acc[h][j][e], acc[h][j][e + 1]);
       }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(mine + (16 * j + g + 8 * h) * 8 + 2 * t) =
-              make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
     }
     __syncwarp();   // the stage is read by all before the next copy into it
     stage(tile + kStages, at);
@@ -392,8 +403,10 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
     __syncthreads();
     for (int o = threadIdx.x; o < slot * (kOuts / 4); o += blockDim.x) {
       const int b = o / (kOuts / 4), q = o % (kOuts / 4);
-      const int m = q / 32 * 8 + q % 2 * 4, r = kGemvRows * (tile + 1 - slot + b) + q % 32 / 2;
-      if (m0 + m >= p.M) continue;
+      const int half = q / (kOuts / 8), f = q % (kOuts / 8);
+      const int m = f / 32 * 8 + f % 2 * 4;
+      const int r = kGemvRows * (tile + 1 - slot + b) + 16 * half + f % 32 / 2;
+      if (m0 + m >= p.M || r >= rows) continue;
       const float4* from = reinterpret_cast<const float4*>(red + b * p.warps * kOuts) + q;
       float v[4] = {};
 #pragma unroll 4
@@ -403,10 +416,9 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (E4M3) v[e] *= INT4 ? 512.f : 64.f;   // of the codes' bits
         if (p.cluster > 1) {
           total[(m + e) * kGemvRows * tiles + r] = v[e];
-        } else if (m0 + m + e < p.M && r < rows) {
+        } else if (m0 + m + e < p.M) {
           const int64_t out = (int64_t)(m0 + m + e) * p.N + n0 + r;
           if (p.fp32)
             static_cast<float*>(p.y)[out] = v[e];
@@ -445,22 +457,22 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   cluster_wait_acquire();
 }
 
-template <bool E4M3, bool INT4, int G>
+template <bool INT4, int G>
 GemvKernel pick_tiles(int nt) {
   switch (nt) {
-    case 1: return gemv_kernel<E4M3, INT4, G, 1>;
-    case 2: return gemv_kernel<E4M3, INT4, G, 2>;
-    default: return gemv_kernel<E4M3, INT4, G, 4>;
+    case 1: return gemv_kernel<INT4, G, 1>;
+    case 2: return gemv_kernel<INT4, G, 2>;
+    default: return gemv_kernel<INT4, G, 4>;
   }
 }
 
 }  // namespace
 
-template <bool E4M3, bool INT4>
+template <bool INT4>
 GemvKernel pick_gemv(int group, int nt) {
-  return group == 32   ? pick_tiles<E4M3, INT4, 32>(nt)
-         : group == 64 ? pick_tiles<E4M3, INT4, 64>(nt)
-                       : pick_tiles<E4M3, INT4, 128>(nt);
+  return group == 32   ? pick_tiles<INT4, 32>(nt)
+         : group == 64 ? pick_tiles<INT4, 64>(nt)
+                       : pick_tiles<INT4, 128>(nt);
 }
 
 }  // namespace nts

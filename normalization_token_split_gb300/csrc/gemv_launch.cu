@@ -28,7 +28,6 @@
 
 #include <algorithm>
 
-#include "block_internal.h"
 #include "gemv_internal.h"
 
 namespace nts {
@@ -36,7 +35,7 @@ namespace nts {
 namespace {
 
 // Tiles of a batch, by tiles of 8 rows of A: 4 KB of sums per warp.
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;
 
 }  // namespace
 
@@ -48,7 +47,6 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.a = rq.A;
   p.a_scales = rq.a_scales;
   p.lda = rq.lda;
-  p.w = static_cast<const uint8_t*>(rq.W);
   p.s = static_cast<const __nv_bfloat16*>(rq.w_scales);
   p.y = rq.Y;
   p.M = (int)rq.M;
@@ -57,30 +55,30 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.groups = (p.K + rq.group - 1) / rq.group;
   p.kb = (p.K + 127) / 128;
   p.fp32 = rq.fp32_out;
-  const bool e4m3 = rq.a_scales != nullptr;
   // slices of A's rows, in even parts; a chunk is half as long from 17 rows on, and a
   // cluster holds 128 chunks
-  const int slices_m = (p.M + 31) / 32 * (!e4m3 && p.M > 16 && p.K > 16384 ? 2 : 1);
+  const int slices_m = (p.M + 31) / 32 * (p.M > 16 && p.K > 16384 ? 2 : 1);
   p.per = ((p.M + slices_m - 1) / slices_m + 7) / 8 * 8;
   const int nt = p.per <= 8 ? 1 : p.per <= 16 ? 2 : 4;
   p.per = 8 * nt;
-  const int chunk = chunk_of(e4m3, nt), stages = stages_of(e4m3, nt);
+  const int chunk = chunk_of(nt), stages = stages_of(nt);
   p.chunks = (p.K + chunk - 1) / chunk;
   p.cluster = (p.chunks + kMaxGemvWarps - 1) / kMaxGemvWarps;
   p.warps = (p.chunks + p.cluster - 1) / p.cluster;
   const int per_row = chunk / rq.group;
   p.vector = per_row >= 2 && p.groups % per_row == 0;
   p.scale_pitch = p.vector ? 2 * per_row : (2 * per_row + 2 + 3) / 4 * 4;
+  p.w = static_cast<const uint8_t*>(rq.W);
   p.stage_bytes = (kGemvRows * (chunk / 2 + p.scale_pitch) + 127) / 128 * 128;
-  const GemvKernel kern = e4m3 ? (rq.int4 ? pick_gemv<true, true> : pick_gemv<true, false>)(rq.group, nt)
-                               : (rq.int4 ? pick_gemv<false, true> : pick_gemv<false, false>)(rq.group, nt);
-
+  const GemvKernel kern = (rq.int4 ? pick_gemv<true> : pick_gemv<false>)(rq.group, nt);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((unsigned)(32 * p.warps));
   p.batch = kBatch / nt;
-  const size_t base =
-      (size_t)p.warps * (stages * p.stage_bytes + (kGemvRows * p.batch + (e4m3 && rq.int4 ? per_row : 0)) *
-                                                      8 * nt * sizeof(float));
+  const auto bytes = [&] {
+    return (size_t)p.warps *
+           (stages * p.stage_bytes + kGemvRows * p.batch * 8 * nt * sizeof(float));
+  };
+  size_t base = bytes();
   // slices: what the GPU holds at once; the sums of a slice across a cluster take
   // shared memory, so a long N takes more slices than that
   const size_t limit = (size_t)dev.max_smem_optin;
@@ -108,12 +106,15 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
   if (rc != NTS_OK) return rc;
   p.slices = (int)std::min<int64_t>(std::max<int64_t>(1, fit / slices_m), p.N);
   if (p.cluster > 1) {
-    const int row = 8 * nt * (int)sizeof(float);
-    const int most = (int)((limit - base) / row) / kGemvRows * kGemvRows;   // rows of a slice
-    p.slices = std::max(p.slices, (p.N + most - 1) / most);
-    while ((p.N + p.slices - 1) / p.slices > most) ++p.slices;
-    const int rows = (p.N + p.slices - 1) / p.slices;
-    cfg.dynamicSmemBytes = base + (size_t)((rows + kGemvRows - 1) / kGemvRows * kGemvRows) * row;
+    // the sums of a slice across the cluster: with shorter batches, or more slices
+    const size_t row = 8 * nt * sizeof(float);
+    const auto whole = [](int64_t n) { return (n + kGemvRows - 1) / kGemvRows * kGemvRows; };
+    const size_t want = whole((p.N + p.slices - 1) / p.slices) * row;
+    while (p.batch > 1 && bytes() + want > limit) p.batch /= 2;
+    base = bytes();
+    const int64_t most = (int64_t)((limit - base) / row) / kGemvRows * kGemvRows;
+    p.slices = (int)std::max<int64_t>(p.slices, (p.N + most - 1) / most);
+    cfg.dynamicSmemBytes = base + whole((p.N + p.slices - 1) / p.slices) * row;
   }
   cfg.gridDim = dim3((unsigned)(p.slices * p.cluster), (unsigned)slices_m);
   cudaLaunchAttribute attr[2];
