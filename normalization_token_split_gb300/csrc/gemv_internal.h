@@ -13,15 +13,8 @@ namespace nts {
 constexpr int kMaxGemvWarps = 16;
 constexpr int kGemvRows = 32;      // weight rows of a tile
 
-#ifdef __CUDACC__
-#define NTS_GEMV_RULE __host__ __device__ constexpr
-#else
-#define NTS_GEMV_RULE constexpr
-#endif
-// k values of a warp's chunk (its part of A fills 64 registers at most), and the ring's
-// stages, for NT tiles of 8 rows of A.
-NTS_GEMV_RULE int chunk_of(int nt) { return nt <= 2 ? 256 : 128; }
-NTS_GEMV_RULE int stages_of(int nt) { return nt <= 2 ? 2 : 3; }
+constexpr int kGemvChunk = 256;    // k values of a warp's chunk
+constexpr int kGemvStages = 2;     // tiles of a warp's ring
 
 struct GemvParams {
   const void* a;

@@ -85,29 +85,61 @@ __device__ __forceinline__ void by_fours(uint32_t (&p)[4]) {
 }
 
 // A warp's chunk of A as B fragments: frag[sub-block of 32][tile of 8 rows], and per
-// block of 128 and tile the factors of the lane's two columns of a product.
-template <bool INT4, int NT>
-__device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
-                                          uint32_t (&frag)[chunk_of(NT) / 32][NT][4],
-                                          float (&factor)[chunk_of(NT) / 128][NT][2]) {
+// block of 128 and tile the factors of the lane's two columns of a product.  First the
+// loads alone, as the rows lie in memory (eight values of a row to a lane), so that they
+// go out before the copies of the weights; then what the products take.
+template <int NT>
+__device__ __forceinline__ void load_rows(const GemvParams& p, int m0, int k0,
+                                          uint32_t (&frag)[kGemvChunk / 32][NT][4],
+                                          float (&factor)[kGemvChunk / 128][NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int end = min(p.M, m0 + p.per);
-  // every load is issued before the first is used
+  if (p.a_scales == nullptr) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      const int m = m0 + 8 * j + g;
+      const __nv_bfloat16* row =
+          static_cast<const __nv_bfloat16*>(p.a) + m * p.lda + k0 + 8 * t;
 #pragma unroll
-    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
-      const int m = m0 + 8 * j + g, k = k0 + 32 * i;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (m < end && k < p.K)
-        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a) +
-                                                 m * p.lda + k + 8 * t));
-      frag[i][j][0] = x.x, frag[i][j][1] = x.y, frag[i][j][2] = x.z, frag[i][j][3] = x.w;
+      for (int i = 0; i < kGemvChunk / 32; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (m < end && k0 + 32 * i < p.K) x = __ldg(reinterpret_cast<const uint4*>(row + 32 * i));
+        frag[i][j][0] = x.x, frag[i][j][1] = x.y, frag[i][j][2] = x.z, frag[i][j][3] = x.w;
+      }
     }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int m = m0 + 8 * j + g;
+    const uint8_t* row = static_cast<const uint8_t*>(p.a) + m * p.lda + k0 + 8 * t;
+#pragma unroll
+    for (int i = 0; i < kGemvChunk / 32; ++i) {
+      uint2 x = make_uint2(0, 0);
+      if (m < end && k0 + 32 * i < p.K) x = __ldg(reinterpret_cast<const uint2*>(row + 32 * i));
+      frag[i][j][0] = x.x, frag[i][j][1] = x.y;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int b = 0; b < chunk_of(NT) / 128; ++b) {
+    for (int b = 0; b < kGemvChunk / 128; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = m0 + 8 * j + 2 * t + i, block = k0 / 128 + b;
+        factor[b][j][i] =
+            col < end && block < p.kb ? __ldg(p.a_scales + (int64_t)col * p.kb + block) : 0.f;
+      }
+}
+
+template <bool INT4, int NT>
+__device__ __forceinline__ void convert_bf16(uint32_t (&frag)[kGemvChunk / 32][NT][4],
+                                             float (&factor)[kGemvChunk / 128][NT][2]) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int b = 0; b < kGemvChunk / 128; ++b) {
       uint32_t most2 = 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) most2 = bf16x2_absmax(most2, frag[4 * b + i / 4][j][i % 4]);
@@ -135,39 +167,14 @@ __device__ __forceinline__ void load_bf16(const GemvParams& p, int m0, int k0,
 }
 
 template <bool INT4, int NT>
-__device__ __forceinline__ void load_e4m3(const GemvParams& p, int m0, int k0,
-                                          uint32_t (&frag)[chunk_of(NT) / 32][NT][4],
-                                          float (&factor)[chunk_of(NT) / 128][NT][2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int end = min(p.M, m0 + p.per);
+__device__ __forceinline__ void convert_e4m3(uint32_t (&frag)[kGemvChunk / 32][NT][4]) {
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
-      const int m = m0 + 8 * j + g, k = k0 + 32 * i;
-      uint2 x = make_uint2(0, 0);
-      if (m < end && k < p.K)
-        x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.a) + m * p.lda + k +
-                                                 8 * t));
-      frag[i][j][0] = x.x, frag[i][j][2] = x.y;
-    }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int b = 0; b < chunk_of(NT) / 128; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = m0 + 8 * j + 2 * t + i, block = k0 / 128 + b;
-        factor[b][j][i] =
-            col < end && block < p.kb ? __ldg(p.a_scales + (int64_t)col * p.kb + block) : 0.f;
-      }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < chunk_of(NT) / 32; ++i) {
+    for (int i = 0; i < kGemvChunk / 32; ++i) {
       uint32_t(&f)[4] = frag[i][j];
-      f[1] = e4m3x2_to_f16x2(f[0] >> 16), f[3] = e4m3x2_to_f16x2(f[2] >> 16);
-      f[0] = e4m3x2_to_f16x2(f[0]), f[2] = e4m3x2_to_f16x2(f[2]);
+      f[3] = e4m3x2_to_f16x2(f[1] >> 16), f[2] = e4m3x2_to_f16x2(f[1]);
+      f[1] = e4m3x2_to_f16x2(f[0] >> 16), f[0] = e4m3x2_to_f16x2(f[0]);
       if (INT4) by_fours(f);
     }
 }
@@ -175,12 +182,13 @@ __device__ __forceinline__ void load_e4m3(const GemvParams& p, int m0, int k0,
 template <bool INT4, int G, int NT>
 __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kChunk = chunk_of(NT), kStages = stages_of(NT);
+  constexpr int kChunk = kGemvChunk, kStages = kGemvStages;
   constexpr int kSubs = kChunk / 32;             // 16-byte pieces of a row's chunk of codes
   constexpr int kPer = kChunk / G;               // scales of a row's chunk
   constexpr int kCodes = kGemvRows * kChunk / 2;
   constexpr int kCopies = kGemvRows * kSubs / 32;   // of 16 bytes, per lane and tile
   constexpr int kStep = 32 / kSubs;              // rows of one copy of the warp
+  static_assert(kSubs == 8, "a row's chunk is a line of 128 bytes");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   // Shared memory: stages [warps][stages] of codes and scales of 32 rows, the warps' sums
   // of a batch of tiles [batch][warps][2 halves][NT][16 rows][8], and across the cluster
@@ -203,30 +211,29 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   // One tile's codes and scales into a stage.  A row's pieces change places with the
   // row's number, so that the eight rows that a warp reads at once meet distinct banks.
   const int row0 = lane / kSubs, piece = lane % kSubs;
-  const int turn = kSubs == 8 ? row0 : row0 >> 1 & 3;
   const int64_t pitch = p.K / 2;
   const unsigned char* codes = p.w + (n0 + row0) * pitch + k0 / 2 + 16 * piece;
   const __nv_bfloat16* scales = p.s + (int64_t)(n0 + lane) * p.groups + chunk * kPer;
   const int bytes = k0 + 32 * piece < p.K ? 16 : 0;
-  const uint32_t to = smem_addr(ring) + row0 * kSubs * 16 + (piece ^ turn) * 16;
+  const uint32_t to = smem_addr(ring) + row0 * kSubs * 16 + (piece ^ row0) * 16;
   auto stage = [&](int tile, uint32_t at) {
     if (live && tile < tiles) {
       const int left = rows - kGemvRows * tile;
       const unsigned char* from = codes;
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
-        // with eight pieces a row, rows four apart differ in the turn's third bit
-        const uint32_t dst = (kSubs == 8 && i % 2 ? to ^ 64u : to) + 512 * i;
+        // rows four apart differ in the third bit of what their pieces change by
+        const uint32_t dst = (i % 2 ? to ^ 64u : to) + 512 * i;
         copy_async16(dst + at, from, row0 + i * kStep < left ? bytes : 0);
         from += kStep * pitch;
       }
       codes = from;
       const uint32_t into = smem_addr(ring) + at + kCodes;
-      if (kPer >= 2 && p.vector) {
+      if (p.vector) {
         const int n = lane < left ? 2 * kPer : 0;
         if constexpr (kPer == 8)
           copy_async16(into + lane * p.scale_pitch, scales, n);
-        else if constexpr (kPer >= 2)
+        else
           copy_async_small<2 * kPer>(into + lane * p.scale_pitch, scales, n);
         scales += (int64_t)kGemvRows * p.groups;
       } else {
@@ -249,24 +256,24 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
   };
   grid_dependency_wait();
   allow_dependent_launch();
-  for (int s = 0; s < kStages; ++s) stage(s, s * p.stage_bytes);
-
   uint32_t frag[kSubs][NT][4];
   float factor[kChunk / 128][NT][2];
+  load_rows<NT>(p, m0, k0, frag, factor);
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) stage(s, s * p.stage_bytes);
   if (p.a_scales != nullptr)
-    load_e4m3<INT4, NT>(p, m0, k0, frag, factor);
+    convert_e4m3<INT4, NT>(frag);
   else
-    load_bf16<INT4, NT>(p, m0, k0, frag, factor);
+    convert_bf16<INT4, NT>(frag, factor);
 
   const int summed = min(p.warps, p.chunks - rank * p.warps);   // warps with a chunk
   // Row and piece of the matrix rows whose addresses this lane gives: matrices 0 and 1
   // are rows 0 to 7 and 8 to 15 of an even sub-block, 2 and 3 of the odd one behind it.
-  const int mrow = lane & 15, mturn = kSubs == 8 ? lane & 7 : lane >> 1 & 3;
   const uint32_t matrices =
-      smem_addr(ring) + mrow * kSubs * 16 + ((lane >> 4) ^ mturn) * 16;
+      smem_addr(ring) + (lane & 15) * kSubs * 16 + ((lane >> 4) ^ (lane & 7)) * 16;
   // Halves of a tile and sub-blocks whose products are formed side by side: independent
   // sums for the tensor pipe, as far as registers go.
-  constexpr int kHalves = NT == 1 ? 2 : 1, kSide = NT == 4 ? 1 : 2;
+  constexpr int kHalves = NT == 1 ? 2 : 1;
   uint32_t at = 0;
   int slot = 0;   // of the batch
   for (int tile = 0; tile < tiles; ++tile) {
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
             const int row = 16 * half + g + 8 * h;
             const unsigned char* from = ring + at + kCodes + row * p.scale_pitch;
             float(&v)[kGroups] = sc[h / 2][h % 2];
-            if (kPer >= 2 && p.vector) {
+            if (p.vector) {
               if constexpr (kGroups == 4) {
                 const uint2 w = lds64(from + 8 * b);
                 v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
                     (uint32_t)reinterpret_cast<const uint16_t*>(from)[odd + kGroups * b + i] << 16);
             }
           }
-          float d[kHalves][NT][4], c[kHalves][kSide][NT][4];
+          float d[kHalves][NT][4], c[kHalves][2][NT][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {   // pairs of sub-blocks
             uint32_t w[kHalves][4];
@@ -316,61 +323,47 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
             for (int h = 0; h < kHalves; ++h)
               load_matrices(((matrices + at) ^ (16u * (4 * b + 2 * i))) +
                                 (half + h) * (16 * kSubs * 16), w[h]);
+            uint32_t lo[kHalves][2][4], hi[kHalves][2][4];
 #pragma unroll
-            for (int s0 = 0; s0 < 2; s0 += kSide) {
-              uint32_t lo[kHalves][kSide][4], hi[kHalves][kSide][4];
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-              for (int s = 0; s < kSide; ++s)
+              for (int h = 0; h < kHalves; ++h) {
+                decode8<INT4>(w[h][2 * s], lo[h][s]);
+                decode8<INT4>(w[h][2 * s + 1], hi[h][s]);
+              }
+            const bool opens = G <= 64 || i == 0;   // the pair opens its group or groups
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                  decode8<INT4>(w[h][2 * (s0 + s)], lo[h][s]);
-                  decode8<INT4>(w[h][2 * (s0 + s) + 1], hi[h][s]);
-                }
-              // whether a sum of this pair (or sub-block) opens its group
-              const bool opens = kSide == 2 ? G <= 64 || i == 0 : 32 * (2 * i + s0) % G == 0;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int s = 0; s < kSide; ++s)
+              for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                   for (int j = 0; j < NT; ++j) {
-                    const uint32_t(&f)[4] = frag[4 * b + 2 * i + s0 + s][j];
-                    float(&x)[4] = c[h][s][j];
+                    const uint32_t(&f)[4] = frag[4 * b + 2 * i + s][j];
                     const uint32_t(&l)[4] = lo[h][s], (&u)[4] = hi[h][s];
-                    if (opens)
+                    float(&x)[4] = c[h][s][j];
+                    if (k == 0 && opens)
                       mma_f16(x, l[0], u[0], l[1], u[1], f[0], f[1], 0.f, 0.f, 0.f, 0.f);
                     else
-                      mma_f16(x, l[0], u[0], l[1], u[1], f[0], f[1], x[0], x[1], x[2], x[3]);
+                      mma_f16(x, l[2 * k], u[2 * k], l[2 * k + 1], u[2 * k + 1], f[2 * k],
+                              f[2 * k + 1], x[0], x[1], x[2], x[3]);
                   }
+            // groups that end here, into the block's sums
 #pragma unroll
-              for (int s = 0; s < kSide; ++s)
+            for (int s = G == 32 ? 0 : 1; s < 2; ++s) {
+              if (32 * (2 * i + s + 1) % G != 0) continue;
+              const int grp = 32 * (2 * i + s) / G;
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h)
+              for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-                  for (int j = 0; j < NT; ++j) {
-                    const uint32_t(&f)[4] = frag[4 * b + 2 * i + s0 + s][j];
-                    float(&x)[4] = c[h][s][j];
-                    const uint32_t(&l)[4] = lo[h][s], (&u)[4] = hi[h][s];
-                    mma_f16(x, l[2], u[2], l[3], u[3], f[2], f[3], x[0], x[1], x[2], x[3]);
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float v = G == 32 ? c[h][s][j][e] : c[h][0][j][e] + c[h][1][j][e];
+                    d[h][j][e] = grp == 0 ? v * sc[h][e >> 1][grp]
+                                          : fmaf(v, sc[h][e >> 1][grp], d[h][j][e]);
                   }
-              // groups that end here, into the block's sums
-#pragma unroll
-              for (int s = 0; s < kSide; ++s) {
-                const int sub = 2 * i + s0 + s;
-                if (32 * (sub + 1) % G != 0) continue;
-                const int grp = 32 * sub / G;
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                  for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      const float v = G > 32 && kSide == 2 ? c[h][0][j][e] + c[h][1][j][e]
-                                                           : c[h][s][j][e];
-                      d[h][j][e] = grp == 0 ? v * sc[h][e >> 1][grp]
-                                            : fmaf(v, sc[h][e >> 1][grp], d[h][j][e]);
-                    }
-              }
             }
           }
 #pragma unroll
@@ -459,11 +452,7 @@ __global__ void __launch_bounds__(32 * kMaxGemvWarps, 1) gemv_kernel(const GemvP
 
 template <bool INT4, int G>
 GemvKernel pick_tiles(int nt) {
-  switch (nt) {
-    case 1: return gemv_kernel<INT4, G, 1>;
-    case 2: return gemv_kernel<INT4, G, 2>;
-    default: return gemv_kernel<INT4, G, 4>;
-  }
+  return nt == 1 ? gemv_kernel<INT4, G, 1> : gemv_kernel<INT4, G, 2>;
 }
 
 }  // namespace

@@ -55,18 +55,16 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.groups = (p.K + rq.group - 1) / rq.group;
   p.kb = (p.K + 127) / 128;
   p.fp32 = rq.fp32_out;
-  // slices of A's rows, in even parts; a chunk is half as long from 17 rows on, and a
-  // cluster holds 128 chunks
-  const int slices_m = (p.M + 31) / 32 * (p.M > 16 && p.K > 16384 ? 2 : 1);
-  p.per = ((p.M + slices_m - 1) / slices_m + 7) / 8 * 8;
-  const int nt = p.per <= 8 ? 1 : p.per <= 16 ? 2 : 4;
+  // slices of A's rows, in even parts
+  const int slices_m = (p.M + 15) / 16;
+  const int nt = p.M <= 8 ? 1 : 2;
   p.per = 8 * nt;
-  const int chunk = chunk_of(nt), stages = stages_of(nt);
+  const int chunk = kGemvChunk, stages = kGemvStages;
   p.chunks = (p.K + chunk - 1) / chunk;
   p.cluster = (p.chunks + kMaxGemvWarps - 1) / kMaxGemvWarps;
   p.warps = (p.chunks + p.cluster - 1) / p.cluster;
   const int per_row = chunk / rq.group;
-  p.vector = per_row >= 2 && p.groups % per_row == 0;
+  p.vector = p.groups % per_row == 0;
   p.scale_pitch = p.vector ? 2 * per_row : (2 * per_row + 2 + 3) / 4 * 4;
   p.w = static_cast<const uint8_t*>(rq.W);
   p.stage_bytes = (kGemvRows * (chunk / 2 + p.scale_pitch) + 127) / 128 * 128;
@@ -104,7 +102,9 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
     cfg.dynamicSmemBytes = base;
   }
   if (rc != NTS_OK) return rc;
-  p.slices = (int)std::min<int64_t>(std::max<int64_t>(1, fit / slices_m), p.N);
+  // More CTAs than SMs only where each still has a whole tile.
+  fit = std::min<int64_t>(fit / slices_m, std::max(dev.sm_count, p.N / kGemvRows));
+  p.slices = (int)std::min<int64_t>(std::max<int64_t>(1, fit), p.N);
   if (p.cluster > 1) {
     // the sums of a slice across the cluster: with shorter batches, or more slices
     const size_t row = 8 * nt * sizeof(float);
