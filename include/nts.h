@@ -2,8 +2,10 @@
  * nts.h -- C ABI of libnts, GB300 (sm_103a) kernels for per-token RMS
  * normalization: split-H layerwise QK-RMSNorm, fused RMSNorm + MX cast, and
  * MXNorm + MX cast; and for the QKV projection between them: block-128 E4M3
- * casts, the block-scaled 8-bit matrix product, and headwise QK-RMSNorm with
- * the rotary position embedding, forward and backward.
+ * casts, the block-scaled 8-bit matrix product, products of few rows with
+ * 4-bit weights, the residual's addition with RMSNorm and the cast, and headwise
+ * QK-RMSNorm with the rotary position embedding of one or several axes, the
+ * last two forward and backward.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -613,9 +615,9 @@ NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scal
  *
  *     Y[m][n] = sum_g w_scales[n][g] sum_{k in group g} A[m][k] W[n][k]
  *
- * Sums in fp32, one rounding to the output type.  Up to 32 rows are one pass
- * over the weights (16 with a K above 16384); more rows are passes of up to as
- * many, and from about 64 on nts_gemm_blockscaled is the faster product.
+ * Sums in fp32, one rounding to the output type.  Up to 8 rows cost what one
+ * does; 16 are one pass over the weights, more are passes of 16.  Beyond 16 rows
+ * weights of 8 bits and nts_gemm_blockscaled take less time, at twice the memory.
  *   A_dev         with a_scales NULL: bf16, row m at m*lda elements, a value that
  *                 is below 2^-31 of the largest of its 128 neighbours along K
  *                 off by up to 2^-39 of that one; otherwise E4M3 codes (uint8)

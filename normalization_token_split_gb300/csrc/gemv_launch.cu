@@ -7,23 +7,36 @@
 // values (the operand of nts_gemm_blockscaled).
 //
 // GB300 mapping: with few rows the weights' bytes are the whole cost (0.5 a weight, and
-// 2 per group), so they go through once, at HBM's rate, and everything else has to fit
-// beside them: about six issue slots for the two weights of a lane.  The products run on
-// mma.sync (m16n8k16, fp16 in, fp32 sums), 16 weight rows against 8 rows of A at a time:
-// a fifth of the tensor instructions' rate is enough, and their operands come from
-// registers, where the codes are turned into fp16 (exactly).  A's rows are the narrow
-// operand, so 1 to 8 of them cost the same.
-// A warp owns a chunk of K: its part of A stays in registers as B fragments for the
-// whole call, and it streams its chunk of one tile of 16 weight rows after the other
-// through its own ring of shared memory (cp.async, no barrier and no other warp's copies
-// to wait for).  The codes of a group lie in the four lanes of a quad, four bytes each,
-// so a group's products end in one fragment, which the group's scale multiplies in fp32.
-// A tile's sums over the warps' chunks meet in shared memory, in a fixed order; a longer
-// K is split over the CTAs of a cluster, whose sums meet once at the end.
+// 2 per group), so they go through once and everything else has to fit beside them: about
+// six issue slots for two weights of a lane at HBM's rate.  The products run on mma.sync
+// (m16n8k16, fp16 in, fp32 sums), 16 weight rows against 8 rows of A at a time, whose
+// operands are registers, where the codes are turned into fp16 (exactly); A's rows are
+// the narrow operand, so 1 to 8 of them cost the same.  tcgen05 reads the weights from
+// shared memory: as fp16 they would pass through it five bytes a weight, above its rate
+// at HBM's.  mma.sync on E4M3 operands is taken apart into fp16 products (25 issue cycles
+// for a k of 32, 16 by fp16 ones; int8 65), so E4M3 rows become fp16 too.
+// A warp owns a chunk of 256 values of K: its part of A stays in registers as B
+// fragments for the whole call, and it streams its chunk of one tile of 32 weight rows
+// after the other through its own ring of shared memory (cp.async: no barrier and no other
+// warp's copies to wait for).  The codes of a group lie in the four lanes of a quad, four
+// bytes each (a matrix load's layout), so a group's products end in one fragment, which
+// the group's scale multiplies in fp32.  The warps' sums of a few tiles at a time meet in
+// shared memory, in a fixed order; a K beyond 16 chunks is split over the CTAs of a
+// cluster, whose sums meet once at the end.
 // A's values become fp16 without loss where it matters: E4M3 codes exactly; bf16 rows by
 // a power of two per 128 values that puts the largest near 2^14, so a value is exact
 // unless it is below 2^-31 of the largest beside it, and then off by at most 2^-39 of it,
 // under the fp32 sums' own roundings.
+//
+// Measured (us, back to back in a graph over more than L2; of the copy's rate): [1, 4096]
+// x [12288, 4096] E2M1, groups of 32, 9.3 (0.45); groups of 128 8.2; [1, 4096] x [4096,
+// 4096] 5.0; [8, 16384] E4M3 x [5120, 16384] int4, groups of 128, 16.9; [8, 16384] x
+// [16384, 16384] 32.4 (0.69); [32, 5120] x [15360, 5120] 33.5.  Of the 13000 cycles after
+// the start of the first of these, 4000 pass before A and the first tile are there, 2100
+// are a tile's 16 steps of 32 values (33 issue slots a step: eight conversions, two
+// products, four scalings and the loads) and 1300 the last sums.  Boxes of 8 or 16 rows
+// by TMA in place of cp.async took 10.8 and 9.4 us; tiles of 16 rows with a barrier each
+// 11.2; the codes by 4-byte loads 11.6; 20 warps of 96 registers the same as 16 of 128.
 #include <cuda_runtime.h>
 
 #include <algorithm>

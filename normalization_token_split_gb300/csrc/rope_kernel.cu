@@ -21,6 +21,9 @@
 // a time, with one read of the table row and the gain for all of them: that read
 // and the position's latency are what a round of heads costs beside its data.
 //
+// Tokens with a position on each of several axes take each pair's angle from the row
+// of the position on its axis (RopeRows); everything else is the same.
+//
 // Measured (us, back to back in a graph; of the copy's rate): forward [8192, 40
 // + 40 heads of 128] 53.4, 0.94; [1237, 20 + 4 heads of 96, 64 turned] 5.8; one
 // token of 32 + 32 heads 1.9 (an empty launch 1.0 to 1.5).  Backward [8192, 40 +
