@@ -233,8 +233,8 @@ __device__ __forceinline__ float row_sum(float v, const Place<C>& at, const AddN
 
 template <int C>
 __device__ __forceinline__ void start_cluster() {
-  if (C > 1) {   // every CTA runs before another writes into its shared memory
-    cluster_arrive_relaxed();
+  if (C > 1) {   // every CTA runs, its parts cleared, before another writes into them
+    cluster_arrive_release();
     cluster_wait_acquire();
   }
 }
