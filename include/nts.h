@@ -616,8 +616,11 @@ NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scal
  *     Y[m][n] = sum_g w_scales[n][g] sum_{k in group g} A[m][k] W[n][k]
  *
  * Sums in fp32, one rounding to the output type.  Up to 8 rows cost what one
- * does; 16 are one pass over the weights, more are passes of 16.  Beyond 16 rows
- * weights of 8 bits and nts_gemm_blockscaled take less time, at twice the memory.
+ * does; 16 are one pass over the weights, more are passes of 16, or of 32 with
+ * more than 4096 x 4096 weights (there a group's products are summed before its
+ * scale multiplies them, so bf16 values from about 2^117 on may leave the range).
+ * Beyond 16 rows weights of 8 bits and nts_gemm_blockscaled take less time, at
+ * twice the memory.
  *   A_dev         with a_scales NULL: bf16, row m at m*lda elements, a value that
  *                 is below 2^-31 of the largest of its 128 neighbours along K
  *                 off by up to 2^-39 of that one; otherwise E4M3 codes (uint8)

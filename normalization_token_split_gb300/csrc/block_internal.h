@@ -4,6 +4,8 @@
 // content the measured traffic of the split-H kernels is tied to.
 #pragma once
 
+#include <cuda.h>   // CUtensorMap
+
 #include "nts_internal.h"
 
 namespace nts {
@@ -13,6 +15,11 @@ constexpr unsigned kStatusPosition = 2u;
 
 // Whether this call is to meet a C++ exception (nts_debug_inject_failure).
 bool take_injected_throw();
+// Map of a matrix [rows, K] of bf16 or one-byte values, `pitch` values from row to row,
+// copied in boxes of box_rows x 128 bytes with the 128-byte swizzle; rows and columns
+// outside read as zeros (gemm_kernel.cu).
+int make_row_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64_t K,
+                 int64_t pitch, int box_rows);
 // CTAs of this kernel that fit an SM (cached per device).
 int blocks_per_sm(const void* kernel, int threads, size_t smem, int* out);
 
@@ -113,10 +120,11 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
 // The operators around a projection whose kernels this process has launched or
 // captured: nts_check_status reads the status words of those alone (a blocking
 // copy of ~13 us each), so the other operators' users do not pay for them.
-enum StatusUnit { kCastUnit, kGemmUnit, kRopeUnit, kStatusUnits };
+enum StatusUnit { kCastUnit, kGemmUnit, kRopeUnit, kGemvUnit, kStatusUnits };
 void note_launch(StatusUnit unit);
 int read_and_clear_cast_status(unsigned* out);
 int read_and_clear_gemm_status(unsigned* out);
 int read_and_clear_rope_status(unsigned* out);
+int read_and_clear_gemv_status(unsigned* out);
 
 }  // namespace nts

@@ -830,22 +830,26 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Map of an E4M3 matrix [rows, K], copied in boxes of box_rows x 128 bytes
-// with the 128-byte swizzle; rows and columns outside read as zeros.
-int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+}  // namespace
+
+int make_row_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64_t K,
+                 int64_t pitch, int box_rows) {
   const EncodeTiled enc = encode_tiled();
   if (enc == nullptr) return fail(NTS_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)K};
-  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 2 * pitch : pitch)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)box_rows};
   const cuuint32_t step[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
-                         strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r =
+      enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+          const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NTS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return NTS_OK;
 }
+
+namespace {
 
 cudaLaunchAttribute cluster_attribute(int cluster) {
   cudaLaunchAttribute a;
@@ -860,8 +864,8 @@ int launch(GemmKernel kern, const GemmRequest& rq, const GemmParams& p, int box_
            dim3 grid, int threads, int regs, size_t smem, int cluster, cudaStream_t stream,
            bool pdl) {
   CUtensorMap map_a, map_w;
-  int rc = make_map(&map_a, rq.A, rq.M, rq.K, box_a);
-  if (rc == NTS_OK) rc = make_map(&map_w, rq.W, rq.N, rq.K, box_w);
+  int rc = make_row_map(&map_a, rq.A, false, rq.M, rq.K, rq.K, box_a);
+  if (rc == NTS_OK) rc = make_row_map(&map_w, rq.W, false, rq.N, rq.K, rq.K, box_w);
   if (rc == NTS_OK) rc = prepare_kernel((const void*)kern, smem);
   if (rc != NTS_OK) return rc;
   if (regs > 0) {   // the split of the registers presumes what the CTA is launched with

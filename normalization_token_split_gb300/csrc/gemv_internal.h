@@ -2,6 +2,7 @@
 // share.
 #pragma once
 
+#include <cuda.h>   // CUtensorMap
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -31,11 +32,13 @@ struct GemvParams {
   int cluster;               // CTAs along K
   int slices;                // row slices (clusters along N)
   int per;                   // rows of A per slice of M (blockIdx.y)
-  int vector;                // a chunk's scales of a row are one aligned copy
+  int vector;                // a chunk's (tiles: a K block's) scales of a row are one aligned piece
   int scale_pitch;           // bytes of a row's scales in a stage
   int stage_bytes;           // a multiple of 128
   int fp32;
   int batch;                 // tiles whose sums the warps keep between two barriers
+  uint64_t wait_limit_ns;    // tile kernel
+  uint32_t missing_tx;       // test hook: bytes expected on the first stage but never sent
 };
 
 using GemvKernel = void (*)(GemvParams);
@@ -45,5 +48,19 @@ template <bool INT4>
 GemvKernel pick_gemv(int group, int nt);
 extern template GemvKernel pick_gemv<false>(int, int);
 extern template GemvKernel pick_gemv<true>(int, int);
+// The tile kernel for a group size and a type of A, whose rows it copies by a tensor map,
+// and its shared memory.
+using GemvTileKernel = void (*)(CUtensorMap, GemvParams);
+constexpr int kTileThreads = 608;
+constexpr int kTileRows = 32;      // rows of A of a tile
+template <bool INT4>
+GemvTileKernel pick_gemv_tile(int group, bool e4m3, size_t* smem);
+extern template GemvTileKernel pick_gemv_tile<false>(int, bool, size_t*);
+extern template GemvTileKernel pick_gemv_tile<true>(int, bool, size_t*);
+// Each unit's status word.
+template <bool INT4>
+int read_and_clear_gemv_unit(unsigned* out);
+extern template int read_and_clear_gemv_unit<false>(unsigned*);
+extern template int read_and_clear_gemv_unit<true>(unsigned*);
 
 }  // namespace nts

@@ -680,7 +680,8 @@ int nts_check_status(void* stream) {
   rc = read_and_clear_mx_status(&mx);
   if (rc != NTS_OK) return rc;
   int (*const read[kStatusUnits])(unsigned*) = {
-      read_and_clear_cast_status, read_and_clear_gemm_status, read_and_clear_rope_status};
+      read_and_clear_cast_status, read_and_clear_gemm_status, read_and_clear_rope_status,
+      read_and_clear_gemv_status};
   int units = 0;
   for (int i = 0; i < kStatusUnits; ++i) {
     if (!g_launched[i].load(std::memory_order_relaxed)) continue;
@@ -689,11 +690,13 @@ int nts_check_status(void* stream) {
     if (rc != NTS_OK) return rc;
   }
   log_launch("check_status", "words of %d operators around a projection read", units);
-  const unsigned cast = unit[kCastUnit], gemm = unit[kGemmUnit], rope = unit[kRopeUnit];
-  if ((qk | mx | cast | gemm | (rope & ~kStatusPosition)) != 0)
+  const unsigned cast = unit[kCastUnit], gemm = unit[kGemmUnit], rope = unit[kRopeUnit],
+                 gemv = unit[kGemvUnit];
+  if ((qk | mx | cast | gemm | gemv | (rope & ~kStatusPosition)) != 0)
     return fail(NTS_ERR_TIMEOUT,
-                "a kernel gave up on a bounded wait (qk=%u mx=%u cast=%u gemm=%u rotation=%u)", qk,
-                mx, cast, gemm, rope);
+                "a kernel gave up on a bounded wait (qk=%u mx=%u cast=%u gemm=%u rotation=%u "
+                "4-bit=%u)",
+                qk, mx, cast, gemm, rope, gemv);
   if (rope != 0)
     return fail(NTS_ERR_INVALID_ARG, "a token position lay outside the rotation table");
   return NTS_OK;
