@@ -33,7 +33,7 @@ struct Tile {
   static constexpr uint32_t kBarOff = kFactorOff + 2 * kTeam * 2 * TN * 4;
   static constexpr uint32_t kLaunch = kBarOff + 512 + 1024;
   static_assert(kCols >= 32 && kCols <= 512 && (kCols & (kCols - 1)) == 0, "tensor memory");
-  static_assert(2 * kStages * kStage >= 2 * TN * 128 * 4, "the sums for the other CTAs fit the ring");
+  static_assert(kStages * kStage >= TN * 128 * 4, "the sums for the other CTAs fit the ring");
   static_assert(kLaunch <= 232448 && kLaunch >= 160 * 1024, "one CTA per SM");
 };
 
@@ -135,8 +135,10 @@ __device__ __forceinline__ uint4 ldg_codes(const unsigned char* p) {
   return v;
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
                : "memory");
 }
 
@@ -160,7 +162,7 @@ gemv_tile_kernel(const __grid_constant__ CUtensorMap rows, const GemvParams p) {
   const int split = p.cluster;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
   const int n0 = (int)blockIdx.x / split * 128, m0 = (int)blockIdx.y * TN;
-  const int b0 = (int)((int64_t)p.kb * rank / split), b1 = (int)((int64_t)p.kb * (rank + 1) / split);
+  const int b0 = p.kb * rank / split, b1 = p.kb * (rank + 1) / split;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * S; ++i) {
