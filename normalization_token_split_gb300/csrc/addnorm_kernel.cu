@@ -430,7 +430,9 @@ __global__ void __maxnreg__(backward_regs(C, F32)) add_rmsnorm_backward_kernel(c
     }
     const float uh = row_sum<C>(f2_lo(q) + f2_hi(q), at, p, part, buf);
     buf ^= 1;
-    const float k = -(uh * p.inv_d * rinv) * (rinv * rinv);
+    // dh = rinv (u - h k) + e, k = rinv^2 (1/D) sum u h: rinv^2 of a row of zeros with a
+    // subnormal eps is beyond fp32, rinv u is not.
+    const float k = -((uh * p.inv_d) * rinv) * rinv;
     const uint64_t kk = f2(k, k);
     const int64_t out = off + 16 * at.lane;
     unsigned char* to = static_cast<unsigned char*>(p.h) + kSize * out;
@@ -442,7 +444,7 @@ __global__ void __maxnreg__(backward_regs(C, F32)) add_rmsnorm_backward_kernel(c
       read_half<F32>(st + 1024, half, h);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        h[i] = f2_fma(h[i], kk, f2_mul(f2_mul(g[i], gain[4 * half + i]), rr));
+        h[i] = f2_mul(f2_fma(h[i], kk, f2_mul(g[i], gain[4 * half + i])), rr);
       if (p.e != nullptr) {
         read_half<F32>(st + kBehind, half, g);
 #pragma unroll
