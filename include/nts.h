@@ -521,8 +521,8 @@ NTS_API int nts_add_rmsnorm_blockcast(const void *X_dev, const void *residual_de
  *     dres_j   = rinv u_j - h_j rinv^3 (1/D) sum u h + e_j
  *     dgamma_j = sum over the rows of dy_j h_j rinv              (fp32)
  *
- * dres is the gradient of x and of the residual alike.  The sums have a fixed
- * order: equal calls give equal bits.
+ * dres is the gradient of x and of the residual alike; that of a row with
+ * rinv = 0 is e.  The sums have a fixed order: equal calls give equal bits.
  *   dY_dev         bf16 [T, D].      rinv_dev      fp32 [T], the forward pass's.
  *   H_dev, dH_dev  [T, D] in the stream's type (residual_type); dH (e) or NULL.
  *   gamma_dev      fp32 [D] or NULL.

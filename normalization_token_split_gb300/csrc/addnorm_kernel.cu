@@ -431,8 +431,9 @@ __global__ void __maxnreg__(backward_regs(C, F32)) add_rmsnorm_backward_kernel(c
     const float uh = row_sum<C>(f2_lo(q) + f2_hi(q), at, p, part, buf);
     buf ^= 1;
     // dh = rinv (u - h k) + e, k = rinv^2 (1/D) sum u h: rinv^2 of a row of zeros with a
-    // subnormal eps is beyond fp32, rinv u is not.
-    const float k = -((uh * p.inv_d) * rinv) * rinv;
+    // subnormal eps is beyond fp32, rinv u is not.  Where rinv is 0 the sum may be beyond
+    // it too.
+    const float k = rinv == 0.f ? 0.f : -((uh * p.inv_d) * rinv) * rinv;
     const uint64_t kk = f2(k, k);
     const int64_t out = off + 16 * at.lane;
     unsigned char* to = static_cast<unsigned char*>(p.h) + kSize * out;

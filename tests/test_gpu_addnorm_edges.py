@@ -30,3 +30,27 @@ def test_rows_of_zeros_and_near_them(D, res, eps):
     c["e"] = None
     check_backward(c, o.h, o.rinv, nts.add_rmsnorm_backward(c["dy"], o.h, o.rinv, c["gamma"]))
     nts.check_status()
+
+
+@pytest.mark.parametrize("res", TYPES)
+@pytest.mark.parametrize("D", WIDTHS)
+def test_rows_beyond_fp32(D, res):
+    """Such a row's rinv is 0, so the gradient from behind is all that is left, also where
+    the sum of u h is beyond fp32 (row 0), or its parts are and cancel to nothing (row 1)."""
+    T = 6
+    c = make(T, D, res, seed=D + 1)
+    c["x"][:2] = 0
+    c["r"][0], c["dy"][0] = 3e38, 2
+    c["r"][1] = 3e38 * (1 - 2 * (torch.arange(D, device=DEV) % 2))
+    c["dy"][1] = 2
+    c["gamma"] = c["gamma"].abs()
+    o = nts.add_rmsnorm_blockcast(c["x"], c["r"], c["gamma"], want_rinv=True)
+    assert not o.rinv[:2].any() and o.rinv[2:].all()
+    got = nts.add_rmsnorm_backward(c["dy"], o.h, o.rinv, c["gamma"], dres=c["e"])
+    check_backward(c, o.h, o.rinv, got)
+    assert torch.equal(got[0][:2], c["e"][:2])
+    c["e"] = None
+    got = nts.add_rmsnorm_backward(c["dy"], o.h, o.rinv, c["gamma"])
+    check_backward(c, o.h, o.rinv, got)
+    assert not got[0][:2].any()
+    nts.check_status()
