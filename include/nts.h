@@ -392,8 +392,8 @@ NTS_API int nts_qknorm_rope(const void *Q_dev, int64_t ldq, const float *gamma_q
  *
  * rinv is formed again from Q and K (the forward pass's inputs).  Padding
  * rows, and rows whose position lies outside the table, get zeros and add
- * nothing to dgamma.  The sums have a fixed order: equal calls give equal
- * bits.
+ * nothing to dgamma; so does a head whose sum of squares is beyond fp32, with
+ * rinv = 0.  The sums have a fixed order: equal calls give equal bits.
  *   dYq_dev, dYk_dev, dQ_dev, dK_dev  bf16, laid out as Q and K, each with its
  *                   own row stride; dQ == dYq or dQ == Q with the same stride
  *                   is allowed (dK likewise).

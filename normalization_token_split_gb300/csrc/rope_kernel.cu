@@ -435,7 +435,8 @@ __device__ __forceinline__ void backward_head(const RopeParams& p, const RopeLan
   const float ss = head_sum(f2_lo(q0) + f2_hi(q0), lanes);
   const float ux = head_sum(f2_lo(w0) + f2_hi(w0), lanes);
   const float rinv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-  const float k = -(ux * p.inv_d * rinv) * (rinv * rinv);
+  // where rinv is 0, x being beyond fp32, the sum of u x may be too
+  const float k = rinv == 0.f ? 0.f : -(ux * p.inv_d * rinv) * (rinv * rinv);
   const uint64_t rr = f2(rinv, rinv), kk = f2(k, k);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
