@@ -617,10 +617,13 @@ NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scal
  *
  * Sums in fp32, one rounding to the output type.  Up to 8 rows cost what one
  * does; 16 are one pass over the weights, more are passes of 16, or of 32 with
- * more than 4096 x 4096 weights (there a group's products are summed before its
- * scale multiplies them, so bf16 values from about 2^117 on may leave the range).
- * Beyond 16 rows weights of 8 bits and nts_gemm_blockscaled take less time, at
- * twice the memory.
+ * more than 4096 x 4096 weights.  Beyond 16 rows weights of 8 bits and
+ * nts_gemm_blockscaled take less time, at twice the memory.
+ * What may leave fp32's range on the way though the output would not: in passes
+ * of 16, outputs of group scales above 2^102 (128 values along K are raised to
+ * 2^14 and more by a power of two that comes off behind the scales); in those
+ * of 32, bf16 values from about 2^117 on (a group's products are summed before
+ * its scale multiplies them).
  *   A_dev         with a_scales NULL: bf16, row m at m*lda elements, a value that
  *                 is below 2^-31 of the largest of its 128 neighbours along K
  *                 off by up to 2^-39 of that one; otherwise E4M3 codes (uint8)

@@ -146,7 +146,9 @@ __device__ __forceinline__ void convert_bf16(uint32_t (&frag)[kGemvChunk / 32][N
       float most = bf16x2_hmax_abs(most2);
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      // 2^f: the largest comes to [2^14, 2^15), as far as 2^f and 2^-f are normal
+      // 2^f: the largest comes to [2^14, 2^15), as far as 2^f and 2^-f are normal.  128 of
+      // them by codes of up to 8 come to 2^25 at most, so group scales of 2^102 fit before
+      // 2^-f takes it off again.
       const int f = max(-113, min(126, 141 - (int)(__float_as_uint(most) >> 23)));
       const float up = __uint_as_float((uint32_t)(127 + f) << 23);
       const float down = __uint_as_float((uint32_t)(127 - f) << 23);
