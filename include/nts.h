@@ -617,7 +617,7 @@ NTS_API int nts_gemm_blockscaled(const uint8_t *A_codes_dev, const float *a_scal
  *
  * Sums in fp32, one rounding to the output type.  Up to 8 rows cost what one
  * does; 16 are one pass over the weights, more are passes of 16, or of 32 with
- * more than 4096 x 4096 weights.  Beyond 16 rows weights of 8 bits and
+ * more than 4096 x 4096 weights.  From 9 rows on weights of 8 bits and
  * nts_gemm_blockscaled take less time, at twice the memory.
  * What may leave fp32's range on the way though the output would not: in passes
  * of 16, outputs of group scales above 2^102 (128 values along K are raised to

@@ -23,7 +23,8 @@ extern "C" {
  *              MX kernels: MX blocks per thread (halves of 64-value
  *              blocks for B = 64), 1..8 with at most 16 vectors per thread;
  *              nts_gemm_blockscaled: the kernel, 1 = of few rows, 2 = of single
- *              CTAs, 3 = of CTA pairs (other values: automatic)
+ *              CTAs, 3 = of CTA pairs; nts_gemv_groupscaled: 1 = passes of 16
+ *              rows, 2 = tiles of 32 (other values: automatic)
  *   rows       token rows per tile (rows * threads-per-row <= 480);
  *              nts_qknorm_rope and its gradient: the ring kernel, with at most
  *              this many rounds of heads per stage
@@ -72,7 +73,7 @@ NTS_API int nts_debug_set_host_chunks(int max_chunks, int64_t min_chunk_bytes);
  * failure was injected; the device is not touched.  count = 0 turns the hook
  * off.  Lets callers' error handling be tested without a failing GPU.
  * status NTS_DEBUG_THROW: the next `count` calls of the operators around a
- * projection (nts_qknorm_rope to nts_gemm_blockscaled) meet a C++ exception in
+ * projection (nts_qknorm_rope to nts_gemv_groupscaled) meet a C++ exception in
  * their launch instead, and return NTS_ERR_CUDA.
  * Errors: INVALID_ARG for count < 0 or another status.
  */

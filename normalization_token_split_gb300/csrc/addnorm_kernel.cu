@@ -22,9 +22,10 @@
 // every CTA's shared memory.
 //
 // Measured (us, back to back in a graph over more than L2; of the copy's rate): forward
-// [16384, 4096] bf16 73.4, 0.95; [1237, 5120] fp32 10.6, 0.97; [8, 4096] 1.9.  Gradient
-// [8192, 5120] bf16 53.7, 0.92; [333, 4096] fp32 9.2, of which 3.8 are its two launches
-// at one row.  Rows of 16384: 0.85 and 0.74, a meeting of the cluster each.
+// [16384, 4096] bf16 73.4, 0.95; [1237, 5120] fp32 10.6, 0.97; [8, 4096] 2.1.  Gradient
+// [8192, 5120] bf16 53.7, 0.92; [8192, 4096] fp32 83.8, 0.94; [333, 4096] fp32 9.2, of
+// which 4.1 are its two launches at one row.  Rows of 16384, a meeting of the cluster
+// each: [2000, 16384] bf16 43.6, 0.78, and [2048, 16384] bf16 53.7, 0.74.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -30,9 +30,10 @@
 // under the fp32 sums' own roundings.
 //
 // Measured (us, back to back in a graph over more than L2; of the copy's rate): [1, 4096]
-// x [12288, 4096] E2M1, groups of 32, 9.3 (0.45); groups of 128 8.2; [1, 4096] x [4096,
-// 4096] 5.0; [8, 16384] E4M3 x [5120, 16384] int4, groups of 128, 16.9; [8, 16384] x
-// [16384, 16384] 32.4 (0.69).  Of the 13000 cycles after
+// x [12288, 4096] E2M1, groups of 32, 9.3 (0.45); groups of 128 8.1; int4, groups of 32,
+// 11.5 (0.36); [1, 4096] x [4096, 4096] 5.0; [1, 16384] x [4096, 16384] 11.6 (0.48); [8,
+// 16384] E4M3 x [5120, 16384] int4, groups of 128, 16.9; [8, 16384] x [16384, 16384] 32.3
+// (0.69); [16, 5120] x [15360, 5120], groups of 64, 20.1 (0.31).  Of the 13000 cycles after
 // the start of the first of these, 4000 pass before A and the first tile are there, 2100
 // are a tile's 16 steps of 32 values (33 issue slots a step: eight conversions, two
 // products, four scalings and the loads) and 1300 the last sums.  Boxes of 8 or 16 rows
@@ -46,13 +47,15 @@
 // blocks' products (a group's into columns of tensor memory of its own), and two more
 // teams read the groups' sums back and multiply them by the scales in fp32.  A last warp
 // starts A's copies and asks L2 for the codes some blocks ahead.
-// [32, 5120] x [15360, 5120], E2M1 with groups of 64: 24.2 us (33.5 in passes of 16 rows);
-// int4, groups of 128: 23.0 (38.3).  A K block takes ~1000 cycles of an SM, ~600 of them the
-// codes' (17 integer instructions for eight of them, two cycles each a warp) and, beside
-// that, ~640 the shared memory's for the stores, copies and products.  With fp16 operands,
-// which E2M1 codes become in a third of the instructions, but A's rows only by 8 more
-// warps, 27.7; with a third team for the codes 26.5; with the sums of every block read by
-// all eight warps 24.6, and with groups of 32 a third more.
+// [32, 5120] x [15360, 5120], E2M1 with groups of 64: 24.5 us (33.5 in passes of 16 rows);
+// groups of 32 27.4, by E4M3 rows 27.1 (33.4 and 33.7); int4, groups of 128: 23.1 (38.1).
+// Weights of 8 bits (nts_gemm_blockscaled) take 15.5, and less than 4 bits from 9 rows on:
+// [8, 16384] E4M3 x [16384, 16384] 43.0 and 32.6, 9 rows 43.0 and 48.3.  A K block takes ~1000 cycles of an
+// SM, ~600 of them the codes' (17 integer instructions for eight of them, two cycles each a
+// warp) and, beside that, ~640 the shared memory's for the stores, copies and products.
+// Other forms, when this one took 24.2: fp16 operands, which E2M1 codes become in a third
+// of the instructions, but A's rows only by 8 more warps, 27.7; a third team for the codes
+// 26.5; the sums of every block read by all eight warps 24.6.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -157,10 +160,18 @@ int launch_gemv(const GemvRequest& rq, cudaStream_t stream, const LaunchTuning& 
   p.w = static_cast<const uint8_t*>(rq.W);
   p.wait_limit_ns = tune.wait_limit_ns;
   p.missing_tx = tune.missing_tx;
-  // Tiles instead of a second pass where the weights are many (us, tiles / passes): [32,
-  // 5120] x [15360, 5120] 24.2 / 33.5, [32, 16384] x [16384, 16384] 80 / 156, [32, 4096] x
-  // [4096, 4096] 10.3 / 10.3, [17, 5120] x [2048, 5120] 15.1 / 8.4; one pass, [16, 5120] x
-  // [15360, 5120], 23.8 / 20.4.
+  // Tiles instead of a second pass where the weights are many.  us, tiles / passes, E2M1
+  // with groups of 32 and bf16 rows, A's rows x [N, K]:
+  //   [4096, 4096]    16: 9.9 /  7.7   32: 10.3 / 10.3   64: 15.1 / 14.1
+  //   [5120, 5120]    16: 13.7 / 10.9  32: 14.1 / 14.8   64: 27.0 / 23.8
+  //   [15360, 5120]   16: 27.1 / 20.3  32: 27.5 / 33.4   64: 53.4 / 62.0
+  //   [16384, 16384]                   32: 80.3 / 156
+  //   [2048, 5120]                     32: 10.3 /  8.5  128: 17.2 / 21.0
+  // The rule does not know how many rounds of tiles fill the SMs, and is behind where the
+  // last round is nearly empty or the tiles are few: 48 x [12288, 4096] 43.6 / 25.6 and
+  // 32: 23.4 / 20.1 (int4 with groups of 128 19.4 / 21.5), 32 x [1024, 32768] 24.4 / 19.5,
+  // 48 x [15360, 5120] 53.0 / 48.3; nor how many passes a long A takes: 512 x [2048, 8192]
+  // 84 / 141, where it takes passes.
   enum { kAuto, kPasses, kTiles };
   const int kind = tune.force_vpt <= kTiles ? tune.force_vpt : kAuto;   // debug: one of these
   if (kind == kTiles || (kind == kAuto && p.M > 16 && (int64_t)p.N * p.K > 4096 * 4096))

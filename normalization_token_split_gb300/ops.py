@@ -526,7 +526,7 @@ def gemv_groupscaled(a: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Ten
     is bf16 (contiguous rows, any row stride), or E4M3 codes (uint8 or
     float8_e4m3fn) with a_scales fp32 [M, ceil(K/128)] (a BlockOut's).  Returns
     Y [M, N], bf16 or fp32 (out_dtype, or out's).  Scales of w are at most 2^102
-    in magnitude; beyond 16 rows gemm_blockscaled's weights of 8 bits take less
+    in magnitude; from 9 rows on gemm_blockscaled's weights of 8 bits take less
     time."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError(f"the output must be bfloat16 or float32, got {out_dtype}")
