@@ -50,9 +50,10 @@
 // [32, 5120] x [15360, 5120], E2M1 with groups of 64: 24.5 us (33.5 in passes of 16 rows);
 // groups of 32 27.4, by E4M3 rows 27.1 (33.4 and 33.7); int4, groups of 128: 23.1 (38.1).
 // Weights of 8 bits (nts_gemm_blockscaled) take 15.5, and less than 4 bits from 9 rows on:
-// [8, 16384] E4M3 x [16384, 16384] 43.0 and 32.6, 9 rows 43.0 and 48.3.  A K block takes ~1000 cycles of an
-// SM, ~600 of them the codes' (17 integer instructions for eight of them, two cycles each a
-// warp) and, beside that, ~640 the shared memory's for the stores, copies and products.
+// [8, 16384] E4M3 x [16384, 16384] 43.0 and 32.6, 9 rows 43.0 and 48.3.
+// A K block takes ~1000 cycles of an SM, ~600 of them the codes' (17 integer instructions
+// for eight of them, two cycles each a warp) and, beside that, ~640 the shared memory's for
+// the stores, copies and products.
 // Other forms, when this one took 24.2: fp16 operands, which E2M1 codes become in a third
 // of the instructions, but A's rows only by 8 more warps, 27.7; a third team for the codes
 // 26.5; the sums of every block read by all eight warps 24.6.
